@@ -20,6 +20,7 @@ AXIS_COLS, AXIS_ROWS = 0, 1
 HAD_NONE, HAD_DET, HAD_SIGNED = 0, 1, 2
 RTN, SR = 0, 1
 OUT_F32, OUT_BF16 = 0, 1
+FMT_MXFP4, FMT_MXFP8 = 0, 1
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp4.so")
@@ -65,6 +66,12 @@ def lib() -> ctypes.CDLL:
     L.nvfp4_quantize_noalloc.restype = i32
     L.nvfp4_workspace_bytes.argtypes = [i64, i64]
     L.nvfp4_workspace_bytes.restype = ctypes.c_size_t
+    L.fp4_rmsnorm_quantize.argtypes = [vp, vp, vp, ctypes.c_double, i64, i64, i32, vp, vp, vp, vp, vp, vp]
+    L.fp4_rmsnorm_quantize.restype = i32
+    L.fp4_rmsnorm_backward.argtypes = [vp, vp, vp, vp, vp, i64, i64, vp, vp, vp, ctypes.c_size_t, vp]
+    L.fp4_rmsnorm_backward.restype = i32
+    L.fp4_rmsnorm_workspace_bytes.argtypes = [i64, i64]
+    L.fp4_rmsnorm_workspace_bytes.restype = ctypes.c_size_t
     L.fp4_status_string.argtypes = [i32]
     L.fp4_status_string.restype = ctypes.c_char_p
     _lib = L
@@ -97,6 +104,28 @@ def _need(t: torch.Tensor, dtype, name: str) -> None:
         raise ValueError("%s must be a GPU tensor" % name)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
+
+
+def _need_on(t: torch.Tensor, dtype, shape, device, name: str) -> None:
+    """A contiguous `dtype` tensor of `shape` on `device` (a GPU)."""
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_cuda or t.device != device:
+        raise ValueError("%s must be a GPU tensor on %s, got one on %s" % (name, device, t.device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _call(fn, device, stream, *args) -> None:
+    """fn(*args, stream) with `device` current, so that the launch goes to the
+    device that holds the tensors."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream_ptr(stream, device)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream_ptr(stream, device)))
 
 
 def code_shape(R: int, C: int):
@@ -341,6 +370,83 @@ def nvfp4_quantize_noalloc(x: torch.Tensor, codes: torch.Tensor, scales: torch.T
                                         scales.data_ptr(), tensor_scale.data_ptr(),
                                         _stream_ptr(stream, x.device)))
     return codes, scales, tensor_scale
+
+
+def mx8_shapes(R: int, C: int):
+    """(codes shape, scales shape) of an MXFP8 operand of R rows of C
+    contraction elements: row-major E4M3 bytes and E8M0 scale bytes."""
+    return (R, C), (R, C // 32)
+
+
+def fp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                         eps: float = 1e-5, fmt: int = FMT_MXFP8, out=None, y: torch.Tensor | None = None,
+                         stream=None):
+    """h = x + residual and its root-mean-square norm times `weight`, quantized
+    along cols: (codes, scales, h, rstd) of bf16 x[rows, cols] (see
+    include/fp4.h).  fmt FMT_MXFP8: codes uint8 [rows, cols] (E4M3), scales
+    uint8 [rows, cols/32]; FMT_MXFP4: codes and scales in the shapes of
+    mx_shapes(rows, cols, AXIS_COLS).  h is x itself without a residual, rstd
+    fp32 [rows].  `out`: optional preallocated (codes, scales, h, rstd); h may
+    be x or residual.  `y`: optional bf16 [rows, cols] that receives the norm
+    before its quantization, rounded to bf16."""
+    rows, cols = x.shape
+    dev = x.device
+    bf = torch.bfloat16
+    _need_on(x, bf, (rows, cols), dev, "x")
+    _need_on(weight, bf, (cols,), dev, "weight")
+    if residual is not None:
+        _need_on(residual, bf, (rows, cols), dev, "residual")
+    cshape, sshape = mx8_shapes(rows, cols) if fmt == FMT_MXFP8 else (code_shape(rows, cols), scale_shape(rows, cols))
+    if out is None:
+        codes = torch.empty(cshape, dtype=torch.uint8, device=dev)
+        scales = torch.empty(sshape, dtype=torch.uint8, device=dev)
+        h = x if residual is None else torch.empty_like(x)
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    else:
+        codes, scales, h, rstd = out
+        _need_on(codes, torch.uint8, cshape, dev, "codes")
+        _need_on(scales, torch.uint8, sshape, dev, "scales")
+        _need_on(h, bf, (rows, cols), dev, "h")
+        _need_on(rstd, torch.float32, (rows,), dev, "rstd")
+    if y is not None:
+        _need_on(y, bf, (rows, cols), dev, "y")
+    _call(lib().fp4_rmsnorm_quantize, dev, stream, x.data_ptr(), _ptr(residual), weight.data_ptr(), eps, rows, cols,
+          fmt, None if residual is None and h is x else h.data_ptr(), rstd.data_ptr(), _ptr(y), codes.data_ptr(), scales.data_ptr())
+    return codes, scales, h, rstd
+
+
+def fp4_rmsnorm_workspace_bytes(rows: int, cols: int) -> int:
+    return int(lib().fp4_rmsnorm_workspace_bytes(rows, cols))
+
+
+def fp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                         dh: torch.Tensor | None = None, out=None, workspace: torch.Tensor | None = None,
+                         stream=None):
+    """(dx bf16 [rows, cols], dw fp32 [cols]) of the norm from dy and the h and
+    rstd of the forward pass; `dh`: the gradient that reaches h past the norm
+    (see include/fp4.h).  `out`: optional preallocated (dx, dw); dx may be dh."""
+    rows, cols = dy.shape
+    dev = dy.device
+    bf = torch.bfloat16
+    _need_on(dy, bf, (rows, cols), dev, "dy")
+    _need_on(h, bf, (rows, cols), dev, "h")
+    _need_on(weight, bf, (cols,), dev, "weight")
+    _need_on(rstd, torch.float32, (rows,), dev, "rstd")
+    if dh is not None:
+        _need_on(dh, bf, (rows, cols), dev, "dh")
+    if out is None:
+        dx, dw = torch.empty_like(dy), torch.empty(cols, dtype=torch.float32, device=dev)
+    else:
+        dx, dw = out
+        _need_on(dx, bf, (rows, cols), dev, "dx")
+        _need_on(dw, torch.float32, (cols,), dev, "dw")
+    if workspace is None:
+        workspace = torch.empty(fp4_rmsnorm_workspace_bytes(rows, cols), dtype=torch.uint8, device=dev)
+    else:
+        _need_on(workspace, torch.uint8, workspace.shape, dev, "workspace")
+    _call(lib().fp4_rmsnorm_backward, dev, stream, dy.data_ptr(), h.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
+          _ptr(dh), rows, cols, dx.data_ptr(), dw.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return dx, dw
 
 
 from . import linear  # noqa: E402  (the autograd layer built on the calls above)

@@ -194,6 +194,48 @@ fp4_status nvfp4_quantize_noalloc(const void* x_bf16, int64_t rows, int64_t cols
                                          (hipStream_t)stream));
 }
 
+namespace {
+// rows and cols of a norm: whole 32-element blocks, a row held in registers
+fp4_status check_norm_shape(int64_t rows, int64_t cols) {
+    if (rows <= 0 || cols <= 0 || cols % 32 || cols > 32768 || rows > INT32_MAX) return FP4_ERR_SHAPE;
+    return FP4_OK;
+}
+}  // namespace
+
+fp4_status fp4_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16, const void* weight_bf16,
+                                double eps, int64_t rows, int64_t cols, fp4_format fmt, void* h_bf16,
+                                float* rstd, void* y_bf16, uint8_t* codes, uint8_t* scales, void* stream) {
+    if (fmt != FP4_FMT_MXFP4 && fmt != FP4_FMT_MXFP8) return FP4_ERR_ENUM;
+    if (!(eps >= 0.0)) return FP4_ERR_ENUM;
+    if (!x_bf16 || !weight_bf16 || !codes || !scales || (residual_bf16 && !h_bf16)) return FP4_ERR_NULL;
+    if (const fp4_status s = check_norm_shape(rows, cols)) return s;
+    if (!aligned16(x_bf16) || !aligned16(residual_bf16) || !aligned16(weight_bf16) || !aligned16(h_bf16) ||
+        !aligned4(rstd) || !aligned16(y_bf16) || !aligned16(codes) || !aligned16(scales))
+        return FP4_ERR_ALIGN;
+    return from_hip(fp4dev::launch_rmsnorm_quant(x_bf16, residual_bf16, weight_bf16, eps, rows, cols,
+                                                 fmt == FP4_FMT_MXFP8, h_bf16, rstd, y_bf16, codes, scales,
+                                                 (hipStream_t)stream));
+}
+
+size_t fp4_rmsnorm_workspace_bytes(int64_t rows, int64_t cols) {
+    if (check_norm_shape(rows, cols) != FP4_OK) return 0;
+    return (size_t)(fp4dev::rmsnorm_back_parts(rows) * cols) * sizeof(float);
+}
+
+fp4_status fp4_rmsnorm_backward(const void* dy_bf16, const void* h_bf16, const void* weight_bf16,
+                                const float* rstd, const void* dh_bf16, int64_t rows, int64_t cols,
+                                void* dx_bf16, float* dw, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+    if (!dy_bf16 || !h_bf16 || !weight_bf16 || !rstd || !dx_bf16 || !dw) return FP4_ERR_NULL;
+    if (const fp4_status s = check_norm_shape(rows, cols)) return s;
+    if (!workspace || workspace_bytes < fp4_rmsnorm_workspace_bytes(rows, cols)) return FP4_ERR_WORKSPACE;
+    if (!aligned16(dy_bf16) || !aligned16(h_bf16) || !aligned16(weight_bf16) || !aligned4(rstd) ||
+        !aligned16(dh_bf16) || !aligned16(dx_bf16) || !aligned16(dw) || !aligned16(workspace))
+        return FP4_ERR_ALIGN;
+    return from_hip(fp4dev::launch_rmsnorm_back(dy_bf16, h_bf16, weight_bf16, rstd, dh_bf16, rows, cols, dx_bf16,
+                                                dw, (float*)workspace, (hipStream_t)stream));
+}
+
 const char* fp4_status_string(fp4_status status) {
     switch (status) {
         case FP4_OK: return "FP4_OK";

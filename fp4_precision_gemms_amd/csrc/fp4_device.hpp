@@ -15,6 +15,14 @@ namespace fp4dev {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// Round-to-nearest-even binary32 -> bfloat16 (NaN -> the quiet NaN 0x7FC0).
+__device__ __forceinline__ uint32_t bf16_rne(float f) {
+    const uint32_t u = __float_as_uint(f);
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0x7FC0u;
+    return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+}
+__device__ __forceinline__ float bf16_value(uint32_t b) { return __uint_as_float(b << 16); }
+
 // ---------------------------------------------------------------------------
 // Philox4x32-10 (Salmon et al., SC'11): 10 rounds, multipliers 0xD2511F53 /
 // 0xCD9E8D57, Weyl key increments 0x9E3779B9 / 0xBB67AE85.
@@ -93,6 +101,12 @@ __device__ __forceinline__ uint32_t e2m1_sr(float v, uint32_t u) {
 __device__ __forceinline__ uint32_t e8m0_from_amax_bits(uint32_t mbits) {
     const uint32_t E = mbits >> 23;
     return E == 255u ? 255u : (E < 2u ? 0u : E - 2u);
+}
+
+// The same for E4M3 elements (largest exponent 8): floor(log2 m) - 8 + 127.
+__device__ __forceinline__ uint32_t e8m0_from_amax_bits_e4m3(uint32_t mbits) {
+    const uint32_t E = mbits >> 23;
+    return E == 255u ? 255u : (E < 8u ? 0u : E - 8u);
 }
 
 // 2^-(byte-127) as binary32, valid for byte in [0, 252].

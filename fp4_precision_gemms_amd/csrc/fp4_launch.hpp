@@ -62,6 +62,17 @@ hipError_t launch_nvfp4(const void* x, int64_t rows, int64_t cols, int had, uint
 // device; looked up once per device, thread-safe).
 hipError_t nvfp4_scratch(void** ptr, size_t* bytes);
 
+// Root-mean-square norm of bf16 x (+ res) with a quantized output (e4m3: MXFP8,
+// else MXFP4); h, rstd and y may be null (h not with a residual).
+hipError_t launch_rmsnorm_quant(const void* x, const void* res, const void* w, double eps, int64_t rows,
+                                int64_t cols, int e4m3, void* h, float* rstd, void* y, uint8_t* codes,
+                                uint8_t* scales, hipStream_t st);
+
+// Its backward pass; parts: fp32 [rmsnorm_back_parts(rows), cols].
+int64_t rmsnorm_back_parts(int64_t rows);
+hipError_t launch_rmsnorm_back(const void* dy, const void* h, const void* w, const float* rstd, const void* dh,
+                               int64_t rows, int64_t cols, void* dx, float* dw, float* parts, hipStream_t st);
+
 uint32_t host_sign_word(int had, uint64_t seed);
 
 }  // namespace fp4dev

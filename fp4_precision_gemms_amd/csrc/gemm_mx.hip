@@ -137,14 +137,6 @@ __device__ __forceinline__ uint32_t mask_scale_word(uint32_t w, int64_t first, i
     return w;
 }
 
-// Round-to-nearest-even binary32 -> bfloat16 (NaN -> the quiet NaN 0x7FC0).
-__device__ __forceinline__ uint32_t bf16_rne(float f) {
-    const uint32_t u = __float_as_uint(f);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0x7FC0u;
-    return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-}
-__device__ __forceinline__ float bf16_value(uint32_t b) { return __uint_as_float(b << 16); }
-
 // A 16-byte store of C marked non-temporal: with whole 128-byte lines per
 // instruction the output streams to HBM during the GEMM instead of sitting
 // dirty in the caches until the next kernel's traffic evicts it.  Partial

@@ -1,0 +1,369 @@
+// norm_mx.hip -- root-mean-square norm that adds the residual and leaves its
+// output quantized, and its backward pass.
+//
+// Forward, per row of C elements:
+//     h = bf16(x + residual)                 (binary32 sum, one rounding; h = x without a residual)
+//     r = fl32(1 / sqrt(sum h^2 / C + eps))  (binary64)
+//     y = fl32(fl32(h r) w)
+// and y goes to 32-element blocks with one E8M0 scale each, either MXFP4
+// (E2M1, scale floor(log2 max|y|) - 2) or MXFP8 (E4M3, floor(log2 max|y|) - 8).
+// The sum is held in binary64 so that r, and with it every code, does not
+// depend on the order of the sum: an FP4 code next to a rounding border would
+// otherwise change with the launch shape.  A square of a bf16 value is exact in
+// binary64, so the sum is off by 2^-53 an addition at most.  y itself is not
+// rounded to bf16 before the quantization: one rounding instead of two.
+//
+// Bound by HBM: 2 bytes read per input, 2 written for h, 1 (MXFP8) or 1/2
+// (MXFP4) for the codes.  Each element is read once and kept in registers
+// (bf16 pairs) across the reduction.
+//
+// Backward, with g = dy w and c = sum_j g_j h_j over the row:
+//     dx = r g - h r^3 c / C (+ dh)          (dh: the gradient that reaches h past the norm)
+//     dw = sum over rows of dy h r
+// (the quantization is passed straight through).  A workgroup walks over rows
+// with its columns' part of dw in registers, so dy and h are read once; the
+// parts of all workgroups are summed in a fixed order by a second kernel.
+#include "fp4_launch.hpp"
+#include "mx_device.hpp"
+
+namespace fp4dev {
+namespace {
+
+// a wave's sum, in every lane
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
+    return v;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& w, float* a) {
+    a[0] = bf16_lo(w.x); a[1] = bf16_hi(w.x); a[2] = bf16_lo(w.y); a[3] = bf16_hi(w.y);
+    a[4] = bf16_lo(w.z); a[5] = bf16_hi(w.z); a[6] = bf16_lo(w.w); a[7] = bf16_hi(w.w);
+}
+
+__device__ __forceinline__ uint4 pack8(const float* a) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = bf16_rne(a[2 * i]) | (bf16_rne(a[2 * i + 1]) << 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Codes of 8 values under scale byte `byte` (not 255) as E4M3: the hardware
+// conversion rounds to nearest even but turns what lies beyond 464 into NaN,
+// so the scaled value is clamped to +-448 first.
+__device__ __forceinline__ uint2 encode8_e4m3(const float* y, uint32_t byte) {
+    const float inv = inv_scale_from_e8m0(byte);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __builtin_amdgcn_fmed3f(y[i] * inv, -448.0f, 448.0f);
+    int lo = 0, hi = 0;
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], lo, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], hi, false);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], hi, true);
+    return make_uint2((uint32_t)lo, (uint32_t)hi);
+}
+
+// TPR threads share a row, RPB rows per workgroup; a lane owns V chunks of 8
+// consecutive elements, so four adjacent lanes hold one 32-element block.
+// (x, res and h are not __restrict__: h may be x or res itself; every lane
+// writes only the chunks it has read.)
+template <int TPR, int RPB, int V, bool RES, bool E4M3>
+__global__ __launch_bounds__(TPR * RPB) void rmsnorm_quant(
+    const uint4* x, const uint4* res, const uint4* __restrict__ weight, double eps, int64_t rows,
+    int cols, uint4* h, float* __restrict__ rstd, uint4* __restrict__ y, uint8_t* __restrict__ codes,
+    uint8_t* __restrict__ scales) {
+    static_assert(TPR == 64 || RPB == 1, "rows that share a workgroup are a wave each");
+    constexpr int kWaves = TPR / 64;
+    const int t = threadIdx.x % TPR, nch = cols / 8, q = t & 3;
+    const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+    if (RPB > 1 && row >= rows) return;               // a wave of its own: no barrier below
+    const int64_t base = row * nch;
+    uint4 v[V], wv[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = i * TPR + t;
+        v[i] = c < nch ? x[base + c] : make_uint4(0, 0, 0, 0);
+    }
+    if constexpr (RES) {
+        uint4 rv[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = i * TPR + t;
+            rv[i] = c < nch ? res[base + c] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = i * TPR + t;
+            wv[i] = c < nch ? weight[c] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float a[8], b[8];
+            unpack8(v[i], a);
+            unpack8(rv[i], b);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) a[k] += b[k];
+            v[i] = pack8(a);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = i * TPR + t;
+            wv[i] = c < nch ? weight[c] : make_uint4(0, 0, 0, 0);
+        }
+    }
+    if (h) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = i * TPR + t;
+            if (c < nch) h[base + c] = v[i];
+        }
+    }
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float a[8];
+        unpack8(v[i], a);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s = __builtin_fma((double)a[k], (double)a[k], s);
+    }
+    s = wave_sum(s);
+    if constexpr (kWaves > 1) {
+        __shared__ double part[kWaves];
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+        __syncthreads();
+        s = 0.0;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) s += part[i];
+    }
+    const float r = (float)(1.0 / __builtin_sqrt(s / (double)cols + eps));
+    if (rstd && t == 0) rstd[row] = r;
+    const int nb = cols / 32;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = i * TPR + t;
+        if (c >= nch) continue;                        // uniform per quad: cols % 32 == 0
+        float a[8], w[8];
+        unpack8(v[i], a);
+        unpack8(wv[i], w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) a[k] = (a[k] * r) * w[k];
+        if (y) y[base + c] = pack8(a);
+        uint32_t m = max_abs_bits<8>(a);
+        m = max(m, quad_xor1(m));
+        m = max(m, quad_xor2(m));
+        const int b = c >> 2;
+        if constexpr (E4M3) {
+            const uint32_t byte = e8m0_from_amax_bits_e4m3(m);
+            uint2 word = make_uint2(0, 0);
+            if (byte != 255u) word = encode8_e4m3(a, byte);
+            reinterpret_cast<uint2*>(codes)[base + c] = word;
+            if (q == 0) scales[row * nb + b] = (uint8_t)byte;
+        } else {
+            const uint32_t byte = e8m0_from_amax_bits(m);
+            uint32_t word = 0;
+            if (byte != 255u) {
+                const uint4 z = make_uint4(0, 0, 0, 0);
+                word = byte != 0u ? encode8_hw(a, byte) : encode8_sw<false>(a, byte, z, z);
+            }
+            *reinterpret_cast<uint32_t*>(codes + tiled_offset(row, b, nb) + 4 * q) = word;
+            if (q == 0) scales[((int64_t)(b >> 3) * rows + row) * 8 + (b & 7)] = (uint8_t)byte;
+        }
+    }
+}
+
+template <int TPR, int RPB, int V>
+hipError_t launch_norm(const void* x, const void* res, const void* w, double eps, int64_t rows, int64_t cols,
+                       int e4m3, void* h, float* rstd, void* y, uint8_t* codes, uint8_t* scales, hipStream_t st) {
+    const dim3 grid((unsigned)((rows + RPB - 1) / RPB)), block(TPR * RPB);
+#define FP4_NORM(RES, E)                                                                                \
+    return launch(&rmsnorm_quant<TPR, RPB, V, RES, E>, grid, block, st, (const uint4*)x, (const uint4*)res, \
+                  (const uint4*)w, eps, rows, (int)cols, (uint4*)h, rstd, (uint4*)y, codes, scales)
+    if (res) {
+        if (e4m3) FP4_NORM(true, true);
+        FP4_NORM(true, false);
+    }
+    if (e4m3) FP4_NORM(false, true);
+    FP4_NORM(false, false);
+#undef FP4_NORM
+}
+
+// ---------------------------------------------------------------- backward
+// One workgroup walks over rows blockIdx.x, + gridDim.x, ...; the next row's
+// loads are issued before this row's reduction.
+template <int TPR, int V, bool DH>
+__global__ __launch_bounds__(TPR) void rmsnorm_back(
+    const uint4* __restrict__ dy, const uint4* __restrict__ h, const uint4* __restrict__ weight,
+    const float* __restrict__ rstd, const uint4* dh, int64_t rows, int cols, uint4* dx,
+    float* __restrict__ parts) {
+    constexpr int kWaves = TPR / 64;
+    __shared__ float part[2][kWaves];
+    const int t = threadIdx.x, nch = cols / 8;
+    const float inv_cols = 1.0f / (float)cols;
+    float acc[V][8];
+    uint4 wv[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = i * TPR + t;
+        wv[i] = c < nch ? weight[c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[i][k] = 0.0f;
+    }
+    uint4 gv[V], hv[V], ev[V];
+    float r = 0.0f;
+    auto load = [&](int64_t row) {
+        const int64_t base = row * nch;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = i * TPR + t;
+            gv[i] = c < nch ? dy[base + c] : make_uint4(0, 0, 0, 0);
+            hv[i] = c < nch ? h[base + c] : make_uint4(0, 0, 0, 0);
+            if constexpr (DH) ev[i] = c < nch ? dh[base + c] : make_uint4(0, 0, 0, 0);
+        }
+        r = rstd[row];
+    };
+    int64_t row = blockIdx.x;                          // gridDim.x <= rows
+    load(row);
+    for (int turn = 0; row < rows; turn ^= 1) {
+        uint4 g1[V], h1[V], e1[V];
+        const float r1 = r;
+#pragma unroll
+        for (int i = 0; i < V; ++i) { g1[i] = gv[i]; h1[i] = hv[i]; if constexpr (DH) e1[i] = ev[i]; }
+        const int64_t next = row + gridDim.x;
+        if (next < rows) load(next);
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float a[8], b[8], w[8];
+            unpack8(g1[i], a);
+            unpack8(h1[i], b);
+            unpack8(wv[i], w);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                s += (a[k] * w[k]) * b[k];
+                acc[i][k] += a[k] * (b[k] * r1);
+            }
+        }
+        s = wave_sum(s);
+        if constexpr (kWaves > 1) {
+            // two buffers: the next row's parts do not overwrite these before
+            // the barrier that every reader of these has passed
+            if ((t & 63) == 0) part[turn][t >> 6] = s;
+            __syncthreads();
+            s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i) s += part[turn][i];
+        }
+        const float k3 = r1 * r1 * r1 * (s * inv_cols);
+        const int64_t base = row * nch;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = i * TPR + t;
+            if (c >= nch) continue;
+            float a[8], b[8], w[8], e[8];
+            unpack8(g1[i], a);
+            unpack8(h1[i], b);
+            unpack8(wv[i], w);
+            if constexpr (DH) unpack8(e1[i], e);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                a[k] = r1 * (a[k] * w[k]) - b[k] * k3;
+                if constexpr (DH) a[k] += e[k];
+            }
+            dx[base + c] = pack8(a);
+        }
+        row = next;
+    }
+    float4* out = reinterpret_cast<float4*>(parts + (int64_t)blockIdx.x * cols);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = i * TPR + t;
+        if (c >= nch) continue;
+        out[2 * c] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        out[2 * c + 1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+    }
+}
+
+// dw[c] = sum of n rows of parts[n, cols]: 32 columns per workgroup, 8 slices
+// of the rows, joined in a fixed order.
+__global__ __launch_bounds__(256) void sum_parts(const float* __restrict__ parts, int n, int cols,
+                                                 float* __restrict__ dw) {
+    __shared__ float part[8][32];
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
+    float s = 0.0f;                                    // cols % 32 == 0: c < cols
+    int i = slice;
+    for (; i + 56 < n; i += 64) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = parts[(int64_t)(i + 8 * k) * cols + c];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s += v[k];
+    }
+    for (; i < n; i += 8) s += parts[(int64_t)i * cols + c];
+    part[slice][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (slice == 0) {
+        s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s += part[k][threadIdx.x];
+        dw[c] = s;
+    }
+}
+
+template <int TPR, int V>
+hipError_t launch_back(const void* dy, const void* h, const void* w, const float* rstd, const void* dh,
+                       int64_t rows, int64_t cols, void* dx, float* parts, int64_t n, hipStream_t st) {
+    if (dh)
+        return launch(&rmsnorm_back<TPR, V, true>, dim3((unsigned)n), dim3(TPR), st, (const uint4*)dy,
+                      (const uint4*)h, (const uint4*)w, rstd, (const uint4*)dh, rows, (int)cols, (uint4*)dx, parts);
+    return launch(&rmsnorm_back<TPR, V, false>, dim3((unsigned)n), dim3(TPR), st, (const uint4*)dy,
+                  (const uint4*)h, (const uint4*)w, rstd, (const uint4*)dh, rows, (int)cols, (uint4*)dx, parts);
+}
+
+// Enough rows to fill the card with a wave per row (256 CUs x 8 waves).
+constexpr int64_t kManyRows = 2048;
+
+}  // namespace
+
+hipError_t launch_rmsnorm_quant(const void* x, const void* res, const void* w, double eps, int64_t rows,
+                                int64_t cols, int e4m3, void* h, float* rstd, void* y, uint8_t* codes,
+                                uint8_t* scales, hipStream_t st) {
+    const int64_t nch = cols / 8;
+#define FP4_ROW(TPR, RPB, V) \
+    return launch_norm<TPR, RPB, V>(x, res, w, eps, rows, cols, e4m3, h, rstd, y, codes, scales, st)
+    // many rows: a wave per row, no barrier; few rows or long ones: a
+    // workgroup per row
+    if (rows >= kManyRows && nch <= 512) {
+        if (nch <= 128) FP4_ROW(64, 4, 2);
+        if (nch <= 256) FP4_ROW(64, 4, 4);
+        FP4_ROW(64, 4, 8);
+    }
+    if (nch <= 256) FP4_ROW(256, 1, 1);
+    if (nch <= 512) FP4_ROW(256, 1, 2);
+    if (nch <= 1024) FP4_ROW(256, 1, 4);
+    if (nch <= 2048) FP4_ROW(1024, 1, 2);
+    FP4_ROW(1024, 1, 4);
+#undef FP4_ROW
+}
+
+int64_t rmsnorm_back_parts(int64_t rows) {
+    // workgroups of the backward pass
+    return rows < 1024 ? rows : 1024;
+}
+
+hipError_t launch_rmsnorm_back(const void* dy, const void* h, const void* w, const float* rstd, const void* dh,
+                               int64_t rows, int64_t cols, void* dx, float* dw, float* parts, hipStream_t st) {
+    const int64_t nch = cols / 8, n = rmsnorm_back_parts(rows);
+    hipError_t e;
+    if (nch <= 256) e = launch_back<256, 1>(dy, h, w, rstd, dh, rows, cols, dx, parts, n, st);
+    else if (nch <= 512) e = launch_back<256, 2>(dy, h, w, rstd, dh, rows, cols, dx, parts, n, st);
+    else if (nch <= 1024) e = launch_back<256, 4>(dy, h, w, rstd, dh, rows, cols, dx, parts, n, st);
+    else if (nch <= 2048) e = launch_back<1024, 2>(dy, h, w, rstd, dh, rows, cols, dx, parts, n, st);
+    else e = launch_back<1024, 4>(dy, h, w, rstd, dh, rows, cols, dx, parts, n, st);
+    if (e != hipSuccess) return e;
+    return launch(&sum_parts, dim3((unsigned)(cols / 32)), dim3(256), st, (const float*)parts, (int)n, (int)cols, dw);
+}
+
+}  // namespace fp4dev

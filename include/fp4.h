@@ -337,6 +337,62 @@ fp4_status nvfp4_quantize_noalloc(const void* x_bf16, int64_t rows, int64_t cols
                                   const float* amax_in, uint8_t* codes, uint8_t* scales_e4m3,
                                   float* tensor_scale, void* stream);
 
+/* Element format of a quantized operand with E8M0 scales per 32 elements. */
+typedef enum {
+    FP4_FMT_MXFP4 = 0,   /* E2M1 codes, tiled; scales k-grouped (as above)        */
+    FP4_FMT_MXFP8 = 1    /* E4M3 codes, row-major [R, C] bytes; scales row-major
+                            [R, C/32]; e = floor(log2 max|y|) - 8, codes to
+                            nearest even, saturating at +-448                     */
+} fp4_format;
+
+/*
+ * fp4_rmsnorm_quantize -- the norm that feeds a quantized linear layer: adds
+ * the residual, normalizes each row by its root mean square and writes the
+ * result quantized along cols.  Per row of x[rows, cols] (C = cols):
+ *   h = bf16(x + residual), the binary32 sum rounded once (h = x without a
+ *       residual);
+ *   r = fl32(1 / sqrt(sum h^2 / C + eps)), computed in binary64;
+ *   y = fl32(fl32(h r) weight), and y in 32-element blocks to `fmt`:
+ *       FP4_FMT_MXFP4 as fp4_hadamard_quantize does without a rotation,
+ *       rounded to nearest; FP4_FMT_MXFP8 with the same rule for the scale
+ *       byte (0xFF and zero codes for a block holding a NaN or an infinity, 0
+ *       for a zero block), E4M3 codes of y 2^-e.
+ * Outputs: codes and scales of an operand of `rows` rows of `cols` elements
+ * (FP4_CODE_BYTES / FP4_SCALE_BYTES bytes for MXFP4; rows * cols and
+ * rows * cols / 32 for MXFP8); h bf16 [rows, cols], required with a residual,
+ * may be x or residual themselves (in place); NULL without one if not wanted;
+ * rstd fp32 [rows] = r, and y_bf16 [rows, cols] = y rounded to bf16, each NULL
+ * if not wanted (a backward pass needs h, rstd and y).  y_bf16 must not
+ * overlap an input.
+ * Requirements: cols % 32 == 0, cols <= 32768, rows < 2^31; weight bf16
+ * [cols]; eps >= 0 (else FP4_ERR_ENUM); pointers 16-byte aligned (rstd 4).
+ */
+fp4_status fp4_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16,
+                                const void* weight_bf16, double eps, int64_t rows, int64_t cols,
+                                fp4_format fmt, void* h_bf16, float* rstd, void* y_bf16,
+                                uint8_t* codes, uint8_t* scales, void* stream);
+
+/*
+ * fp4_rmsnorm_backward -- gradients of y = h r weight (the quantization is
+ * passed straight through), from dy bf16 [rows, cols], the h and rstd of the
+ * forward pass and the weight.  With g = dy weight and c = sum_j g_j h_j:
+ *   dx = bf16(r g - h r^3 c / C + dh), dh (bf16, may be NULL) the gradient
+ *        that reaches h past the norm; dx is the gradient of x and of the
+ *        residual alike, and may be dh itself (in place) but no other input;
+ *   dw[cols] = sum over rows of dy h r, fp32, summed in an order that depends
+ *        on rows only (the same inputs give the same bits).
+ * All in binary32.  workspace: fp4_rmsnorm_workspace_bytes() bytes, whose
+ * contents need not be kept between calls; calls that overlap need one each.
+ * Requirements as for fp4_rmsnorm_quantize; FP4_ERR_WORKSPACE if too small.
+ */
+fp4_status fp4_rmsnorm_backward(const void* dy_bf16, const void* h_bf16, const void* weight_bf16,
+                                const float* rstd, const void* dh_bf16, int64_t rows, int64_t cols,
+                                void* dx_bf16, float* dw, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* Workspace bytes fp4_rmsnorm_backward needs for [rows, cols]. */
+size_t fp4_rmsnorm_workspace_bytes(int64_t rows, int64_t cols);
+
 /* Static, NUL-terminated name of a status code. */
 const char* fp4_status_string(fp4_status status);
 
