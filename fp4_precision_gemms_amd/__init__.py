@@ -72,6 +72,12 @@ def lib() -> ctypes.CDLL:
     L.fp4_rmsnorm_backward.restype = i32
     L.fp4_rmsnorm_workspace_bytes.argtypes = [i64, i64]
     L.fp4_rmsnorm_workspace_bytes.restype = ctypes.c_size_t
+    L.fp4_gemm_decode.argtypes = [vp, vp, i32, vp, vp, i64, i64, i64, vp, i32, vp]
+    L.fp4_gemm_decode.restype = i32
+    L.fp4_quantize_grouped.argtypes = [vp, vp, i64, i64, i64, i32, i32, u64, i32, u64, u64, vp, vp, vp, vp, vp]
+    L.fp4_quantize_grouped.restype = i32
+    L.fp4_gemm_grouped.argtypes = [vp, vp, i32, vp, i64, i64, vp, vp, i64, i64, vp, i32, vp]
+    L.fp4_gemm_grouped.restype = i32
     L.fp4_status_string.argtypes = [i32]
     L.fp4_status_string.restype = ctypes.c_char_p
     _lib = L
@@ -447,6 +453,130 @@ def fp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor
     _call(lib().fp4_rmsnorm_backward, dev, stream, dy.data_ptr(), h.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
           _ptr(dh), rows, cols, dx.data_ptr(), dw.data_ptr(), workspace.data_ptr(), workspace.numel())
     return dx, dw
+
+
+_OUT_TYPES = {OUT_F32: torch.float32, OUT_BF16: torch.bfloat16}
+
+
+def _few_operand(a: torch.Tensor, as_: torch.Tensor):
+    """(fmt, rows, K) of activations, by the shape of their codes."""
+    if a.dim() == 2:
+        if as_.shape != (a.shape[0], a.shape[1] // 32):
+            raise ValueError("MXFP8 codes %s and scales %s do not describe one operand"
+                             % (tuple(a.shape), tuple(as_.shape)))
+        return FMT_MXFP8, a.shape[0], a.shape[1]
+    return (FMT_MXFP4, *mx_dims(a, as_))
+
+
+def _product_out(out, shape, out_dtype: int, device):
+    dt = _OUT_TYPES[out_dtype]
+    if out is None:
+        return torch.empty(shape, dtype=dt, device=device)
+    _need_on(out, dt, shape, device, "out")
+    return out
+
+
+def fp4_gemm_decode(aq: torch.Tensor, as_: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
+                    out: torch.Tensor | None = None, out_dtype: int = OUT_BF16, stream=None):
+    """c[M, N] = A W^T for few rows: A MXFP8 (codes [M, K], scales [M, K/32])
+    or MXFP4 (codes and scales of mx_shapes(M, K)), W [N, K] MXFP4 (see
+    include/fp4.h)."""
+    fmt, M, K = _few_operand(aq, as_)
+    N, Kw = mx_dims(wq, ws)
+    if K != Kw:
+        raise ValueError("decode operands have different contraction sizes (%d, %d)" % (K, Kw))
+    dev = aq.device
+    for t, n in ((aq, "a codes"), (as_, "a scales"), (wq, "w codes"), (ws, "w scales")):
+        _need_on(t, torch.uint8, t.shape, dev, n)
+    out = _product_out(out, (M, N), out_dtype, dev)
+    _call(lib().fp4_gemm_decode, dev, stream, aq.data_ptr(), as_.data_ptr(), fmt, wq.data_ptr(), ws.data_ptr(),
+          M, N, K, out.data_ptr(), out_dtype)
+    return out
+
+
+def grouped_shapes(rows: int, cols: int, experts: int, axis: int):
+    """(codes shape, scales shape) of fp4_quantize_grouped's outputs for
+    x[rows, cols] along `axis`."""
+    units = rows // 32 + experts
+    if axis == AXIS_COLS:
+        return (units, cols // 32, 512), scale_shape(32 * units, cols)
+    return (cols // 32, units, 512), (rows // 256 + experts, cols, 8)
+
+
+def _offsets(offsets: torch.Tensor, device) -> int:
+    """The number of experts of row offsets (int32 [experts + 1])."""
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("offsets must be int32 [experts + 1], got shape %s" % (tuple(offsets.shape),))
+    _need_on(offsets, torch.int32, offsets.shape, device, "offsets")
+    return offsets.shape[0] - 1
+
+
+def _quantize_grouped(x, offsets, axes, had_n, had, sign_seed, rnd, sr_rows, sr_cols, out, stream):
+    rows, cols = x.shape
+    dev = x.device
+    _need_on(x, torch.bfloat16, (rows, cols), dev, "x")
+    experts = _offsets(offsets, dev)
+    shapes = [s for axis in axes for s in grouped_shapes(rows, cols, experts, axis)]
+    if out is None:
+        out = [torch.empty(s, dtype=torch.uint8, device=dev) for s in shapes]
+    elif len(out) != len(shapes):
+        raise ValueError("out must hold %d tensors" % len(shapes))
+    else:
+        for t, s in zip(out, shapes):
+            _need_on(t, torch.uint8, s, dev, "output")
+    p = [t.data_ptr() for t in out]
+    r = p[:2] if AXIS_ROWS in axes else [None, None]
+    c = p[-2:] if AXIS_COLS in axes else [None, None]
+    m = 2 ** 64 - 1
+    _call(lib().fp4_quantize_grouped, dev, stream, x.data_ptr(), offsets.data_ptr(), experts, rows, cols, had_n, had,
+          sign_seed & m, rnd, sr_rows & m, sr_cols & m, *r, *c)
+    return tuple(out)
+
+
+def fp4_quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, axis: int = AXIS_COLS, had_n: int = 32,
+                         had: int = HAD_NONE, sign_seed: int = 0, rnd: int = RTN, sr_seed: int = 0, out=None,
+                         stream=None):
+    """(codes, scales) of bf16 x[rows, cols] with rows grouped by expert
+    (offsets int32 [experts + 1], on the GPU), along `axis`, in the shapes of
+    grouped_shapes (see include/fp4.h)."""
+    return _quantize_grouped(x, offsets, (axis,), had_n, had, sign_seed, rnd, sr_seed, sr_seed, out, stream)
+
+
+def fp4_quantize_grouped_dual(x: torch.Tensor, offsets: torch.Tensor, had_n: int = 32, had: int = HAD_NONE,
+                              sign_seed: int = 0, rnd: int = RTN, sr_seed_rows: int = 0, sr_seed_cols: int = 0,
+                              out=None, stream=None):
+    """Both quantizations of x from one read: (codes, scales) along rows,
+    rotated, and (codes, scales) along cols, not rotated."""
+    return _quantize_grouped(x, offsets, (AXIS_ROWS, AXIS_COLS), had_n, had, sign_seed, rnd, sr_seed_rows,
+                             sr_seed_cols, out, stream)
+
+
+def fp4_gemm_grouped(aq: torch.Tensor, as_: torch.Tensor, offsets: torch.Tensor, wq: torch.Tensor,
+                     ws: torch.Tensor, rows: int, out: torch.Tensor | None = None, out_dtype: int = OUT_BF16,
+                     stream=None):
+    """c[rows, N]: each expert's rows times its weight (see include/fp4.h).
+    aq, as_: MXFP4 of fp4_quantize_grouped(x, offsets) or MXFP8 row-major; wq
+    [experts, ceil(N/32), K/32, 512] and ws [experts, ceil(K/256), N, 8]: the
+    experts' weights, each quantized along its contraction.  Rows of no expert
+    are left as they were (in a new tensor: not set)."""
+    dev = aq.device
+    experts = _offsets(offsets, dev)
+    if wq.dim() != 4 or ws.dim() != 4 or wq.shape[0] != experts or ws.shape[0] != experts:
+        raise ValueError("weights must be codes [experts, ceil(N/32), K/32, 512] and scales [experts, ceil(K/256), "
+                         "N, 8] of %d experts, got %s and %s" % (experts, tuple(wq.shape), tuple(ws.shape)))
+    N, K = ws.shape[2], wq.shape[2] * 32
+    if wq.shape[1:] != code_shape(N, K) or ws.shape[1:] != scale_shape(N, K):
+        raise ValueError("codes %s and scales %s do not describe one operand" % (tuple(wq.shape), tuple(ws.shape)))
+    fmt = FMT_MXFP8 if aq.dim() == 2 else FMT_MXFP4
+    shapes = mx8_shapes(rows, K) if fmt == FMT_MXFP8 else grouped_shapes(rows, K, experts, AXIS_COLS)
+    _need_on(aq, torch.uint8, shapes[0], dev, "a codes")
+    _need_on(as_, torch.uint8, shapes[1], dev, "a scales")
+    _need_on(wq, torch.uint8, wq.shape, dev, "w codes")
+    _need_on(ws, torch.uint8, ws.shape, dev, "w scales")
+    out = _product_out(out, (rows, N), out_dtype, dev)
+    _call(lib().fp4_gemm_grouped, dev, stream, aq.data_ptr(), as_.data_ptr(), fmt, offsets.data_ptr(), experts, rows,
+          wq.data_ptr(), ws.data_ptr(), N, K, out.data_ptr(), out_dtype)
+    return out
 
 
 from . import linear  # noqa: E402  (the autograd layer built on the calls above)

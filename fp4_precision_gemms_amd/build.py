@@ -24,7 +24,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "libfp4.so")
 CALIB_LIB_PATH = os.path.join(HERE, "libfp4calib.so")
 
-SOURCES = ["fp4_abi.cpp", "quant_mx.hip", "gemm_mx.hip", "nvfp4.hip", "norm_mx.hip"]
+SOURCES = ["fp4_abi.cpp", "quant_mx.hip", "gemm_mx.hip", "nvfp4.hip", "norm_mx.hip", "gemm_few.hip",
+           "quant_grouped.hip"]
 CALIB_SOURCES = ["calib_mfma.hip"]
 ARCH = "gfx950"
 

@@ -236,6 +236,64 @@ fp4_status fp4_rmsnorm_backward(const void* dy_bf16, const void* h_bf16, const v
                                                 dw, (float*)workspace, (hipStream_t)stream));
 }
 
+namespace {
+constexpr int64_t kMaxExperts = 1024;
+
+fp4_status check_grouped_product(const uint8_t* a, const uint8_t* as, fp4_format fmt, const uint8_t* wq,
+                                 const uint8_t* ws, int64_t experts, int64_t rows, int64_t N, int64_t K,
+                                 const void* c, fp4_out_dtype out) {
+    if (fmt != FP4_FMT_MXFP4 && fmt != FP4_FMT_MXFP8) return FP4_ERR_ENUM;
+    if (out != FP4_OUT_F32 && out != FP4_OUT_BF16) return FP4_ERR_ENUM;
+    if (!a || !as || !wq || !ws || !c) return FP4_ERR_NULL;
+    if (rows <= 0 || N <= 0 || K <= 0 || K % 32 || K >= kMaxContraction || rows > INT32_MAX || N > INT32_MAX ||
+        experts <= 0 || experts > kMaxExperts)
+        return FP4_ERR_SHAPE;
+    if (!product_ok(rows + 32 * experts, K) || !product_ok(N * experts, K) || !product_ok(rows, N))
+        return FP4_ERR_SHAPE;
+    if (!aligned16(a) || !aligned16(as) || !aligned16(wq) || !aligned16(ws) || !aligned16(c)) return FP4_ERR_ALIGN;
+    return FP4_OK;
+}
+}  // namespace
+
+fp4_status fp4_gemm_decode(const uint8_t* a, const uint8_t* as, fp4_format fmt, const uint8_t* wq,
+                           const uint8_t* ws, int64_t M, int64_t N, int64_t K, void* c, fp4_out_dtype out,
+                           void* stream) {
+    if (const fp4_status s = check_grouped_product(a, as, fmt, wq, ws, 1, M, N, K, c, out)) return s;
+    return from_hip(fp4dev::launch_gemm_few(a, as, fmt == FP4_FMT_MXFP8, nullptr, wq, ws, M, 1, N, K, c,
+                                            out == FP4_OUT_BF16, (hipStream_t)stream));
+}
+
+fp4_status fp4_quantize_grouped(const void* x_bf16, const int32_t* offsets, int64_t experts, int64_t rows,
+                                int64_t cols, int had_n, fp4_hadamard had, uint64_t sign_seed, fp4_rounding rnd,
+                                uint64_t sr_seed_rows, uint64_t sr_seed_cols, uint8_t* codes_rows,
+                                uint8_t* scales_rows, uint8_t* codes_cols, uint8_t* scales_cols, void* stream) {
+    if (had != FP4_HAD_NONE && had != FP4_HAD_DET && had != FP4_HAD_SIGNED) return FP4_ERR_ENUM;
+    if (had != FP4_HAD_NONE && had_n != 16 && had_n != 32) return FP4_ERR_ENUM;
+    if (rnd != FP4_RTN && rnd != FP4_SR) return FP4_ERR_ENUM;
+    if (!x_bf16 || !offsets || (!codes_rows && !codes_cols) || !codes_rows != !scales_rows ||
+        !codes_cols != !scales_cols)
+        return FP4_ERR_NULL;
+    if (rows <= 0 || rows > INT32_MAX || cols <= 0 || cols % 32 || cols >= kMaxContraction || experts <= 0 ||
+        experts > kMaxExperts || ((cols + 255) / 256) * (rows / 32 + experts) > INT32_MAX)
+        return FP4_ERR_SHAPE;
+    if (!aligned16(x_bf16) || !aligned4(offsets) || !aligned16(codes_rows) || !aligned16(scales_rows) ||
+        !aligned16(codes_cols) || !aligned16(scales_cols))
+        return FP4_ERR_ALIGN;
+    return from_hip(fp4dev::launch_quant_grouped(x_bf16, offsets, experts, rows, cols, had_n, (int)had, sign_seed,
+                                                 (int)rnd, sr_seed_rows, sr_seed_cols, codes_rows, scales_rows,
+                                                 codes_cols, scales_cols, (hipStream_t)stream));
+}
+
+fp4_status fp4_gemm_grouped(const uint8_t* a, const uint8_t* as, fp4_format fmt, const int32_t* offsets,
+                            int64_t experts, int64_t rows, const uint8_t* wq, const uint8_t* ws, int64_t N,
+                            int64_t K, void* c, fp4_out_dtype out, void* stream) {
+    if (!offsets) return FP4_ERR_NULL;
+    if (const fp4_status s = check_grouped_product(a, as, fmt, wq, ws, experts, rows, N, K, c, out)) return s;
+    if (!aligned4(offsets)) return FP4_ERR_ALIGN;
+    return from_hip(fp4dev::launch_gemm_few(a, as, fmt == FP4_FMT_MXFP8, offsets, wq, ws, rows, experts, N, K, c,
+                                            out == FP4_OUT_BF16, (hipStream_t)stream));
+}
+
 const char* fp4_status_string(fp4_status status) {
     switch (status) {
         case FP4_OK: return "FP4_OK";

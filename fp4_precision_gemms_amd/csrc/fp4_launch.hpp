@@ -73,6 +73,19 @@ int64_t rmsnorm_back_parts(int64_t rows);
 hipError_t launch_rmsnorm_back(const void* dy, const void* h, const void* w, const float* rstd, const void* dh,
                                int64_t rows, int64_t cols, void* dx, float* dw, float* parts, hipStream_t st);
 
+// C[rows, N] = A W^T for few rows (per expert): A MXFP8 (a_e4m3) or MXFP4, W
+// MXFP4; offsets null and experts 1 for a product without groups.
+hipError_t launch_gemm_few(const uint8_t* a, const uint8_t* as, int a_e4m3, const int* offsets, const uint8_t* w,
+                           const uint8_t* ws, int64_t rows, int64_t experts, int64_t N, int64_t K, void* c,
+                           int out_bf16, hipStream_t st);
+
+// MXFP4 quantization of rows grouped by expert, along rows (codes_r) and / or
+// along cols (codes_c).
+hipError_t launch_quant_grouped(const void* x, const int* offsets, int64_t experts, int64_t rows, int64_t cols,
+                                int had_n, int had, uint64_t sign_seed, int rnd, uint64_t sr_rows, uint64_t sr_cols,
+                                uint8_t* codes_r, uint8_t* scales_r, uint8_t* codes_c, uint8_t* scales_c,
+                                hipStream_t st);
+
 uint32_t host_sign_word(int had, uint64_t seed);
 
 }  // namespace fp4dev

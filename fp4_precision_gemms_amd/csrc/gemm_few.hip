@@ -1,0 +1,310 @@
+// gemm_few.hip -- product of a few rows with MXFP4 weights on gfx950 matrix
+// cores: C[m, n] = sum_k a[m, k] w[n, k], for single tokens and small batches,
+// dense or with the rows grouped by expert.  The activations are MXFP8 (E4M3,
+// row-major) or MXFP4 (the tiled layout of the quantizers).
+//
+// Bound by the weights, read once from HBM: N K (1/2 + 1/32) bytes.  So the
+// split follows the weights:
+//   - a workgroup owns 16 NT weight rows n (of one expert) and all of K; its
+//     waves take the 256-element k-groups in turn, so that a weight matrix
+//     of a few thousand rows already fills the card with loads, and the
+//     partial sums meet in LDS, added in a fixed order (no atomics, no second
+//     launch);
+//   - the weights are the first operand of 16-row MFMAs, so a lane's
+//     accumulator is four consecutive n of one row m.  16 rows is the smallest
+//     tile there is; rows past the last read as zero (out-of-range buffer
+//     loads fetch nothing);
+//   - a lane holds block l / 16 of row l mod 16 of each 128-element k-step:
+//     16 bytes of a tiled chunk (32 bytes of a row for MXFP8).  The scales of
+//     a row's 8 blocks of a k-group are one 8-byte load; the next k-group's
+//     loads are issued before this one's products.
+//   - MXFP4 activations: one V_MFMA_SCALE_F32_16X16X128_F8F6F4 per k-step,
+//     exact products, fp32 sums.  MXFP8 activations: that instruction with an
+//     8-bit operand drops what lies 2^-14 below the largest product it adds up
+//     (measured with one large and one small product), so both operands are
+//     turned into bf16 instead -- exact: E2M1 has 2 significant bits, E4M3
+//     has 4, and the block scale is a power of two that the conversion
+//     applies -- and take four V_MFMA_F32_16X16X32_BF16.  A k-step's elements
+//     are then in another order (the lane's 8 consecutive ones per
+//     instruction), the same for both operands.
+// More than 16 MT rows (of an expert) are taken one tile after another; the
+// weights then come from the caches.
+#include "fp4_device.hpp"
+#include "fp4_launch.hpp"
+#include "grouped.hpp"
+
+namespace fp4dev {
+namespace {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+
+constexpr int kBufferWord3 = 0x00020000;   // raw buffer, 32-bit data format
+constexpr uint32_t kOob = 0x80000000u;     // a buffer offset past any range: reads zero
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, kBufferWord3);
+}
+__device__ __forceinline__ v4i load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
+// Bytes of the scale word of blocks first .. first + 3 that lie past the last
+// block set to 127 (2^0): their codes read as zero, and a stray 0xFF (NaN)
+// would not.
+__device__ __forceinline__ uint32_t past_end_to_one(uint32_t w, int first, int nb) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (first + i >= nb) w = (w & ~(0xFFu << (8 * i))) | (127u << (8 * i));
+    return w;
+}
+
+// A block's 32 elements times 2^(byte - 127) as bf16, 8 consecutive ones per
+// vector.  Byte 255 gives NaN and byte 0 2^-127 (the conversions take the
+// exponent field of the scale as it is).
+__device__ __forceinline__ void bf16_of_e2m1(const v4i& codes, uint32_t byte, v8bf* out) {
+    const float s = __uint_as_float(byte << 23);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const uint32_t w = (uint32_t)codes[p];
+        const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
+        const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
+        const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
+        const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
+        out[p] = v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+    }
+}
+__device__ __forceinline__ void bf16_of_e4m3(const v4i* codes, uint32_t byte, v8bf* out) {
+    const float s = __uint_as_float(byte << 23);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const uint32_t lo = (uint32_t)codes[p / 2][2 * (p & 1)], hi = (uint32_t)codes[p / 2][2 * (p & 1) + 1];
+        const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false);
+        const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true);
+        const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, false);
+        const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true);
+        out[p] = v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+    }
+}
+
+// What one 256-element k-group needs: two 128-element k-steps of MT row tiles
+// and NT weight tiles, with their scales.
+template <bool A8, int MT, int NT>
+struct Group {
+    v4i w[NT][2];
+    uint2 ws[NT];
+    v4i a[MT][2][A8 ? 2 : 1];
+    uint2 as[MT];       // MXFP4: the 8 blocks' bytes; MXFP8: this lane's byte of each k-step
+};
+
+template <bool A8, int MT, int NT, int W, bool OBF16>
+__global__ __launch_bounds__(64 * W) void gemm_few(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ SA, const int* __restrict__ offsets,
+    const uint8_t* __restrict__ B, const uint8_t* __restrict__ SB, int64_t rows, int experts, int64_t N,
+    int64_t K, void* __restrict__ C) {
+    __shared__ v4f part[W][MT * NT][64];
+    const int lane = threadIdx.x & 63, l16 = lane & 15, quad = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int e = blockIdx.y;
+    const int64_t n0 = (int64_t)blockIdx.x * (16 * NT);
+    const int nb = (int)(K / 32), groups = (nb + 7) / 8;
+
+    // this expert's rows [lo, hi), clamped to the operand whatever the offsets say
+    int64_t lo = 0, hi = rows, first = 0, arows = rows;
+    if (offsets) {
+        const RowRange r = expert_rows(offsets, e, rows);
+        lo = r.lo;
+        hi = r.hi;
+        if (lo == hi) return;
+        if constexpr (A8) {
+            first = lo;
+        } else {
+            first = (lo / 32 + e) * 32;
+            arows = (rows / 32 + experts) * 32;
+        }
+    }
+    const int64_t gstride = (int64_t)nb * 512;         // bytes of a 32-row group of codes
+    B += (int64_t)e * ((N + 31) / 32) * gstride;
+    SB += (int64_t)e * groups * N * 8;
+    const int nleft = (int)((N - n0) < 16 * NT ? (N - n0) : 16 * NT);
+    const __amdgpu_buffer_rsrc_t rb =
+        buffer(B + (n0 / 32) * gstride, ((n0 + nleft + 31) / 32 - n0 / 32) * gstride);
+    uint32_t offb[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int r = (int)(n0 & 31) + 16 * j + l16;
+        offb[j] = (uint32_t)((r >> 5) * gstride) + (r & 31) * 16;
+    }
+
+    for (int64_t m0 = lo; m0 < hi; m0 += 16 * MT) {
+        const int mleft = (int)((hi - m0) < 16 * MT ? (hi - m0) : 16 * MT);
+        const int64_t p0 = first + (m0 - lo);          // the tile's first row in the A operand
+        const __amdgpu_buffer_rsrc_t ra =
+            A8 ? buffer(A + p0 * K, (int64_t)mleft * K)
+               : buffer(A + (p0 / 32) * gstride, (((p0 & 31) + mleft + 31) / 32) * gstride);
+        const __amdgpu_buffer_rsrc_t rsa = buffer(SA + (A8 ? p0 * nb : 0), A8 ? (int64_t)mleft * nb : 0);
+        auto load = [&](int g) {
+            Group<A8, MT, NT> t;
+            const int b0 = 8 * g + quad;
+            const bool in[2] = {b0 < nb, b0 + 4 < nb};
+            const __amdgpu_buffer_rsrc_t rsb = buffer(SB + ((int64_t)g * N + n0) * 8, nleft * 8);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    t.w[j][s] = load16(rb, in[s] ? offb[j] + (uint32_t)(b0 + 4 * s) * 512 : kOob);
+                const auto v = __builtin_amdgcn_raw_buffer_load_b64(rsb, (16 * j + l16) * 8, 0, 0);
+                t.ws[j] = make_uint2(v[0], v[1]);
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const int m = 16 * i + l16;
+                if constexpr (A8) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const uint32_t o = in[s] ? (uint32_t)m * (uint32_t)K + (uint32_t)(b0 + 4 * s) * 32 : kOob;
+                        t.a[i][s][0] = load16(ra, o);
+                        t.a[i][s][1] = load16(ra, o + 16);
+                    }
+                    const uint32_t o = (uint32_t)m * (uint32_t)nb + (uint32_t)b0;
+                    t.as[i].x = __builtin_amdgcn_raw_buffer_load_b8(rsa, in[0] ? o : kOob, 0, 0);
+                    t.as[i].y = __builtin_amdgcn_raw_buffer_load_b8(rsa, in[1] ? o + 4 : kOob, 0, 0);
+                } else {
+                    const int r = (int)(p0 & 31) + m;
+                    const uint32_t o = (uint32_t)((r >> 5) * gstride) + (r & 31) * 16;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+                        t.a[i][s][0] = load16(ra, in[s] ? o + (uint32_t)(b0 + 4 * s) * 512 : kOob);
+                    const auto v = __builtin_amdgcn_raw_buffer_load_b64(
+                        buffer(SA + ((int64_t)g * arows + p0) * 8, mleft * 8), m * 8, 0, 0);
+                    t.as[i] = make_uint2(v[0], v[1]);
+                }
+            }
+            return t;
+        };
+        v4f acc[MT][NT] = {};
+        auto multiply = [&](Group<A8, MT, NT>& t, int g) {
+            if (8 * g + 8 > nb) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    t.ws[j] = make_uint2(past_end_to_one(t.ws[j].x, 8 * g, nb),
+                                         past_end_to_one(t.ws[j].y, 8 * g + 4, nb));
+                if constexpr (!A8)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+                        t.as[i] = make_uint2(past_end_to_one(t.as[i].x, 8 * g, nb),
+                                             past_end_to_one(t.as[i].y, 8 * g + 4, nb));
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                uint32_t sw[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) sw[j] = (s ? t.ws[j].y : t.ws[j].x) >> (8 * quad);
+                if constexpr (A8) {
+                    v8bf a[MT][4];
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) bf16_of_e4m3(t.a[i][s], s ? t.as[i].y : t.as[i].x, a[i]);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        v8bf w[4];
+                        bf16_of_e2m1(t.w[j][s], sw[j] & 255u, w);
+#pragma unroll
+                        for (int p = 0; p < 4; ++p)
+#pragma unroll
+                            for (int i = 0; i < MT; ++i)
+                                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[p], a[i][p], acc[i][j], 0, 0, 0);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const v8i w = __builtin_shufflevector(t.w[j][s], v4i{0, 0, 0, 0}, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            const v8i a = __builtin_shufflevector(t.a[i][s][0], v4i{0, 0, 0, 0}, 0, 1, 2, 3, 4, 5, 6, 7);
+                            const uint32_t sa = (s ? t.as[i].y : t.as[i].x) >> (8 * quad);
+                            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, acc[i][j], 4, 4, 0,
+                                                                                         (int)sw[j], 0, (int)sa);
+                        }
+                    }
+                }
+            }
+        };
+        int g = wave;
+        if (g < groups) {
+            Group<A8, MT, NT> t = load(g);
+            for (; g + W < groups; g += W) {
+                Group<A8, MT, NT> next = load(g + W);
+                multiply(t, g);
+                t = next;
+            }
+            multiply(t, g);
+        }
+        // join the waves' sums: tile (i, j) is added up by wave (i NT + j) mod W
+        if (m0 != lo) __syncthreads();                 // the previous tile's sums have been read
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) part[wave][i * NT + j][lane] = acc[i][j];
+        __syncthreads();
+        for (int q = wave; q < MT * NT; q += W) {
+            v4f s = part[0][q][lane];
+#pragma unroll
+            for (int w = 1; w < W; ++w) s += part[w][q][lane];
+            const int m = 16 * (q / NT) + l16, n = 16 * (q % NT) + 4 * quad;
+            if (m >= mleft || n >= nleft) continue;
+            const int64_t at = (m0 + m) * N + n0 + n;
+            const bool whole = n + 4 <= nleft && (N & 3) == 0;
+            if constexpr (OBF16) {
+                uint16_t* p = reinterpret_cast<uint16_t*>(C) + at;
+                if (whole) {
+                    *reinterpret_cast<uint2*>(p) = make_uint2(bf16_rne(s[0]) | (bf16_rne(s[1]) << 16),
+                                                              bf16_rne(s[2]) | (bf16_rne(s[3]) << 16));
+                } else {
+                    for (int k = 0; k < 4 && n + k < nleft; ++k) p[k] = (uint16_t)bf16_rne(s[k]);
+                }
+            } else {
+                float* p = reinterpret_cast<float*>(C) + at;
+                if (whole) {
+                    *reinterpret_cast<v4f*>(p) = s;
+                } else {
+                    for (int k = 0; k < 4 && n + k < nleft; ++k) p[k] = s[k];
+                }
+            }
+        }
+    }
+}
+
+template <bool A8, int MT, int NT, int W>
+hipError_t launch_few(const uint8_t* a, const uint8_t* as, const int* offsets, const uint8_t* w, const uint8_t* ws,
+                      int64_t rows, int64_t experts, int64_t N, int64_t K, void* c, int out_bf16, hipStream_t st) {
+    const dim3 grid((unsigned)((N + 16 * NT - 1) / (16 * NT)), (unsigned)experts);
+    return out_bf16 ? launch(&gemm_few<A8, MT, NT, W, true>, grid, dim3(64 * W), st, a, as, offsets, w, ws, rows,
+                             (int)experts, N, K, c)
+                    : launch(&gemm_few<A8, MT, NT, W, false>, grid, dim3(64 * W), st, a, as, offsets, w, ws, rows,
+                             (int)experts, N, K, c);
+}
+
+template <bool A8>
+hipError_t choose(const uint8_t* a, const uint8_t* as, const int* offsets, const uint8_t* w, const uint8_t* ws,
+                  int64_t rows, int64_t experts, int64_t N, int64_t K, void* c, int out_bf16, hipStream_t st) {
+#define FP4_FEW(MT, NT) return launch_few<A8, MT, NT, 8>(a, as, offsets, w, ws, rows, experts, N, K, c, out_bf16, st)
+    const int64_t each = (rows + experts - 1) / experts;
+    if (each <= 16) FP4_FEW(1, 1);
+    if (each <= 32) FP4_FEW(2, 1);
+    FP4_FEW(4, 1);
+#undef FP4_FEW
+}
+
+}  // namespace
+
+hipError_t launch_gemm_few(const uint8_t* a, const uint8_t* as, int a_e4m3, const int* offsets, const uint8_t* w,
+                           const uint8_t* ws, int64_t rows, int64_t experts, int64_t N, int64_t K, void* c,
+                           int out_bf16, hipStream_t st) {
+    return a_e4m3 ? choose<true>(a, as, offsets, w, ws, rows, experts, N, K, c, out_bf16, st)
+                  : choose<false>(a, as, offsets, w, ws, rows, experts, N, K, c, out_bf16, st);
+}
+
+}  // namespace fp4dev

@@ -1,0 +1,50 @@
+// grouped.hpp -- rows grouped by expert: where an expert's rows sit in the
+// operands, from the row offsets alone.
+//
+// offsets[0 .. experts]: expert e owns rows [offsets[e], offsets[e + 1]) of a
+// tensor of `rows` rows.  In a layout with units of U rows (U = 32: a row
+// group of the codes or a 32-token block; U = 256: a scale group) expert e
+// starts at unit offsets[e] / U + e.  Its ceil(count / U) units always fit
+// before the next expert's first one: floor((o + n) / U) + 1 >= floor(o / U) +
+// ceil(n / U).  So no prefix sum over the experts, no plan and no look at the
+// counts on the host is needed, and rows / U + experts units hold any split.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace fp4dev {
+
+constexpr int kMaxExperts = 1024;
+
+struct RowRange {
+    int64_t lo, hi;
+};
+
+// Rows of expert e, clamped to the tensor whatever the offsets say.
+__device__ __forceinline__ RowRange expert_rows(const int* offsets, int e, int64_t rows) {
+    int64_t lo = offsets[e], hi = offsets[e + 1];
+    lo = lo < 0 ? 0 : lo > rows ? rows : lo;
+    hi = hi < lo ? lo : hi > rows ? rows : hi;
+    return {lo, hi};
+}
+
+// The expert whose span of 32-row units holds unit p (the last one that
+// starts at or before p; -1 if none does).  Called by whole waves.
+__device__ __forceinline__ int expert_of_unit(const int* offsets, int experts, int64_t rows, int64_t p) {
+    const int lane = threadIdx.x & 63;
+    int n = 0;
+    for (int base = 0; base < experts; base += 64) {
+        const int e = base + lane;
+        bool before = false;
+        if (e < experts) {
+            int64_t lo = offsets[e];
+            lo = lo < 0 ? 0 : lo > rows ? rows : lo;
+            before = lo / 32 + e <= p;
+        }
+        n += __popcll(__ballot(before));
+    }
+    return __builtin_amdgcn_readfirstlane(n) - 1;
+}
+
+}  // namespace fp4dev

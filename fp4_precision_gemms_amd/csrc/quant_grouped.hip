@@ -1,0 +1,165 @@
+// quant_grouped.hip -- MXFP4 quantization of rows grouped by expert, along
+// cols (the operands of the forward and Dgrad products), along rows (those of
+// Wgrad: each expert's tokens in 32-token blocks of their own, the last one
+// filled up with zeros) or both from one read.
+//
+// Bound by HBM like the quantizers without groups, and built the same way: a
+// workgroup takes two consecutive 32-row units x 256 columns, moved global ->
+// LDS by DMA in 512-byte row segments (16-byte chunks swizzled by row mod 4 so
+// that both the column reads and the row reads are free of bank conflicts).
+// A unit's rows belong to one expert (grouped.hpp); rows past its last one are
+// out-of-range loads and read as zero.  Along rows a thread owns a column and
+// its 32 values of the unit, along cols one 32-element block of a row.
+#include "fp4_launch.hpp"
+#include "grouped.hpp"
+#include "mx_device.hpp"
+
+namespace fp4dev {
+namespace {
+
+typedef __attribute__((address_space(3))) void lds_void_t;
+
+constexpr int kCols = 256, kUnits = 2;
+constexpr uint32_t kOob = 0x80000000u;
+
+struct Rotation {
+    uint32_t sign_word;
+    float norm;
+};
+
+// HADN: rotation size along the axis (0 = none); with both outputs it is the
+// rows output's and the cols output is not rotated.
+template <int HADN, bool SR, bool ROWS, bool COLS>
+__global__ __launch_bounds__(kCols) void quant_grouped(
+    const uint16_t* __restrict__ x, const int* __restrict__ offsets, int experts, int64_t rows, int cols,
+    Rotation rot, uint64_t sr_rows, uint64_t sr_cols, uint8_t* __restrict__ codes_r, uint8_t* __restrict__ scales_r,
+    uint8_t* __restrict__ codes_c, uint8_t* __restrict__ scales_c) {
+    __shared__ __attribute__((aligned(1024))) uint16_t tile[kUnits][32 * kCols];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t units = rows / 32 + experts, nbc = cols / 32;
+    const int gx = (cols + kCols - 1) / kCols;
+    const int c0 = (int)(blockIdx.x % gx) * kCols;
+    const int64_t p0 = (int64_t)(blockIdx.x / gx) * kUnits;
+    int64_t r0[kUnits], local[kUnits];
+    int expert[kUnits], left[kUnits];                  // rows of the unit (0: none)
+#pragma unroll
+    for (int t = 0; t < kUnits; ++t) {
+        const int64_t p = p0 + t;
+        left[t] = 0;
+        r0[t] = local[t] = 0;
+        expert[t] = p < units ? expert_of_unit(offsets, experts, rows, p) : -1;
+        if (expert[t] < 0) continue;
+        const RowRange rr = expert_rows(offsets, expert[t], rows);
+        local[t] = p - (rr.lo / 32 + expert[t]);
+        r0[t] = rr.lo + 32 * local[t];
+        left[t] = rr.hi - r0[t] >= 32 ? 32 : rr.hi > r0[t] ? (int)(rr.hi - r0[t]) : 0;
+        left[t] = __builtin_amdgcn_readfirstlane(left[t]);
+    }
+#pragma unroll
+    for (int t = 0; t < kUnits; ++t) {
+        if (left[t] == 0) continue;
+        const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)(x + r0[t] * cols), (short)0, left[t] * cols * 2, 0x00020000);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int j = wave * 4 + k, row = 2 * j + (lane >> 5);
+            const int chunk = (lane & 31) ^ (row & 3);
+            const uint32_t o = (uint32_t)(row * cols + c0) * 2 + chunk * 16;
+            const bool in = row < left[t] && c0 + 8 * chunk < cols;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void_t*)((uint8_t*)tile[t] + j * 1024), 16,
+                                                     in ? o : kOob, 0, 0, 0);
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);                // the DMA has landed
+    __syncthreads();
+    int colpos[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) colpos[q] = (((tid >> 3) ^ q) << 3) | (tid & 7);
+    const int col = c0 + tid;
+#pragma unroll
+    for (int t = 0; t < kUnits; ++t) {
+        if (left[t] == 0) continue;
+        const int64_t p = p0 + t;
+        if constexpr (ROWS) {
+            if (col < cols) {
+                float a[32];
+#pragma unroll
+                for (int r = 0; r < 32; ++r)
+                    a[r] = __uint_as_float((uint32_t)tile[t][r * kCols + colpos[r & 3]] << 16);
+                uint32_t wd[4];
+                const uint64_t g = ((uint64_t)col * (uint64_t)(32 * units) + (uint64_t)(32 * p)) >> 2;
+                const uint32_t byte = quant_block32<HADN, SR>(a, rot.sign_word, rot.norm, sr_rows, g, wd);
+                *reinterpret_cast<uint4*>(codes_r + tiled_offset(col, p, units)) =
+                    make_uint4(wd[0], wd[1], wd[2], wd[3]);
+                const int64_t sg = (r0[t] - 32 * local[t]) / 256 + expert[t] + local[t] / 8;
+                scales_r[(sg * cols + col) * 8 + (local[t] & 7)] = (uint8_t)byte;
+            }
+        }
+        if constexpr (COLS) {
+            const int grp = lane >> 4;
+            const int r = 8 * wave + 4 * (grp & 1) + ((lane >> 2) & 3), b = 4 * (grp >> 1) + (lane & 3);
+            const int64_t cb = c0 + 32 * b;
+            if (r < left[t] && cb < cols) {
+                float a[32];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint4 v =
+                        *reinterpret_cast<const uint4*>(&tile[t][r * kCols + (((4 * b + k) ^ (r & 3)) << 3)]);
+                    a[8 * k + 0] = bf16_lo(v.x); a[8 * k + 1] = bf16_hi(v.x);
+                    a[8 * k + 2] = bf16_lo(v.y); a[8 * k + 3] = bf16_hi(v.y);
+                    a[8 * k + 4] = bf16_lo(v.z); a[8 * k + 5] = bf16_hi(v.z);
+                    a[8 * k + 6] = bf16_lo(v.w); a[8 * k + 7] = bf16_hi(v.w);
+                }
+                uint32_t wd[4];
+                const uint64_t g = ((uint64_t)(r0[t] + r) * (uint64_t)cols + (uint64_t)cb) >> 2;
+                const uint32_t byte =
+                    quant_block32<ROWS ? 0 : HADN, SR>(a, rot.sign_word, rot.norm, sr_cols, g, wd);
+                const int64_t pr = 32 * p + r, blk = cb / 32;
+                *reinterpret_cast<uint4*>(codes_c + tiled_offset(pr, blk, nbc)) =
+                    make_uint4(wd[0], wd[1], wd[2], wd[3]);
+                scales_c[((blk >> 3) * (32 * units) + pr) * 8 + (blk & 7)] = (uint8_t)byte;
+            }
+        }
+    }
+}
+
+template <int HADN, bool SR, bool ROWS, bool COLS>
+hipError_t launch_one(const void* x, const int* offsets, int64_t experts, int64_t rows, int64_t cols, Rotation rot,
+                      uint64_t sr_rows, uint64_t sr_cols, uint8_t* cr, uint8_t* sr, uint8_t* cc, uint8_t* sc,
+                      hipStream_t st) {
+    const int64_t units = rows / 32 + experts;
+    const int64_t blocks = ((cols + kCols - 1) / kCols) * ((units + kUnits - 1) / kUnits);
+    return launch(&quant_grouped<HADN, SR, ROWS, COLS>, dim3((unsigned)blocks), dim3(kCols), st, (const uint16_t*)x,
+                  offsets, (int)experts, rows, (int)cols, rot, sr_rows, sr_cols, cr, sr, cc, sc);
+}
+
+template <int HADN, bool SR, typename... A>
+hipError_t launch_axes(bool r, bool c, A... a) {
+    if (r && c) return launch_one<HADN, SR, true, true>(a...);
+    if (r) return launch_one<HADN, SR, true, false>(a...);
+    return launch_one<HADN, SR, false, true>(a...);
+}
+
+}  // namespace
+
+hipError_t launch_quant_grouped(const void* x, const int* offsets, int64_t experts, int64_t rows, int64_t cols,
+                                int had_n, int had, uint64_t sign_seed, int rnd, uint64_t sr_rows, uint64_t sr_cols,
+                                uint8_t* codes_r, uint8_t* scales_r, uint8_t* codes_c, uint8_t* scales_c,
+                                hipStream_t st) {
+    const bool r = codes_r != nullptr, c = codes_c != nullptr, sr = rnd == 1;
+    const int n = had == 0 ? 0 : had_n;
+    const Rotation rot{host_sign_word(had, sign_seed),
+                       n == 16 ? 0.25f : __builtin_bit_cast(float, 0x3E3504F3u)};   // fl(1 / sqrt(n))
+#define FP4_GROUPED(N)                                                                                             \
+    return sr ? launch_axes<N, true>(r, c, x, offsets, experts, rows, cols, rot, sr_rows, sr_cols, codes_r, scales_r, \
+                                     codes_c, scales_c, st)                                                       \
+              : launch_axes<N, false>(r, c, x, offsets, experts, rows, cols, rot, sr_rows, sr_cols, codes_r, scales_r, \
+                                      codes_c, scales_c, st)
+    if (n == 0) FP4_GROUPED(0);
+    if (n == 16) FP4_GROUPED(16);
+    FP4_GROUPED(32);
+#undef FP4_GROUPED
+}
+
+}  // namespace fp4dev

@@ -393,6 +393,81 @@ fp4_status fp4_rmsnorm_backward(const void* dy_bf16, const void* h_bf16, const v
 /* Workspace bytes fp4_rmsnorm_backward needs for [rows, cols]. */
 size_t fp4_rmsnorm_workspace_bytes(int64_t rows, int64_t cols);
 
+/*
+ * fp4_gemm_decode -- the product of a few activation rows (single tokens,
+ * small batches) with MXFP4 weights: C[m, n] = sum_k a[m, k] w[n, k], fp32
+ * accumulation, C row-major [M, N] in `out` (bf16: the fp32 result rounded to
+ * nearest even).  a / as: an operand of M rows of K elements in `fmt`, as
+ * fp4_rmsnorm_quantize or fp4_hadamard_quantize (AXIS_COLS) writes it; wq / ws:
+ * the weight [N, K] quantized along cols.  It computes what fp4_gemm_mx does
+ * (for MXFP4 activations, up to the order of the fp32 sums) for any M, but is
+ * made for M up to a few dozen, where the weights' bytes are the time.
+ * Requirements: K % 32 == 0 and K < 2^24; M, N < 2^31; pointers 16-byte
+ * aligned.  A scale byte of 0xFF makes its block NaN.
+ */
+fp4_status fp4_gemm_decode(const uint8_t* a, const uint8_t* as, fp4_format fmt, const uint8_t* wq,
+                           const uint8_t* ws, int64_t M, int64_t N, int64_t K, void* c,
+                           fp4_out_dtype out, void* stream);
+
+/*
+ * Rows grouped by expert.  `offsets` (int32 [experts + 1], device memory):
+ * expert e owns rows [offsets[e], offsets[e+1]) of the row-major tensors of
+ * `rows` rows; they must not decrease and stay in [0, rows].  Experts may be
+ * empty.  Rows before offsets[0] or from offsets[experts] on belong to no
+ * expert: they are not read and nothing is written for them.  The offsets are
+ * read on the device only.  (Offsets out of order or of range give unspecified
+ * values, but no access outside the buffers.)
+ *
+ * Quantized rows of `rows` x `cols` elements, U = FP4_GROUPED_UNITS(rows,
+ * experts) = rows / 32 + experts units of 32 rows; expert e starts at unit
+ * offsets[e] / 32 + e (its units never reach the next expert's):
+ *   along cols (forward, Dgrad): an MXFP4 operand of 32 U rows of `cols`
+ *     elements (codes [U][cols/32][512], scales [ceil(cols/256)][32 U][8]);
+ *     row offsets[e] + i is the operand's row 32 (offsets[e] / 32 + e) + i.
+ *   along rows (Wgrad): codes of `cols` rows of 32 U elements
+ *     ([cols/32][U][512]; unit u of expert e, its rows 32 u .. 32 u + 31 with
+ *     zeros past the last one, is block offsets[e] / 32 + e + u) and scales
+ *     [FP4_GROUPED_SCALE_GROUPS(rows, experts)][cols][8] with the byte of that
+ *     unit at group offsets[e] / 256 + e + u / 8, position u % 8.
+ * Units, rows and bytes that belong to no row of an expert are not written.
+ */
+#define FP4_GROUPED_UNITS(rows, experts) ((int64_t)(rows) / 32 + (int64_t)(experts))
+#define FP4_GROUPED_SCALE_GROUPS(rows, experts) ((int64_t)(rows) / 256 + (int64_t)(experts))
+
+/*
+ * fp4_quantize_grouped -- bf16 x[rows, cols] with rows grouped by expert to
+ * MXFP4 along rows (codes_rows, scales_rows), along cols (codes_cols,
+ * scales_cols) or both from one read; the pair that is not wanted is NULL.
+ * Rotation, rounding and scales as fp4_hadamard_quantize on each expert's rows
+ * alone; with both outputs the rotation is the rows output's and the cols
+ * output is not rotated.  Stochastic rounding: element (row, col) of the cols
+ * output has index row * cols + col (row of x), element i of unit p of column
+ * col of the rows output index col * 32 U + 32 p + i.
+ * Requirements: cols % 32 == 0, cols < 2^24; 0 < rows < 2^31; 1 <= experts <=
+ * 1024; pointers 16-byte aligned (offsets 4).
+ */
+fp4_status fp4_quantize_grouped(const void* x_bf16, const int32_t* offsets, int64_t experts,
+                                int64_t rows, int64_t cols, int had_n, fp4_hadamard had,
+                                uint64_t sign_seed, fp4_rounding rnd, uint64_t sr_seed_rows,
+                                uint64_t sr_seed_cols, uint8_t* codes_rows, uint8_t* scales_rows,
+                                uint8_t* codes_cols, uint8_t* scales_cols, void* stream);
+
+/*
+ * fp4_gemm_grouped -- each expert's rows times its weight:
+ *   C[r, n] = sum_k a[r, k] w_e[n, k] for every row r of expert e.
+ * a / as: MXFP4 as fp4_quantize_grouped writes along cols, or MXFP8 row-major
+ * [rows, K] / [rows, K/32] (as fp4_rmsnorm_quantize writes; no units).  wq /
+ * ws: the experts' weights [N, K], one quantized operand after another
+ * (FP4_CODE_BYTES(N, K) and FP4_SCALE_BYTES(N, K) bytes each).  C row-major
+ * [rows, N] in `out`; rows of no expert are left as they were.  The forward
+ * product takes W along cols; Dgrad is the same call with dY and W^T (W along
+ * rows).  Requirements as for fp4_gemm_decode and fp4_quantize_grouped.
+ */
+fp4_status fp4_gemm_grouped(const uint8_t* a, const uint8_t* as, fp4_format fmt,
+                            const int32_t* offsets, int64_t experts, int64_t rows,
+                            const uint8_t* wq, const uint8_t* ws, int64_t N, int64_t K, void* c,
+                            fp4_out_dtype out, void* stream);
+
 /* Static, NUL-terminated name of a status code. */
 const char* fp4_status_string(fp4_status status);
 

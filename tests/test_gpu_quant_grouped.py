@@ -1,0 +1,89 @@
+"""fp4_quantize_grouped bit for bit against the oracle on the padded layout:
+the experts' rows at their units, zeros between them."""
+import numpy as np
+import pytest
+import torch
+
+import fp4_precision_gemms_amd as F
+import oracle as O
+from _grouped import SPLITS, dev_offsets, padded_rows
+from _util import bf16_bits, need_gpu, say, sentinel_u8, to_gpu_bf16, ungroup_scales, untile_codes
+
+pytestmark = pytest.mark.gpu
+
+MODES = {"plain": (32, F.HAD_NONE, 0, F.RTN), "had32": (32, F.HAD_DET, 0, F.RTN),
+         "had16 signed": (16, F.HAD_SIGNED, 99, F.RTN), "sr": (32, F.HAD_NONE, 0, F.SR),
+         "had16 sr": (16, F.HAD_DET, 0, F.SR), "had32 sr": (32, F.HAD_SIGNED, 5, F.SR)}
+
+
+def check_rows(codes, scales, bits, rows, offsets, mode, seed):
+    """Every written byte of the rows output; every other byte still 0xCD."""
+    had_n, had, sign_seed, rnd = mode
+    at, units = padded_rows(rows, offsets)
+    full = np.zeros((32 * units, bits.shape[1]), np.uint16)
+    full[at[at >= 0]] = bits[at >= 0]
+    rc, rs = O.quant_mx(full, O.AXIS_ROWS, had_n, had, sign_seed, rnd, seed)
+    C = bits.shape[1]
+    used = np.unique(at[at >= 0] // 32)
+    want = np.full((C, units, 16), 0xCD, np.uint8)
+    want[:, used] = rc.reshape(C, units, 16)[:, used]
+    assert np.array_equal(untile_codes(codes.cpu().numpy(), C).reshape(C, units, 16), want)
+    ws = np.full(tuple(scales.shape), 0xCD, np.uint8)
+    for e, (lo, hi) in enumerate(zip(offsets, offsets[1:])):
+        for u in range((hi - lo + 31) // 32):
+            ws[lo // 256 + e + u // 8, :, u % 8] = rs[:, lo // 32 + e + u]
+    assert np.array_equal(scales.cpu().numpy(), ws)
+
+
+def check_cols(codes, scales, bits, rows, offsets, mode, seed):
+    had_n, had, sign_seed, rnd = mode
+    at, units = padded_rows(rows, offsets)
+    rc, rs = O.quant_mx(bits, O.AXIS_COLS, had_n, had, sign_seed, rnd, seed)
+    nb = bits.shape[1] // 32
+    want, ws = np.full((32 * units, 16 * nb), 0xCD, np.uint8), np.full((32 * units, nb), 0xCD, np.uint8)
+    want[at[at >= 0]], ws[at[at >= 0]] = rc[at >= 0], rs[at >= 0]
+    assert np.array_equal(untile_codes(codes.cpu().numpy(), 32 * units), want)
+    assert np.array_equal(ungroup_scales(scales.cpu().numpy(), nb), ws)
+
+
+def out(rows, cols, E, *axes):
+    return [sentinel_u8(s) for a in axes for s in F.grouped_shapes(rows, cols, E, a)]
+
+
+@pytest.mark.parametrize("split", list(SPLITS))
+@pytest.mark.parametrize("mode", list(MODES))
+def test_grouped_quantizers(split, mode):
+    need_gpu()
+    rows, offsets = SPLITS[split]
+    E, m = len(offsets) - 1, MODES[mode]
+    for cols in (32, 288):
+        say("quantize grouped", split, mode, cols)
+        rng = np.random.default_rng(rows + cols)
+        bits = bf16_bits(rng.standard_t(4, (rows, cols)))
+        x, off = to_gpu_bf16(bits), dev_offsets(offsets)
+        got = F.fp4_quantize_grouped(x, off, F.AXIS_ROWS, *m, sr_seed=11, out=out(rows, cols, E, F.AXIS_ROWS))
+        torch.cuda.synchronize()
+        check_rows(*got, bits, rows, offsets, m, 11)
+        got = F.fp4_quantize_grouped(x, off, F.AXIS_COLS, *m, sr_seed=12, out=out(rows, cols, E, F.AXIS_COLS))
+        torch.cuda.synchronize()
+        check_cols(*got, bits, rows, offsets, m, 12)
+        got = F.fp4_quantize_grouped_dual(x, off, *m, sr_seed_rows=13, sr_seed_cols=14,
+                                          out=out(rows, cols, E, F.AXIS_ROWS, F.AXIS_COLS))
+        torch.cuda.synchronize()
+        check_rows(*got[:2], bits, rows, offsets, m, 13)
+        check_cols(*got[2:], bits, rows, offsets, (32, F.HAD_NONE, 0, m[3]), 14)
+
+
+def test_non_finite_values():
+    need_gpu()
+    rows, offsets = SPLITS["odd"]
+    rng = np.random.default_rng(0)
+    v = rng.standard_normal((rows, 64)).astype(np.float32)
+    v[3, 5], v[40, 33], v[150] = np.nan, np.inf, 0
+    bits = bf16_bits(v)
+    m = MODES["plain"]
+    got = F.fp4_quantize_grouped_dual(to_gpu_bf16(bits), dev_offsets(offsets),
+                                      out=out(rows, 64, len(offsets) - 1, F.AXIS_ROWS, F.AXIS_COLS))
+    torch.cuda.synchronize()
+    check_rows(*got[:2], bits, rows, offsets, m, 0)
+    check_cols(*got[2:], bits, rows, offsets, m, 0)
