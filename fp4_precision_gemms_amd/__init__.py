@@ -78,6 +78,8 @@ def lib() -> ctypes.CDLL:
     L.fp4_quantize_grouped.restype = i32
     L.fp4_gemm_grouped.argtypes = [vp, vp, i32, vp, i64, i64, vp, vp, i64, i64, vp, i32, vp]
     L.fp4_gemm_grouped.restype = i32
+    L.fp4_gemm_grouped_wgrad.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, i32, vp]
+    L.fp4_gemm_grouped_wgrad.restype = i32
     L.fp4_status_string.argtypes = [i32]
     L.fp4_status_string.restype = ctypes.c_char_p
     _lib = L
@@ -576,6 +578,25 @@ def fp4_gemm_grouped(aq: torch.Tensor, as_: torch.Tensor, offsets: torch.Tensor,
     out = _product_out(out, (rows, N), out_dtype, dev)
     _call(lib().fp4_gemm_grouped, dev, stream, aq.data_ptr(), as_.data_ptr(), fmt, offsets.data_ptr(), experts, rows,
           wq.data_ptr(), ws.data_ptr(), N, K, out.data_ptr(), out_dtype)
+    return out
+
+
+def fp4_gemm_grouped_wgrad(dytq: torch.Tensor, dyts: torch.Tensor, xtq: torch.Tensor, xts: torch.Tensor,
+                           offsets: torch.Tensor, rows: int, out: torch.Tensor | None = None,
+                           out_dtype: int = OUT_BF16, stream=None):
+    """dw[experts, N, K] = each expert's dY^T X from dY [rows, N] and X
+    [rows, K] quantized along rows by fp4_quantize_grouped with these offsets
+    (see include/fp4.h)."""
+    dev = dytq.device
+    experts = _offsets(offsets, dev)
+    N, K = dyts.shape[1], xts.shape[1]
+    for q, s, c, n in ((dytq, dyts, N, "dY"), (xtq, xts, K, "X")):
+        shapes = grouped_shapes(rows, c, experts, AXIS_ROWS)
+        _need_on(q, torch.uint8, shapes[0], dev, n + " codes")
+        _need_on(s, torch.uint8, shapes[1], dev, n + " scales")
+    out = _product_out(out, (experts, N, K), out_dtype, dev)
+    _call(lib().fp4_gemm_grouped_wgrad, dev, stream, dytq.data_ptr(), dyts.data_ptr(), xtq.data_ptr(), xts.data_ptr(),
+          offsets.data_ptr(), experts, rows, N, K, out.data_ptr(), out_dtype)
     return out
 
 

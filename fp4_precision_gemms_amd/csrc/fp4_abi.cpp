@@ -248,7 +248,8 @@ fp4_status check_grouped_product(const uint8_t* a, const uint8_t* as, fp4_format
     if (rows <= 0 || N <= 0 || K <= 0 || K % 32 || K >= kMaxContraction || rows > INT32_MAX || N > INT32_MAX ||
         experts <= 0 || experts > kMaxExperts)
         return FP4_ERR_SHAPE;
-    if (!product_ok(rows + 32 * experts, K) || !product_ok(N * experts, K) || !product_ok(rows, N))
+    if (!product_ok(rows + 32 * experts, K) || !product_ok(N * experts, K) || !product_ok(rows, N) ||
+        (rows / 128 + experts) * ((N + 255) / 256) >= kMaxTiles)
         return FP4_ERR_SHAPE;
     if (!aligned16(a) || !aligned16(as) || !aligned16(wq) || !aligned16(ws) || !aligned16(c)) return FP4_ERR_ALIGN;
     return FP4_OK;
@@ -290,8 +291,29 @@ fp4_status fp4_gemm_grouped(const uint8_t* a, const uint8_t* as, fp4_format fmt,
     if (!offsets) return FP4_ERR_NULL;
     if (const fp4_status s = check_grouped_product(a, as, fmt, wq, ws, experts, rows, N, K, c, out)) return s;
     if (!aligned4(offsets)) return FP4_ERR_ALIGN;
+    if (fmt == FP4_FMT_MXFP4 && fp4dev::many_rows(rows, experts))
+        return from_hip(fp4dev::launch_gemm_row_groups(a, as, offsets, experts, rows, wq, ws, N, K, c,
+                                                       out == FP4_OUT_BF16, (hipStream_t)stream));
     return from_hip(fp4dev::launch_gemm_few(a, as, fmt == FP4_FMT_MXFP8, offsets, wq, ws, rows, experts, N, K, c,
                                             out == FP4_OUT_BF16, (hipStream_t)stream));
+}
+
+fp4_status fp4_gemm_grouped_wgrad(const uint8_t* dytq, const uint8_t* dyts, const uint8_t* xtq,
+                                  const uint8_t* xts, const int32_t* offsets, int64_t experts, int64_t rows,
+                                  int64_t N, int64_t K, void* dw, fp4_out_dtype out, void* stream) {
+    if (out != FP4_OUT_F32 && out != FP4_OUT_BF16) return FP4_ERR_ENUM;
+    if (!dytq || !dyts || !xtq || !xts || !offsets || !dw) return FP4_ERR_NULL;
+    if (rows <= 0 || N <= 0 || K <= 0 || N % 32 || K % 32 || rows > INT32_MAX || N > INT32_MAX || K > INT32_MAX ||
+        experts <= 0 || experts > kMaxExperts || 32 * (rows / 32 + experts) >= kMaxContraction)
+        return FP4_ERR_SHAPE;
+    if (!product_ok(N, K) || !product_ok(N * K, experts) ||
+        ((N + 255) / 256) * ((K + 255) / 256) >= kMaxTiles / experts)
+        return FP4_ERR_SHAPE;
+    if (!aligned16(dytq) || !aligned16(dyts) || !aligned16(xtq) || !aligned16(xts) || !aligned4(offsets) ||
+        !aligned16(dw))
+        return FP4_ERR_ALIGN;
+    return from_hip(fp4dev::launch_gemm_depth_groups(dytq, dyts, xtq, xts, offsets, experts, rows, N, K, dw,
+                                                     out == FP4_OUT_BF16, (hipStream_t)stream));
 }
 
 const char* fp4_status_string(fp4_status status) {

@@ -52,6 +52,7 @@
 //     the tile boundaries of the 256 workgroups do not coincide.
 #include "fp4_device.hpp"
 #include "fp4_launch.hpp"
+#include "grouped.hpp"
 
 #include <atomic>
 
@@ -160,11 +161,32 @@ constexpr int kEpiRegion = 32 * kEpiRow;        // 32 rows per wave
 // the ring), so no lane ever reads out of range; the prefetches past the
 // last stage re-load the last stage (never read) and each stage's offset is
 // a scalar added to per-tile descriptors.
-template <int FM, int GM, bool FAST, bool KTAIL, bool OBF16, bool ACC>
-__global__ __launch_bounds__(kThreads) void gemm_mx_tn(
+//
+// GROUP (grouped.hpp): kRowGroups -- the rows of A and C belong to experts, each
+// with a B of its own; M is the row count of A's grouped layout, a tile never
+// crosses into the next expert, and FAST's full tiles hold for the columns and
+// the contraction only.  kDepthGroups -- each expert owns a span of the
+// contraction and an output [M, N] of its own (KTAIL: spans end anywhere).
+enum { kNoGroups = 0, kRowGroups = 1, kDepthGroups = 2 };
+
+struct GroupArgs {
+    const int* offsets;
+    int experts;
+    int64_t rows;         // of the tensor that the offsets split
+};
+
+// One int per expert in LDS; Which tells several arrays apart.
+template <int Which>
+__device__ __forceinline__ int* expert_ints() {
+    __shared__ int v[kMaxExperts];
+    return v;
+}
+
+template <int FM, int GM, bool FAST, bool KTAIL, bool OBF16, bool ACC, int GROUP>
+__device__ __forceinline__ void gemm_tiles(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ SA, const uint8_t* __restrict__ B,
     const uint8_t* __restrict__ SB, int64_t M, int64_t N, int64_t K, void* __restrict__ C,
-    int tiles_m, int tiles_n) {
+    int tiles_m, int tiles_n, const GroupArgs ga) {
     constexpr int BM = 32 * FM, FN = 2;
     constexpr int kACodes = FM * 4096;                 // FM row groups x 8 chunks of 512 B
     constexpr int kAScales = 2048;                     // 8 scale DMAs of 32 rows x 8 B
@@ -190,14 +212,56 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_tn(
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // wave-uniform
     const int h = lane >> 5, l32 = lane & 31;
-    const int ntiles = tiles_m * tiles_n;
-    const int64_t nb = K / 32;                         // blocks per row
-    const int nks = (int)((nb + 1) / 2);               // MFMA k-steps (K < 2^24)
-    const int nk = (int)((nb + 7) / 8);                // 256-k stages
+    int ntiles = tiles_m * tiles_n;
+    int64_t nb = K / 32;                               // blocks per row
+    int nks = (int)((nb + 1) / 2);                     // MFMA k-steps (K < 2^24)
+    int nk = (int)((nb + 7) / 8);                      // 256-k stages
     // leading all-zero stages round the stage count up to a multiple of the
     // ring (the loop below handles four stages per iteration)
-    const int kfirst = -((kSlots - nk % kSlots) % kSlots);
+    int kfirst = -((kSlots - nk % kSlots) % kSlots);
     const uint32_t gstride = (uint32_t)(nb * 512);     // bytes per 32-row group of codes
+    if constexpr (GROUP == kRowGroups) {
+        // the experts' row tiles, counted up: ends[e] of them belong to
+        // experts 0 .. e
+        int* const los = expert_ints<0>();
+        int* const his = expert_ints<1>();
+        int* const ends = expert_ints<2>();
+        if (wave == 0) {
+            int before = 0;
+            for (int base = 0; base < ga.experts; base += 64) {
+                const int e = base + lane;
+                int n = 0;
+                if (e < ga.experts) {
+                    const RowRange r = expert_rows(ga.offsets, e, ga.rows);
+                    los[e] = (int)r.lo;
+                    his[e] = (int)r.hi;
+                    n = (int)((r.hi - r.lo + BM - 1) / BM);
+                }
+#pragma unroll
+                for (int o = 1; o < 64; o <<= 1) {
+                    const int v = __shfl_up(n, o);
+                    if (lane >= o) n += v;
+                }
+                n += before;
+                if (e < ga.experts) ends[e] = n;
+                before = __shfl(n, 63);
+            }
+        }
+        __syncthreads();
+        tiles_m = __builtin_amdgcn_readfirstlane(ends[ga.experts - 1]);
+        ntiles = tiles_m * tiles_n;
+        if ((int)blockIdx.x >= ntiles) return;
+    } else if constexpr (GROUP == kDepthGroups) {
+        int* const los = expert_ints<0>();
+        int* const his = expert_ints<1>();
+        for (int e = tid; e < ga.experts; e += kThreads) {
+            const RowRange r = expert_rows(ga.offsets, e, ga.rows);
+            los[e] = (int)r.lo;
+            his[e] = (int)r.hi;
+        }
+        __syncthreads();
+        ntiles *= ga.experts;
+    }
 
     // Per-lane parts of the buffer offsets (the stage / k-step part goes in
     // the scalar offset): A chunk d of this wave's k-step (wave) of a stage,
@@ -208,9 +272,14 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_tn(
 #pragma unroll
     for (int j = 0; j < FN; ++j) offb[j] = (uint32_t)(2 * wave + j) * gstride + (uint32_t)lane * 16;
     // the upper half of a k-step past the last block (nb odd) reads zero
-    const bool half_tail = KTAIL && (nb & 1) && h == 1;
+    bool half_tail = KTAIL && (nb & 1) && h == 1;
 
     int64_t m0 = 0, n0 = 0, rows_a = 0, rows_b = 0;
+    // the tile's first row in C, and what comes before its expert's output
+    int64_t c0 = 0, cbase = 0;
+    // per-expert parts of the scale addresses
+    const uint8_t* sa_tile = SA;
+    const uint8_t* sb_tile = SB;
     __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)A, (short)0, 0, kBufferWord3);
     __amdgpu_buffer_rsrc_t rb = ra, rsa = ra, rsb = ra;   // rsa, rsb: FAST scale descriptors
     // FAST: lane parts of the scale offsets (A: 16 bytes of this wave's
@@ -221,24 +290,73 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_tn(
     for (int j = 0; j < FN; ++j) offsb[j] = (uint32_t)((64 * wave + 32 * j + l32) * 8);
     auto set_tile = [&](int t) {
         int tile_m, tile_n;
-        tile_of_block<GM>(t, ntiles, tiles_m, tiles_n, tile_m, tile_n);
+        int e = 0;
+        if constexpr (GROUP == kDepthGroups) {
+            // experts one after another; an expert's tiles spread over all XCDs
+            const int per = tiles_m * tiles_n;
+            e = t / per;
+            tile_of_block<GM>(t - e * per, per, tiles_m, tiles_n, tile_m, tile_n);
+        } else {
+            tile_of_block<GM>(t, ntiles, tiles_m, tiles_n, tile_m, tile_n);
+        }
         tile_m = __builtin_amdgcn_readfirstlane(tile_m);
         tile_n = __builtin_amdgcn_readfirstlane(tile_n);
         m0 = (int64_t)tile_m * BM;
         n0 = (int64_t)tile_n * kBN;
         rows_a = (M - m0) < BM ? (M - m0) : BM;
         rows_b = (N - n0) < kBN ? (N - n0) : kBN;
+        c0 = m0;
+        if constexpr (GROUP == kRowGroups) {
+            const int* const ends = expert_ints<2>();
+            for (int base = 0; base < ga.experts; base += 64)
+                e += __popcll(__ballot(base + lane < ga.experts && ends[base + lane] <= tile_m));
+            e = __builtin_amdgcn_readfirstlane(e);
+            const int first = e ? __builtin_amdgcn_readfirstlane(ends[e - 1]) : 0;
+            const int lo = __builtin_amdgcn_readfirstlane(expert_ints<0>()[e]);
+            const int hi = __builtin_amdgcn_readfirstlane(expert_ints<1>()[e]);
+            const int64_t local = (int64_t)(tile_m - first) * BM;
+            m0 = 32 * ((int64_t)lo / 32 + e) + local;
+            c0 = lo + local;
+            rows_a = (hi - c0) < BM ? (hi - c0) : BM;
+            ra = __builtin_amdgcn_make_buffer_rsrc((void*)(A + (m0 / 32) * (int64_t)gstride), (short)0,
+                                                   (int)(((rows_a + 31) / 32) * (int64_t)gstride), kBufferWord3);
+            const int64_t groups = (N + 31) / 32;      // of an expert's B
+            rb = __builtin_amdgcn_make_buffer_rsrc((void*)(B + (e * groups + n0 / 32) * (int64_t)gstride), (short)0,
+                                                   (int)(((rows_b + 31) / 32) * (int64_t)gstride), kBufferWord3);
+            sb_tile = SB + (int64_t)e * nk * N * 8;
+        } else if constexpr (GROUP == kDepthGroups) {
+            e = __builtin_amdgcn_readfirstlane(e);
+            const int lo = __builtin_amdgcn_readfirstlane(expert_ints<0>()[e]);
+            const int hi = __builtin_amdgcn_readfirstlane(expert_ints<1>()[e]);
+            nb = (hi - lo + 31) / 32;
+            nks = (int)((nb + 1) / 2);
+            nk = (int)((nb + 7) / 8);
+            kfirst = -((kSlots - nk % kSlots) % kSlots);
+            half_tail = KTAIL && (nb & 1) && h == 1;
+            const int64_t b0 = lo / 32 + e, q0 = lo / 256 + e;
+            cbase = (int64_t)e * M * N;
+            sa_tile = SA + q0 * M * 8;
+            sb_tile = SB + q0 * N * 8;
+            // an expert's span of each 32-row group: up to its last block
+            ra = __builtin_amdgcn_make_buffer_rsrc(
+                (void*)(A + (m0 / 32) * (int64_t)gstride + b0 * 512), (short)0,
+                (int)(((rows_a + 31) / 32 - 1) * (int64_t)gstride + nb * 512), kBufferWord3);
+            rb = __builtin_amdgcn_make_buffer_rsrc(
+                (void*)(B + (n0 / 32) * (int64_t)gstride + b0 * 512), (short)0,
+                (int)(((rows_b + 31) / 32 - 1) * (int64_t)gstride + nb * 512), kBufferWord3);
+        } else {
         // the tile's row groups of each operand; groups past the operand's
         // last one are out of range and read as zero
         ra = __builtin_amdgcn_make_buffer_rsrc((void*)(A + (m0 / 32) * (int64_t)gstride), (short)0,
                                                (int)(((rows_a + 31) / 32) * (int64_t)gstride), kBufferWord3);
         rb = __builtin_amdgcn_make_buffer_rsrc((void*)(B + (n0 / 32) * (int64_t)gstride), (short)0,
                                                (int)(((rows_b + 31) / 32) * (int64_t)gstride), kBufferWord3);
+        }
         if constexpr (FAST) {
             // stage q of the tile's rows starts q R 8 bytes further on
-            rsa = __builtin_amdgcn_make_buffer_rsrc((void*)(SA + m0 * 8), (short)0,
+            rsa = __builtin_amdgcn_make_buffer_rsrc((void*)(sa_tile + m0 * 8), (short)0,
                                                     (int)(((int64_t)nk * M - m0) * 8), kBufferWord3);
-            rsb = __builtin_amdgcn_make_buffer_rsrc((void*)(SB + n0 * 8), (short)0,
+            rsb = __builtin_amdgcn_make_buffer_rsrc((void*)(sb_tile + n0 * 8), (short)0,
                                                     (int)(((int64_t)nk * N - n0) * 8), kBufferWord3);
         }
     };
@@ -280,7 +398,7 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_tn(
         if (scales) {
             const int64_t q = zero ? 0 : kt;
             const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-                (void*)(SA + (q * M + m0) * 8), (short)0, (int)(rows_a * 8), kBufferWord3);
+                (void*)(sa_tile + (q * M + m0) * 8), (short)0, (int)(rows_a * 8), kBufferWord3);
             const uint32_t zoob = zero ? kOob : 0u;
             dma4_to_lds(rs, slot + kACodes + wave * 256, (uint32_t)(wave * 256 + lane * 4) | zoob, 0);
             dma4_to_lds(rs, slot + kACodes + (wave + 4) * 256,
@@ -318,7 +436,7 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_tn(
         const bool zero = kt < 0 || kt >= nk;
         const int64_t q = zero ? 0 : kt;
         const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-            (void*)(SB + (q * N + n0) * 8), (short)0, (int)(rows_b * 8), kBufferWord3);
+            (void*)(sb_tile + (q * N + n0) * 8), (short)0, (int)(rows_b * 8), kBufferWord3);
         BSc r;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
@@ -523,7 +641,7 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_tn(
     for (int t = blockIdx.x; t < ntiles; t += gridDim.x) {
         // (an accumulating fast-path launch issues no prologue during its
         // epilogues, which read C: its later tiles take theirs here)
-        if ((!FAST || ACC) && !early) {
+        if ((!FAST || ACC || GROUP == kRowGroups) && !early) {
             if (t != (int)blockIdx.x) {
                 // every wave is done with the previous tile's LDS before it is refilled
                 __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
@@ -560,13 +678,15 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_tn(
         // refilled (and before the workgroup goes away)
         __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
         __syncthreads();                                // all fragment reads of the tile are done
-        const int64_t em0 = m0, en0 = n0;               // the tile the epilogue writes
+        // the tile the epilogue writes: rows em0 .. em0 + erows - 1 of C
+        const int64_t em0 = c0, en0 = n0, ebase = cbase, erows = rows_a;
         const bool vec_store = (N % 4) == 0;
         // workgroup-uniform; constant on the fast path, whose tiles are all
         // full: the epilogue then has no partial-tile branch, whose zero-store
         // path made the compiler wait for most of these stores before the
         // next tile's first fragment moves
-        const bool full_tile = FAST || (vec_store && em0 + BM <= M && en0 + kBN <= N);
+        const bool full_tile = GROUP == kRowGroups ? (FAST || (vec_store && en0 + kBN <= N)) && erows == BM
+                                                   : FAST || (vec_store && em0 + BM <= M && en0 + kBN <= N);
         early = false;
         if constexpr (!KTAIL && !ACC) {
             // The next tile's first stages go out now, into slots 0..2 (this
@@ -612,7 +732,7 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_tn(
                     const int64_t n = en0 + 64 * wave + c4;
                     float v[4] = {f[k].x, f[k].y, f[k].z, f[k].w};
                     if constexpr (OBF16) {
-                        uint2* p = reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(C) + m * N + n);
+                        uint2* p = reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(C) + ebase + m * N + n);
                         if constexpr (ACC) {
                             const uint2 o = *p;
                             v[0] += bf16_value(o.x & 0xFFFFu); v[1] += bf16_value(o.x >> 16);
@@ -621,7 +741,7 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_tn(
                         *p = make_uint2(bf16_rne(v[0]) | (bf16_rne(v[1]) << 16),
                                         bf16_rne(v[2]) | (bf16_rne(v[3]) << 16));
                     } else {
-                        float* p = reinterpret_cast<float*>(C) + m * N + n;
+                        float* p = reinterpret_cast<float*>(C) + ebase + m * N + n;
                         if constexpr (ACC) {
                             const float4 o = *reinterpret_cast<const float4*>(p);
                             v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
@@ -636,10 +756,10 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_tn(
                 const int row = 4 * k + lr;
                 const float4 f = *reinterpret_cast<const float4*>(reg + row * kEpiRow + c4 * 4);
                 const int64_t m = em0 + i * 32 + row, n = en0 + 64 * wave + c4;
-                if (m >= M || n >= N) continue;
+                if ((GROUP ? m >= em0 + erows : m >= M) || n >= N) continue;
                 float v[4] = {f.x, f.y, f.z, f.w};
                 if constexpr (OBF16) {
-                    uint16_t* crow = reinterpret_cast<uint16_t*>(C) + m * N;
+                    uint16_t* crow = reinterpret_cast<uint16_t*>(C) + ebase + m * N;
                     if (vec_store && n + 4 <= N) {
                         uint2* p = reinterpret_cast<uint2*>(crow + n);
                         if constexpr (ACC) {
@@ -657,7 +777,7 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_tn(
                         }
                     }
                 } else {
-                    float* crow = reinterpret_cast<float*>(C) + m * N;
+                    float* crow = reinterpret_cast<float*>(C) + ebase + m * N;
                     if (vec_store && n + 4 <= N) {
                         if constexpr (ACC) {
                             const float4 o = *reinterpret_cast<const float4*>(crow + n);
@@ -674,6 +794,22 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_tn(
             }
         }
     }
+}
+
+template <int FM, int GM, bool FAST, bool KTAIL, bool OBF16, bool ACC>
+__global__ __launch_bounds__(kThreads) void gemm_mx_tn(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ SA, const uint8_t* __restrict__ B,
+    const uint8_t* __restrict__ SB, int64_t M, int64_t N, int64_t K, void* __restrict__ C,
+    int tiles_m, int tiles_n) {
+    gemm_tiles<FM, GM, FAST, KTAIL, OBF16, ACC, kNoGroups>(A, SA, B, SB, M, N, K, C, tiles_m, tiles_n, GroupArgs{});
+}
+
+template <int FM, int GM, bool FAST, bool KTAIL, bool OBF16, int GROUP>
+__global__ __launch_bounds__(kThreads) void gemm_mx_grouped(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ SA, const uint8_t* __restrict__ B,
+    const uint8_t* __restrict__ SB, int64_t M, int64_t N, int64_t K, void* __restrict__ C,
+    int tiles_m, int tiles_n, const GroupArgs ga) {
+    gemm_tiles<FM, GM, FAST, KTAIL, OBF16, false, GROUP>(A, SA, B, SB, M, N, K, C, tiles_m, tiles_n, ga);
 }
 
 // Compute units of each device, queried once per device (concurrent first
@@ -749,6 +885,50 @@ hipError_t launch_gemm_mx(const uint8_t* aq, const uint8_t* as, const uint8_t* b
     };
     if (cost(224) < cost(256)) return launch_out<7>(aq, as, bq, bs, M, N, K, c, out_bf16, accumulate, st);
     return launch_out<8>(aq, as, bq, bs, M, N, K, c, out_bf16, accumulate, st);
+}
+
+namespace {
+template <int FM, bool FAST, bool KTAIL, int GROUP>
+hipError_t launch_grouped(const uint8_t* aq, const uint8_t* as, const uint8_t* bq, const uint8_t* bs, int64_t M,
+                          int64_t N, int64_t K, void* c, int out_bf16, int64_t most, int64_t tm, int64_t tn,
+                          const GroupArgs& ga, hipStream_t st) {
+    const int64_t cus = cu_count();
+    const dim3 grid((unsigned)(most < cus ? most : cus));
+    return out_bf16 ? launch(&gemm_mx_grouped<FM, kGroupRows, FAST, KTAIL, true, GROUP>, grid, dim3(kThreads), st, aq,
+                             as, bq, bs, M, N, K, c, (int)tm, (int)tn, ga)
+                    : launch(&gemm_mx_grouped<FM, kGroupRows, FAST, KTAIL, false, GROUP>, grid, dim3(kThreads), st, aq,
+                             as, bq, bs, M, N, K, c, (int)tm, (int)tn, ga);
+}
+
+template <int FM>
+hipError_t launch_row_groups(const uint8_t* aq, const uint8_t* as, const int* offsets, int64_t experts, int64_t rows,
+                             const uint8_t* wq, const uint8_t* ws, int64_t N, int64_t K, void* c, int out_bf16,
+                             hipStream_t st) {
+    const int64_t M = 32 * (rows / 32 + experts), tn = (N + kBN - 1) / kBN;
+    const int64_t most = (rows / (32 * FM) + experts) * tn;     // tiles of any split, at most
+    const GroupArgs ga{offsets, (int)experts, rows};
+    const bool fast = N % kBN == 0 && K % 1024 == 0 && (K / 256) * (M > N ? M : N) * 8 < (INT64_C(1) << 31);
+    if (fast)
+        return launch_grouped<FM, true, false, kRowGroups>(aq, as, wq, ws, M, N, K, c, out_bf16, most, 0, tn, ga, st);
+    if (K % 256 == 0)
+        return launch_grouped<FM, false, false, kRowGroups>(aq, as, wq, ws, M, N, K, c, out_bf16, most, 0, tn, ga, st);
+    return launch_grouped<FM, false, true, kRowGroups>(aq, as, wq, ws, M, N, K, c, out_bf16, most, 0, tn, ga, st);
+}
+}  // namespace
+
+hipError_t launch_gemm_row_groups(const uint8_t* aq, const uint8_t* as, const int* offsets, int64_t experts,
+                                  int64_t rows, const uint8_t* wq, const uint8_t* ws, int64_t N, int64_t K, void* c,
+                                  int out_bf16, hipStream_t st) {
+    return launch_row_groups<8>(aq, as, offsets, experts, rows, wq, ws, N, K, c, out_bf16, st);
+}
+
+hipError_t launch_gemm_depth_groups(const uint8_t* aq, const uint8_t* as, const uint8_t* bq, const uint8_t* bs,
+                                    const int* offsets, int64_t experts, int64_t rows, int64_t M, int64_t N, void* c,
+                                    int out_bf16, hipStream_t st) {
+    const int64_t K = 32 * (rows / 32 + experts);               // of the grouped layout
+    const int64_t tm = (M + 255) / 256, tn = (N + kBN - 1) / kBN;
+    return launch_grouped<8, false, true, kDepthGroups>(aq, as, bq, bs, M, N, K, c, out_bf16, tm * tn * experts, tm,
+                                                        tn, GroupArgs{offsets, (int)experts, rows}, st);
 }
 
 }  // namespace fp4dev

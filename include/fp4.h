@@ -402,8 +402,9 @@ size_t fp4_rmsnorm_workspace_bytes(int64_t rows, int64_t cols);
  * the weight [N, K] quantized along cols.  It computes what fp4_gemm_mx does
  * (for MXFP4 activations, up to the order of the fp32 sums) for any M, but is
  * made for M up to a few dozen, where the weights' bytes are the time.
- * Requirements: K % 32 == 0 and K < 2^24; M, N < 2^31; pointers 16-byte
- * aligned.  A scale byte of 0xFF makes its block NaN.
+ * Requirements: K % 32 == 0 and K < 2^24; M, N < 2^31; fewer than 2^24 tiles
+ * of 128 x 256 outputs; pointers 16-byte aligned.  A scale byte of 0xFF makes
+ * its block NaN.
  */
 fp4_status fp4_gemm_decode(const uint8_t* a, const uint8_t* as, fp4_format fmt, const uint8_t* wq,
                            const uint8_t* ws, int64_t M, int64_t N, int64_t K, void* c,
@@ -467,6 +468,21 @@ fp4_status fp4_gemm_grouped(const uint8_t* a, const uint8_t* as, fp4_format fmt,
                             const int32_t* offsets, int64_t experts, int64_t rows,
                             const uint8_t* wq, const uint8_t* ws, int64_t N, int64_t K, void* c,
                             fp4_out_dtype out, void* stream);
+
+/*
+ * fp4_gemm_grouped_wgrad -- each expert's weight gradient,
+ *   dW_e[n, k] = sum over the rows r of expert e of dY[r, n] X[r, k],
+ * from dY [rows, N] and X [rows, K] quantized along rows by
+ * fp4_quantize_grouped with the same offsets, had, had_n and sign_seed.  dw is
+ * [experts, N, K] in `out`, overwritten; that of an expert without rows is zero.
+ * Requirements: N % 32 == 0, K % 32 == 0 (the quantizer's); 32 (rows / 32 +
+ * experts) < 2^24; at most 2^24 - 1 output tiles of 256 x 256; pointers 16-byte
+ * aligned (offsets 4).
+ */
+fp4_status fp4_gemm_grouped_wgrad(const uint8_t* dytq, const uint8_t* dyts, const uint8_t* xtq,
+                                  const uint8_t* xts, const int32_t* offsets, int64_t experts,
+                                  int64_t rows, int64_t N, int64_t K, void* dw, fp4_out_dtype out,
+                                  void* stream);
 
 /* Static, NUL-terminated name of a status code. */
 const char* fp4_status_string(fp4_status status);

@@ -138,3 +138,18 @@ def test_units_of_the_grouped_layout_never_meet():
             for e in range(E):
                 end = off[e] // U + e + (off[e + 1] - off[e] + U - 1) // U
                 assert end <= (off[e + 1] // U + e + 1 if e + 1 < E else rows // U + E)
+
+
+def test_gemm_grouped_wgrad_errors(L):
+    def call(p=(A, A, A, A), off=A, E=4, rows=64, N=64, K=64, c=A, out=1):
+        return L.fp4_gemm_grouped_wgrad(*p, off, E, rows, N, K, c, out, None)
+
+    assert call(out=2) == ERR_ENUM
+    for i in range(4):
+        assert call(p=tuple(None if j == i else A for j in range(4))) == ERR_NULL
+        assert call(p=tuple(MIS if j == i else A for j in range(4))) == ERR_ALIGN
+    assert call(off=None) == ERR_NULL and call(c=None) == ERR_NULL
+    assert call(off=A + 2) == ERR_ALIGN and call(c=MIS) == ERR_ALIGN
+    for bad in (dict(E=0), dict(E=1025), dict(rows=0), dict(rows=2 ** 24), dict(N=48), dict(K=16), dict(N=0),
+                dict(N=2 ** 20, K=2 ** 20)):
+        assert call(**bad) == ERR_SHAPE, bad
