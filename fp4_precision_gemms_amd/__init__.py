@@ -3,10 +3,11 @@ for AMD Instinct MI355X (gfx950).
 
 The functions below carry the names of the C entry points (include/fp4.h)
 and only marshal arguments: shapes and pointers of torch tensors in, status
-codes out.  Every step of the computation runs in the HIP kernels of the
+codes out (through ctypes; the norm, grouped and few-row operators, whose
+calls are short, through the CPython functions of csrc/torch_binding.cpp).  Every step of the computation runs in the HIP kernels of the
 library.  torch supplies device memory and the current HIP stream.
 
-If libfp4.so has not been built (``python -m fp4_precision_gemms_amd.build``)
+If the libraries have not been built (``python -m fp4_precision_gemms_amd.build``)
 every call raises; there is no fallback.
 """
 from __future__ import annotations
@@ -114,26 +115,28 @@ def _need(t: torch.Tensor, dtype, name: str) -> None:
         raise ValueError("%s must be contiguous" % name)
 
 
-def _need_on(t: torch.Tensor, dtype, shape, device, name: str) -> None:
-    """A contiguous `dtype` tensor of `shape` on `device` (a GPU)."""
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if not t.is_cuda or t.device != device:
-        raise ValueError("%s must be a GPU tensor on %s, got one on %s" % (name, device, t.device))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
+_binding = None
 
 
-def _call(fn, device, stream, *args) -> None:
-    """fn(*args, stream) with `device` current, so that the launch goes to the
-    device that holds the tensors."""
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream_ptr(stream, device)))
-    else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream_ptr(stream, device)))
+def _native():
+    """The functions of csrc/torch_binding.cpp; raises if they are not built."""
+    global _binding
+    if _binding is None:
+        lib()
+        try:
+            from . import _torch_binding
+        except ImportError as e:
+            raise RuntimeError("_torch_binding.so is not built: run `python -m fp4_precision_gemms_amd.build`") from e
+        _torch_binding.set_error(Fp4Error)
+        _binding = _torch_binding
+    return _binding
+
+
+def _stream_of(stream, t: torch.Tensor) -> int:
+    """`stream` as an integer; by default the current stream of t's device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.device.index) if t.is_cuda else 0
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def code_shape(R: int, C: int):
@@ -397,30 +400,7 @@ def fp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.
     fp32 [rows].  `out`: optional preallocated (codes, scales, h, rstd); h may
     be x or residual.  `y`: optional bf16 [rows, cols] that receives the norm
     before its quantization, rounded to bf16."""
-    rows, cols = x.shape
-    dev = x.device
-    bf = torch.bfloat16
-    _need_on(x, bf, (rows, cols), dev, "x")
-    _need_on(weight, bf, (cols,), dev, "weight")
-    if residual is not None:
-        _need_on(residual, bf, (rows, cols), dev, "residual")
-    cshape, sshape = mx8_shapes(rows, cols) if fmt == FMT_MXFP8 else (code_shape(rows, cols), scale_shape(rows, cols))
-    if out is None:
-        codes = torch.empty(cshape, dtype=torch.uint8, device=dev)
-        scales = torch.empty(sshape, dtype=torch.uint8, device=dev)
-        h = x if residual is None else torch.empty_like(x)
-        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-    else:
-        codes, scales, h, rstd = out
-        _need_on(codes, torch.uint8, cshape, dev, "codes")
-        _need_on(scales, torch.uint8, sshape, dev, "scales")
-        _need_on(h, bf, (rows, cols), dev, "h")
-        _need_on(rstd, torch.float32, (rows,), dev, "rstd")
-    if y is not None:
-        _need_on(y, bf, (rows, cols), dev, "y")
-    _call(lib().fp4_rmsnorm_quantize, dev, stream, x.data_ptr(), _ptr(residual), weight.data_ptr(), eps, rows, cols,
-          fmt, None if residual is None and h is x else h.data_ptr(), rstd.data_ptr(), _ptr(y), codes.data_ptr(), scales.data_ptr())
-    return codes, scales, h, rstd
+    return _native().rmsnorm_quantize(x, weight, residual, eps, fmt, out, y, _stream_of(stream, x))
 
 
 def fp4_rmsnorm_workspace_bytes(rows: int, cols: int) -> int:
@@ -433,49 +413,7 @@ def fp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor
     """(dx bf16 [rows, cols], dw fp32 [cols]) of the norm from dy and the h and
     rstd of the forward pass; `dh`: the gradient that reaches h past the norm
     (see include/fp4.h).  `out`: optional preallocated (dx, dw); dx may be dh."""
-    rows, cols = dy.shape
-    dev = dy.device
-    bf = torch.bfloat16
-    _need_on(dy, bf, (rows, cols), dev, "dy")
-    _need_on(h, bf, (rows, cols), dev, "h")
-    _need_on(weight, bf, (cols,), dev, "weight")
-    _need_on(rstd, torch.float32, (rows,), dev, "rstd")
-    if dh is not None:
-        _need_on(dh, bf, (rows, cols), dev, "dh")
-    if out is None:
-        dx, dw = torch.empty_like(dy), torch.empty(cols, dtype=torch.float32, device=dev)
-    else:
-        dx, dw = out
-        _need_on(dx, bf, (rows, cols), dev, "dx")
-        _need_on(dw, torch.float32, (cols,), dev, "dw")
-    if workspace is None:
-        workspace = torch.empty(fp4_rmsnorm_workspace_bytes(rows, cols), dtype=torch.uint8, device=dev)
-    else:
-        _need_on(workspace, torch.uint8, workspace.shape, dev, "workspace")
-    _call(lib().fp4_rmsnorm_backward, dev, stream, dy.data_ptr(), h.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
-          _ptr(dh), rows, cols, dx.data_ptr(), dw.data_ptr(), workspace.data_ptr(), workspace.numel())
-    return dx, dw
-
-
-_OUT_TYPES = {OUT_F32: torch.float32, OUT_BF16: torch.bfloat16}
-
-
-def _few_operand(a: torch.Tensor, as_: torch.Tensor):
-    """(fmt, rows, K) of activations, by the shape of their codes."""
-    if a.dim() == 2:
-        if as_.shape != (a.shape[0], a.shape[1] // 32):
-            raise ValueError("MXFP8 codes %s and scales %s do not describe one operand"
-                             % (tuple(a.shape), tuple(as_.shape)))
-        return FMT_MXFP8, a.shape[0], a.shape[1]
-    return (FMT_MXFP4, *mx_dims(a, as_))
-
-
-def _product_out(out, shape, out_dtype: int, device):
-    dt = _OUT_TYPES[out_dtype]
-    if out is None:
-        return torch.empty(shape, dtype=dt, device=device)
-    _need_on(out, dt, shape, device, "out")
-    return out
+    return _native().rmsnorm_backward(dy, h, weight, rstd, dh, out, workspace, _stream_of(stream, dy))
 
 
 def fp4_gemm_decode(aq: torch.Tensor, as_: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
@@ -483,17 +421,7 @@ def fp4_gemm_decode(aq: torch.Tensor, as_: torch.Tensor, wq: torch.Tensor, ws: t
     """c[M, N] = A W^T for few rows: A MXFP8 (codes [M, K], scales [M, K/32])
     or MXFP4 (codes and scales of mx_shapes(M, K)), W [N, K] MXFP4 (see
     include/fp4.h)."""
-    fmt, M, K = _few_operand(aq, as_)
-    N, Kw = mx_dims(wq, ws)
-    if K != Kw:
-        raise ValueError("decode operands have different contraction sizes (%d, %d)" % (K, Kw))
-    dev = aq.device
-    for t, n in ((aq, "a codes"), (as_, "a scales"), (wq, "w codes"), (ws, "w scales")):
-        _need_on(t, torch.uint8, t.shape, dev, n)
-    out = _product_out(out, (M, N), out_dtype, dev)
-    _call(lib().fp4_gemm_decode, dev, stream, aq.data_ptr(), as_.data_ptr(), fmt, wq.data_ptr(), ws.data_ptr(),
-          M, N, K, out.data_ptr(), out_dtype)
-    return out
+    return _native().gemm_decode(aq, as_, wq, ws, out, out_dtype, _stream_of(stream, aq))
 
 
 def grouped_shapes(rows: int, cols: int, experts: int, axis: int):
@@ -505,43 +433,16 @@ def grouped_shapes(rows: int, cols: int, experts: int, axis: int):
     return (cols // 32, units, 512), (rows // 256 + experts, cols, 8)
 
 
-def _offsets(offsets: torch.Tensor, device) -> int:
-    """The number of experts of row offsets (int32 [experts + 1])."""
-    if offsets.dim() != 1 or offsets.shape[0] < 2:
-        raise ValueError("offsets must be int32 [experts + 1], got shape %s" % (tuple(offsets.shape),))
-    _need_on(offsets, torch.int32, offsets.shape, device, "offsets")
-    return offsets.shape[0] - 1
-
-
-def _quantize_grouped(x, offsets, axes, had_n, had, sign_seed, rnd, sr_rows, sr_cols, out, stream):
-    rows, cols = x.shape
-    dev = x.device
-    _need_on(x, torch.bfloat16, (rows, cols), dev, "x")
-    experts = _offsets(offsets, dev)
-    shapes = [s for axis in axes for s in grouped_shapes(rows, cols, experts, axis)]
-    if out is None:
-        out = [torch.empty(s, dtype=torch.uint8, device=dev) for s in shapes]
-    elif len(out) != len(shapes):
-        raise ValueError("out must hold %d tensors" % len(shapes))
-    else:
-        for t, s in zip(out, shapes):
-            _need_on(t, torch.uint8, s, dev, "output")
-    p = [t.data_ptr() for t in out]
-    r = p[:2] if AXIS_ROWS in axes else [None, None]
-    c = p[-2:] if AXIS_COLS in axes else [None, None]
-    m = 2 ** 64 - 1
-    _call(lib().fp4_quantize_grouped, dev, stream, x.data_ptr(), offsets.data_ptr(), experts, rows, cols, had_n, had,
-          sign_seed & m, rnd, sr_rows & m, sr_cols & m, *r, *c)
-    return tuple(out)
-
-
 def fp4_quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, axis: int = AXIS_COLS, had_n: int = 32,
                          had: int = HAD_NONE, sign_seed: int = 0, rnd: int = RTN, sr_seed: int = 0, out=None,
                          stream=None):
     """(codes, scales) of bf16 x[rows, cols] with rows grouped by expert
     (offsets int32 [experts + 1], on the GPU), along `axis`, in the shapes of
     grouped_shapes (see include/fp4.h)."""
-    return _quantize_grouped(x, offsets, (axis,), had_n, had, sign_seed, rnd, sr_seed, sr_seed, out, stream)
+    if axis not in (AXIS_COLS, AXIS_ROWS):
+        raise ValueError("axis must be AXIS_COLS or AXIS_ROWS")
+    return _native().quantize_grouped(x, offsets, 1 + axis, had_n, had, sign_seed, rnd, sr_seed, sr_seed, out,
+                                      _stream_of(stream, x))
 
 
 def fp4_quantize_grouped_dual(x: torch.Tensor, offsets: torch.Tensor, had_n: int = 32, had: int = HAD_NONE,
@@ -549,8 +450,8 @@ def fp4_quantize_grouped_dual(x: torch.Tensor, offsets: torch.Tensor, had_n: int
                               out=None, stream=None):
     """Both quantizations of x from one read: (codes, scales) along rows,
     rotated, and (codes, scales) along cols, not rotated."""
-    return _quantize_grouped(x, offsets, (AXIS_ROWS, AXIS_COLS), had_n, had, sign_seed, rnd, sr_seed_rows,
-                             sr_seed_cols, out, stream)
+    return _native().quantize_grouped(x, offsets, 3, had_n, had, sign_seed, rnd, sr_seed_rows, sr_seed_cols, out,
+                                      _stream_of(stream, x))
 
 
 def fp4_gemm_grouped(aq: torch.Tensor, as_: torch.Tensor, offsets: torch.Tensor, wq: torch.Tensor,
@@ -561,24 +462,7 @@ def fp4_gemm_grouped(aq: torch.Tensor, as_: torch.Tensor, offsets: torch.Tensor,
     [experts, ceil(N/32), K/32, 512] and ws [experts, ceil(K/256), N, 8]: the
     experts' weights, each quantized along its contraction.  Rows of no expert
     are left as they were (in a new tensor: not set)."""
-    dev = aq.device
-    experts = _offsets(offsets, dev)
-    if wq.dim() != 4 or ws.dim() != 4 or wq.shape[0] != experts or ws.shape[0] != experts:
-        raise ValueError("weights must be codes [experts, ceil(N/32), K/32, 512] and scales [experts, ceil(K/256), "
-                         "N, 8] of %d experts, got %s and %s" % (experts, tuple(wq.shape), tuple(ws.shape)))
-    N, K = ws.shape[2], wq.shape[2] * 32
-    if wq.shape[1:] != code_shape(N, K) or ws.shape[1:] != scale_shape(N, K):
-        raise ValueError("codes %s and scales %s do not describe one operand" % (tuple(wq.shape), tuple(ws.shape)))
-    fmt = FMT_MXFP8 if aq.dim() == 2 else FMT_MXFP4
-    shapes = mx8_shapes(rows, K) if fmt == FMT_MXFP8 else grouped_shapes(rows, K, experts, AXIS_COLS)
-    _need_on(aq, torch.uint8, shapes[0], dev, "a codes")
-    _need_on(as_, torch.uint8, shapes[1], dev, "a scales")
-    _need_on(wq, torch.uint8, wq.shape, dev, "w codes")
-    _need_on(ws, torch.uint8, ws.shape, dev, "w scales")
-    out = _product_out(out, (rows, N), out_dtype, dev)
-    _call(lib().fp4_gemm_grouped, dev, stream, aq.data_ptr(), as_.data_ptr(), fmt, offsets.data_ptr(), experts, rows,
-          wq.data_ptr(), ws.data_ptr(), N, K, out.data_ptr(), out_dtype)
-    return out
+    return _native().gemm_grouped(aq, as_, offsets, wq, ws, rows, out, out_dtype, _stream_of(stream, aq))
 
 
 def fp4_gemm_grouped_wgrad(dytq: torch.Tensor, dyts: torch.Tensor, xtq: torch.Tensor, xts: torch.Tensor,
@@ -587,17 +471,8 @@ def fp4_gemm_grouped_wgrad(dytq: torch.Tensor, dyts: torch.Tensor, xtq: torch.Te
     """dw[experts, N, K] = each expert's dY^T X from dY [rows, N] and X
     [rows, K] quantized along rows by fp4_quantize_grouped with these offsets
     (see include/fp4.h)."""
-    dev = dytq.device
-    experts = _offsets(offsets, dev)
-    N, K = dyts.shape[1], xts.shape[1]
-    for q, s, c, n in ((dytq, dyts, N, "dY"), (xtq, xts, K, "X")):
-        shapes = grouped_shapes(rows, c, experts, AXIS_ROWS)
-        _need_on(q, torch.uint8, shapes[0], dev, n + " codes")
-        _need_on(s, torch.uint8, shapes[1], dev, n + " scales")
-    out = _product_out(out, (experts, N, K), out_dtype, dev)
-    _call(lib().fp4_gemm_grouped_wgrad, dev, stream, dytq.data_ptr(), dyts.data_ptr(), xtq.data_ptr(), xts.data_ptr(),
-          offsets.data_ptr(), experts, rows, N, K, out.data_ptr(), out_dtype)
-    return out
+    return _native().gemm_grouped_wgrad(dytq, dyts, xtq, xts, offsets, rows, out, out_dtype,
+                                        _stream_of(stream, dytq))
 
 
 from . import linear  # noqa: E402  (the autograd layer built on the calls above)

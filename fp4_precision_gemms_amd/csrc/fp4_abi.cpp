@@ -219,7 +219,7 @@ fp4_status fp4_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16, c
 
 size_t fp4_rmsnorm_workspace_bytes(int64_t rows, int64_t cols) {
     if (check_norm_shape(rows, cols) != FP4_OK) return 0;
-    return (size_t)(fp4dev::rmsnorm_back_parts(rows) * cols) * sizeof(float);
+    return (size_t)(fp4dev::rmsnorm_back_parts(rows, cols) * cols) * sizeof(float);
 }
 
 fp4_status fp4_rmsnorm_backward(const void* dy_bf16, const void* h_bf16, const void* weight_bf16,

@@ -68,8 +68,8 @@ hipError_t launch_rmsnorm_quant(const void* x, const void* res, const void* w, d
                                 int64_t cols, int e4m3, void* h, float* rstd, void* y, uint8_t* codes,
                                 uint8_t* scales, hipStream_t st);
 
-// Its backward pass; parts: fp32 [rmsnorm_back_parts(rows), cols].
-int64_t rmsnorm_back_parts(int64_t rows);
+// Its backward pass; parts: fp32 [rmsnorm_back_parts(rows, cols), cols].
+int64_t rmsnorm_back_parts(int64_t rows, int64_t cols);
 hipError_t launch_rmsnorm_back(const void* dy, const void* h, const void* w, const float* rstd, const void* dh,
                                int64_t rows, int64_t cols, void* dx, float* dw, float* parts, hipStream_t st);
 

@@ -290,11 +290,30 @@ hipError_t launch_few(const uint8_t* a, const uint8_t* as, const int* offsets, c
 template <bool A8>
 hipError_t choose(const uint8_t* a, const uint8_t* as, const int* offsets, const uint8_t* w, const uint8_t* ws,
                   int64_t rows, int64_t experts, int64_t N, int64_t K, void* c, int out_bf16, hipStream_t st) {
-#define FP4_FEW(MT, NT) return launch_few<A8, MT, NT, 8>(a, as, offsets, w, ws, rows, experts, N, K, c, out_bf16, st)
-    const int64_t each = (rows + experts - 1) / experts;
-    if (each <= 16) FP4_FEW(1, 1);
-    if (each <= 32) FP4_FEW(2, 1);
-    FP4_FEW(4, 1);
+#define FP4_FEW(MT, NT, W) return launch_few<A8, MT, NT, W>(a, as, offsets, w, ws, rows, experts, N, K, c, out_bf16, st)
+#define FP4_FEW_ROWS(NT, W)                      \
+    do {                                         \
+        if (each <= 16) FP4_FEW(1, NT, W);       \
+        if (each <= 32) FP4_FEW(2, NT, W);       \
+        FP4_FEW(4, A8 ? 1 : NT, W);              \
+    } while (0)
+    // Row tiles by the rows an expert has on average.  Weight rows and waves
+    // per workgroup: 32 and 4 where that makes 256 workgroups (96 rows over 64
+    // experts of 1408 x 2048: 15.8 us, against 27.4 with 16 and 8; 1 x 14336 x
+    // 4096: 8.1 and 8.8), else 16 and 8 (24 x 4096 x 14336: 8.0 us, 9.4 with 32
+    // rows and 10.0 with 4 waves).  Fewer waves where the contraction does not
+    // have two k-groups for each (50 rows an expert, 40 experts of 1120 x 736:
+    // 12.3 us with two, 14.3 with four).  MXFP8 with four row tiles has no
+    // registers for a second weight tile.
+    const int64_t each = (rows + experts - 1) / experts, groups = (K + 255) / 256;
+    if ((N + 31) / 32 * experts >= 256) {
+        if (groups >= 8) FP4_FEW_ROWS(2, 4);
+        FP4_FEW_ROWS(2, 2);
+    }
+    if (groups >= 16) FP4_FEW_ROWS(1, 8);
+    if (groups >= 8) FP4_FEW_ROWS(1, 4);
+    FP4_FEW_ROWS(1, 2);
+#undef FP4_FEW_ROWS
 #undef FP4_FEW
 }
 

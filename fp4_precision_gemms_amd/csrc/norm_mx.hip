@@ -65,6 +65,18 @@ __device__ __forceinline__ uint2 encode8_e4m3(const float* y, uint32_t byte) {
     return make_uint2((uint32_t)lo, (uint32_t)hi);
 }
 
+// The row block of workgroup b of n.  Workgroups go round-robin over the 8
+// XCDs, each with an L2 of its own; here B consecutive row blocks (32 rows) run
+// on one XCD, so that the 16-byte code pieces and 8-byte scale groups of
+// neighbouring rows meet in one L2 and leave as whole lines (8192 x 4096 to
+// MXFP4 43.6 us, 52.8 with the rows in launch order; 8192 x 8192 82.9 and 98.9).
+template <int B>
+__device__ __forceinline__ unsigned row_block(unsigned b, unsigned n) {
+    if (b >= n / (8 * B) * (8 * B)) return b;
+    const unsigned xcd = b & 7, i = b >> 3;
+    return (i / B) * (8 * B) + xcd * B + i % B;
+}
+
 // TPR threads share a row, RPB rows per workgroup; a lane owns V chunks of 8
 // consecutive elements, so four adjacent lanes hold one 32-element block.
 // (x, res and h are not __restrict__: h may be x or res itself; every lane
@@ -77,7 +89,7 @@ __global__ __launch_bounds__(TPR * RPB) void rmsnorm_quant(
     static_assert(TPR == 64 || RPB == 1, "rows that share a workgroup are a wave each");
     constexpr int kWaves = TPR / 64;
     const int t = threadIdx.x % TPR, nch = cols / 8, q = t & 3;
-    const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+    const int64_t row = (int64_t)row_block<32 / RPB>(blockIdx.x, gridDim.x) * RPB + threadIdx.x / TPR;
     if (RPB > 1 && row >= rows) return;               // a wave of its own: no barrier below
     const int64_t base = row * nch;
     uint4 v[V], wv[V];
@@ -192,13 +204,15 @@ hipError_t launch_norm(const void* x, const void* res, const void* w, double eps
 
 // ---------------------------------------------------------------- backward
 // One workgroup walks over rows blockIdx.x, + gridDim.x, ...; the next row's
-// loads are issued before this row's reduction.
+// loads are issued before this row's reduction (not with 1024 threads of 4
+// chunks each, which have no registers for it).
 template <int TPR, int V, bool DH>
 __global__ __launch_bounds__(TPR) void rmsnorm_back(
     const uint4* __restrict__ dy, const uint4* __restrict__ h, const uint4* __restrict__ weight,
     const float* __restrict__ rstd, const uint4* dh, int64_t rows, int cols, uint4* dx,
     float* __restrict__ parts) {
     constexpr int kWaves = TPR / 64;
+    constexpr bool kAhead = TPR * V < 4096;
     __shared__ float part[2][kWaves];
     const int t = threadIdx.x, nch = cols / 8;
     const float inv_cols = 1.0f / (float)cols;
@@ -225,14 +239,15 @@ __global__ __launch_bounds__(TPR) void rmsnorm_back(
         r = rstd[row];
     };
     int64_t row = blockIdx.x;                          // gridDim.x <= rows
-    load(row);
+    if constexpr (kAhead) load(row);
     for (int turn = 0; row < rows; turn ^= 1) {
+        if constexpr (!kAhead) load(row);
         uint4 g1[V], h1[V], e1[V];
         const float r1 = r;
 #pragma unroll
         for (int i = 0; i < V; ++i) { g1[i] = gv[i]; h1[i] = hv[i]; if constexpr (DH) e1[i] = ev[i]; }
         const int64_t next = row + gridDim.x;
-        if (next < rows) load(next);
+        if (kAhead && next < rows) load(next);
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -286,28 +301,26 @@ __global__ __launch_bounds__(TPR) void rmsnorm_back(
     }
 }
 
-// dw[c] = sum of n rows of parts[n, cols]: 32 columns per workgroup, 8 slices
+// dw[c] = sum of n rows of parts[n, cols]: 32 columns per workgroup, 32 slices
 // of the rows, joined in a fixed order.
-__global__ __launch_bounds__(256) void sum_parts(const float* __restrict__ parts, int n, int cols,
-                                                 float* __restrict__ dw) {
-    __shared__ float part[8][32];
+__global__ __launch_bounds__(1024) void sum_parts(const float* __restrict__ parts, int n, int cols,
+                                                  float* __restrict__ dw) {
+    __shared__ float part[32][32];
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
     float s = 0.0f;                                    // cols % 32 == 0: c < cols
-    int i = slice;
-    for (; i + 56 < n; i += 64) {
+    for (int i = slice; i < n; i += 256) {
         float v[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = parts[(int64_t)(i + 8 * k) * cols + c];
+        for (int k = 0; k < 8; ++k) v[k] = i + 32 * k < n ? parts[(int64_t)(i + 32 * k) * cols + c] : 0.0f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) s += v[k];
     }
-    for (; i < n; i += 8) s += parts[(int64_t)i * cols + c];
     part[slice][threadIdx.x & 31] = s;
     __syncthreads();
     if (slice == 0) {
         s = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s += part[k][threadIdx.x];
+        for (int k = 0; k < 32; ++k) s += part[k][threadIdx.x];
         dw[c] = s;
     }
 }
@@ -322,9 +335,6 @@ hipError_t launch_back(const void* dy, const void* h, const void* w, const float
                   (const uint4*)h, (const uint4*)w, rstd, (const uint4*)dh, rows, (int)cols, (uint4*)dx, parts);
 }
 
-// Enough rows to fill the card with a wave per row (256 CUs x 8 waves).
-constexpr int64_t kManyRows = 2048;
-
 }  // namespace
 
 hipError_t launch_rmsnorm_quant(const void* x, const void* res, const void* w, double eps, int64_t rows,
@@ -333,37 +343,41 @@ hipError_t launch_rmsnorm_quant(const void* x, const void* res, const void* w, d
     const int64_t nch = cols / 8;
 #define FP4_ROW(TPR, RPB, V) \
     return launch_norm<TPR, RPB, V>(x, res, w, eps, rows, cols, e4m3, h, rstd, y, codes, scales, st)
-    // many rows: a wave per row, no barrier; few rows or long ones: a
-    // workgroup per row
-    if (rows >= kManyRows && nch <= 512) {
-        if (nch <= 128) FP4_ROW(64, 4, 2);
-        if (nch <= 256) FP4_ROW(64, 4, 4);
-        FP4_ROW(64, 4, 8);
-    }
-    if (nch <= 256) FP4_ROW(256, 1, 1);
+    // two 16-byte loads of each input per lane; a wave per row (four rows a
+    // workgroup, no barrier) up to 1024 columns.  Measured to MXFP8 with a
+    // residual, rows in launch order: 8192 x 4096 with 128, 256 and 512 threads
+    // a row 45.7, 43.7 and 44.3 us (a wave a row 49), 8192 x 8192 with 256 and
+    // 512 84.4 and 81.6, 8192 x 2048 with 64, 128 and 256 24.8, 23.4 and 24.1.
+    if (nch <= 64) FP4_ROW(64, 4, 1);
+    if (nch <= 128) FP4_ROW(64, 4, 2);
+    if (nch <= 256) FP4_ROW(128, 1, 2);
     if (nch <= 512) FP4_ROW(256, 1, 2);
-    if (nch <= 1024) FP4_ROW(256, 1, 4);
+    if (nch <= 1024) FP4_ROW(512, 1, 2);
     if (nch <= 2048) FP4_ROW(1024, 1, 2);
     FP4_ROW(1024, 1, 4);
 #undef FP4_ROW
 }
 
-int64_t rmsnorm_back_parts(int64_t rows) {
-    // workgroups of the backward pass
-    return rows < 1024 ? rows : 1024;
+// Workgroups of the backward pass: one per CU keeps the parts of dw, and the
+// kernel that adds them up, small (8192 x 8192: 256 parts 97 + 5 us, 1024 parts
+// 103 + 10); narrow rows, whose workgroups are a few waves, take more of them.
+int64_t rmsnorm_back_parts(int64_t rows, int64_t cols) {
+    const int64_t most = cols <= 1024 ? 1024 : cols <= 2048 ? 512 : 256;
+    return rows < most ? rows : most;
 }
 
 hipError_t launch_rmsnorm_back(const void* dy, const void* h, const void* w, const float* rstd, const void* dh,
                                int64_t rows, int64_t cols, void* dx, float* dw, float* parts, hipStream_t st) {
-    const int64_t nch = cols / 8, n = rmsnorm_back_parts(rows);
+    const int64_t nch = cols / 8, n = rmsnorm_back_parts(rows, cols);
     hipError_t e;
-    if (nch <= 256) e = launch_back<256, 1>(dy, h, w, rstd, dh, rows, cols, dx, parts, n, st);
-    else if (nch <= 512) e = launch_back<256, 2>(dy, h, w, rstd, dh, rows, cols, dx, parts, n, st);
-    else if (nch <= 1024) e = launch_back<256, 4>(dy, h, w, rstd, dh, rows, cols, dx, parts, n, st);
-    else if (nch <= 2048) e = launch_back<1024, 2>(dy, h, w, rstd, dh, rows, cols, dx, parts, n, st);
+    if (nch <= 128) e = launch_back<128, 1>(dy, h, w, rstd, dh, rows, cols, dx, parts, n, st);
+    else if (nch <= 256) e = launch_back<256, 1>(dy, h, w, rstd, dh, rows, cols, dx, parts, n, st);
+    else if (nch <= 512) e = launch_back<512, 1>(dy, h, w, rstd, dh, rows, cols, dx, parts, n, st);
+    else if (nch <= 1024) e = launch_back<512, 2>(dy, h, w, rstd, dh, rows, cols, dx, parts, n, st);
+    else if (nch <= 2048) e = launch_back<512, 4>(dy, h, w, rstd, dh, rows, cols, dx, parts, n, st);
     else e = launch_back<1024, 4>(dy, h, w, rstd, dh, rows, cols, dx, parts, n, st);
     if (e != hipSuccess) return e;
-    return launch(&sum_parts, dim3((unsigned)(cols / 32)), dim3(256), st, (const float*)parts, (int)n, (int)cols, dw);
+    return launch(&sum_parts, dim3((unsigned)(cols / 32)), dim3(1024), st, (const float*)parts, (int)n, (int)cols, dw);
 }
 
 }  // namespace fp4dev

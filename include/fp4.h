@@ -380,7 +380,7 @@ fp4_status fp4_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16,
  *        that reaches h past the norm; dx is the gradient of x and of the
  *        residual alike, and may be dh itself (in place) but no other input;
  *   dw[cols] = sum over rows of dy h r, fp32, summed in an order that depends
- *        on rows only (the same inputs give the same bits).
+ *        on the sizes only (the same inputs give the same bits).
  * All in binary32.  workspace: fp4_rmsnorm_workspace_bytes() bytes, whose
  * contents need not be kept between calls; calls that overlap need one each.
  * Requirements as for fp4_rmsnorm_quantize; FP4_ERR_WORKSPACE if too small.

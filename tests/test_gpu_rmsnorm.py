@@ -167,9 +167,9 @@ def test_backward(rows, cols, with_dh):
     torch.cuda.synchronize()
     ref, near, dwref, dwsize = back_reference(dy, h, w, rstd, dh)
     assert (np.abs(dx.double().cpu().numpy() - ref) <= near).all()
-    # dw: rows of a workgroup one after another, then eight slices of the parts
-    parts = min(rows, 1024)
-    depth = -(-rows // parts) + -(-parts // 8) + 8 + 3
+    # dw: rows of a workgroup one after another, then 32 slices of the parts
+    parts = F.fp4_rmsnorm_workspace_bytes(rows, cols) // (4 * cols)
+    depth = -(-rows // parts) + -(-parts // 32) + 32 + 3
     assert (np.abs(dw.double().cpu().numpy() - dwref) <= depth * U32 * dwsize).all()
     assert torch.equal(dx.view(torch.int16), again[0].view(torch.int16)) and torch.equal(dw, again[1])
 
