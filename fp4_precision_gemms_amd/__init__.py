@@ -430,7 +430,7 @@ def grouped_shapes(rows: int, cols: int, experts: int, axis: int):
     units = rows // 32 + experts
     if axis == AXIS_COLS:
         return (units, cols // 32, 512), scale_shape(32 * units, cols)
-    return (cols // 32, units, 512), (rows // 256 + experts, cols, 8)
+    return (cols // 32, 8 * (rows // 256 + experts), 512), (rows // 256 + experts, cols, 8)
 
 
 def fp4_quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, axis: int = AXIS_COLS, had_n: int = 32,

@@ -275,7 +275,7 @@ fp4_status fp4_quantize_grouped(const void* x_bf16, const int32_t* offsets, int6
         !codes_cols != !scales_cols)
         return FP4_ERR_NULL;
     if (rows <= 0 || rows > INT32_MAX || cols <= 0 || cols % 32 || cols >= kMaxContraction || experts <= 0 ||
-        experts > kMaxExperts || ((cols + 255) / 256) * (rows / 32 + experts) > INT32_MAX)
+        experts > kMaxExperts || ((cols + 255) / 256) * (rows / 32 + 8 * experts) > INT32_MAX)
         return FP4_ERR_SHAPE;
     if (!aligned16(x_bf16) || !aligned4(offsets) || !aligned16(codes_rows) || !aligned16(scales_rows) ||
         !aligned16(codes_cols) || !aligned16(scales_cols))
@@ -304,7 +304,8 @@ fp4_status fp4_gemm_grouped_wgrad(const uint8_t* dytq, const uint8_t* dyts, cons
     if (out != FP4_OUT_F32 && out != FP4_OUT_BF16) return FP4_ERR_ENUM;
     if (!dytq || !dyts || !xtq || !xts || !offsets || !dw) return FP4_ERR_NULL;
     if (rows <= 0 || N <= 0 || K <= 0 || N % 32 || K % 32 || rows > INT32_MAX || N > INT32_MAX || K > INT32_MAX ||
-        experts <= 0 || experts > kMaxExperts || 32 * (rows / 32 + experts) >= kMaxContraction)
+        experts <= 0 || experts > kMaxExperts || 256 * (rows / 256 + experts) >= kMaxContraction ||
+        (rows / 256 + experts) * (N > K ? N : K) >= (INT64_C(1) << 28))
         return FP4_ERR_SHAPE;
     if (!product_ok(N, K) || !product_ok(N * K, experts) ||
         ((N + 255) / 256) * ((K + 255) / 256) >= kMaxTiles / experts)

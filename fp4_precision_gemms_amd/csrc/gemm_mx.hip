@@ -165,8 +165,12 @@ constexpr int kEpiRegion = 32 * kEpiRow;        // 32 rows per wave
 // GROUP (grouped.hpp): kRowGroups -- the rows of A and C belong to experts, each
 // with a B of its own; M is the row count of A's grouped layout, a tile never
 // crosses into the next expert, and FAST's full tiles hold for the columns and
-// the contraction only.  kDepthGroups -- each expert owns a span of the
-// contraction and an output [M, N] of its own (KTAIL: spans end anywhere).
+// the contraction only.  kDepthGroups -- each expert owns whole stages of the
+// contraction and an output [M, N] of its own.  With groups FAST means its
+// loads alone: the contraction is a multiple of 256 and tiles may be partial
+// (code rows past the operand read as zero, scale rows as whatever follows
+// them: they reach no output that is stored); stages before the first are
+// clamped like those past the last, and take scales that make them vanish.
 enum { kNoGroups = 0, kRowGroups = 1, kDepthGroups = 2 };
 
 struct GroupArgs {
@@ -198,6 +202,7 @@ __device__ __forceinline__ void gemm_tiles(
     constexpr int kVmStage = FM + (FAST ? 1 : 2) + 2 * kKS + 2;
     static_assert(FM >= 4 && FM <= 8, "tile rows");
     static_assert(!(FAST && KTAIL), "the fast path has no contraction tail");
+    static_assert(GROUP != kDepthGroups || FAST, "an expert's span is whole stages");
     constexpr int kWaitStage = 2 * kVmStage - 2;
     static_assert(kWaitStage <= 63, "vmcnt range");
     static_assert(kSlots * kSlot <= 160 * 1024, "LDS");
@@ -272,7 +277,7 @@ __device__ __forceinline__ void gemm_tiles(
 #pragma unroll
     for (int j = 0; j < FN; ++j) offb[j] = (uint32_t)(2 * wave + j) * gstride + (uint32_t)lane * 16;
     // the upper half of a k-step past the last block (nb odd) reads zero
-    bool half_tail = KTAIL && (nb & 1) && h == 1;
+    const bool half_tail = KTAIL && (nb & 1) && h == 1;
 
     int64_t m0 = 0, n0 = 0, rows_a = 0, rows_b = 0;
     // the tile's first row in C, and what comes before its expert's output
@@ -328,22 +333,23 @@ __device__ __forceinline__ void gemm_tiles(
             e = __builtin_amdgcn_readfirstlane(e);
             const int lo = __builtin_amdgcn_readfirstlane(expert_ints<0>()[e]);
             const int hi = __builtin_amdgcn_readfirstlane(expert_ints<1>()[e]);
-            nb = (hi - lo + 31) / 32;
-            nks = (int)((nb + 1) / 2);
-            nk = (int)((nb + 7) / 8);
+            nk = (hi - lo + 255) / 256;
+            nb = 8 * nk;
+            nks = 4 * nk;
             kfirst = -((kSlots - nk % kSlots) % kSlots);
-            half_tail = KTAIL && (nb & 1) && h == 1;
-            const int64_t b0 = lo / 32 + e, q0 = lo / 256 + e;
+            const int64_t q0 = lo / 256 + e;
             cbase = (int64_t)e * M * N;
             sa_tile = SA + q0 * M * 8;
             sb_tile = SB + q0 * N * 8;
-            // an expert's span of each 32-row group: up to its last block
+            // an expert's span of each 32-row group: up to its last stage (one
+            // without rows still loads a stage, which stays unused)
+            const int64_t span = (nk ? nk : 1) * 4096;
             ra = __builtin_amdgcn_make_buffer_rsrc(
-                (void*)(A + (m0 / 32) * (int64_t)gstride + b0 * 512), (short)0,
-                (int)(((rows_a + 31) / 32 - 1) * (int64_t)gstride + nb * 512), kBufferWord3);
+                (void*)(A + (m0 / 32) * (int64_t)gstride + q0 * 4096), (short)0,
+                (int)(((rows_a + 31) / 32 - 1) * (int64_t)gstride + span), kBufferWord3);
             rb = __builtin_amdgcn_make_buffer_rsrc(
-                (void*)(B + (n0 / 32) * (int64_t)gstride + b0 * 512), (short)0,
-                (int)(((rows_b + 31) / 32 - 1) * (int64_t)gstride + nb * 512), kBufferWord3);
+                (void*)(B + (n0 / 32) * (int64_t)gstride + q0 * 4096), (short)0,
+                (int)(((rows_b + 31) / 32 - 1) * (int64_t)gstride + span), kBufferWord3);
         } else {
         // the tile's row groups of each operand; groups past the operand's
         // last one are out of range and read as zero
@@ -355,10 +361,17 @@ __device__ __forceinline__ void gemm_tiles(
         if constexpr (FAST) {
             // stage q of the tile's rows starts q R 8 bytes further on
             rsa = __builtin_amdgcn_make_buffer_rsrc((void*)(sa_tile + m0 * 8), (short)0,
-                                                    (int)(((int64_t)nk * M - m0) * 8), kBufferWord3);
+                                                    (int)(((int64_t)(GROUP && nk == 0 ? 1 : nk) * M - m0) * 8), kBufferWord3);
             rsb = __builtin_amdgcn_make_buffer_rsrc((void*)(sb_tile + n0 * 8), (short)0,
-                                                    (int)(((int64_t)nk * N - n0) * 8), kBufferWord3);
+                                                    (int)(((int64_t)(GROUP && nk == 0 ? 1 : nk) * N - n0) * 8), kBufferWord3);
         }
+    };
+
+    // FAST: the stage loaded in place of stage kt, which may lie past the last
+    // one (or before the first, with groups; an expert without rows has none)
+    auto stage_of = [&](int kt) {
+        if (GROUP) return kt < 0 ? 0 : kt < nk ? kt : nk ? nk - 1 : 0;
+        return kt < nk ? kt : nk - 1;
     };
 
     // ---- loads ---------------------------------------------------------
@@ -367,7 +380,7 @@ __device__ __forceinline__ void gemm_tiles(
     // `scales`.  A stage outside [0, nk) is all zero.
     auto dma_a = [&](int kt, uint8_t* slot, int d0, int d1, bool scales) {
         if constexpr (FAST) {
-            const int kc = kt < nk ? kt : nk - 1;
+            const int kc = stage_of(kt);
             const int soff = __builtin_amdgcn_readfirstlane((4 * kc + wave) * 1024);
 #pragma unroll
             for (int d = 0; d < FM; ++d)
@@ -408,7 +421,8 @@ __device__ __forceinline__ void gemm_tiles(
     // B fragment j of k-step s (global index) into registers.
     auto load_b = [&](int s, int j) -> v4i {
         if constexpr (FAST) {
-            const int soff = __builtin_amdgcn_readfirstlane((s < nks ? s : nks - 1) * 1024);
+            const int soff = GROUP ? __builtin_amdgcn_readfirstlane((s < 0 ? 0 : s < nks ? s : nks ? nks - 1 : 0) * 1024)
+                                   : __builtin_amdgcn_readfirstlane((s < nks ? s : nks - 1) * 1024);
             return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rb, offb[j], soff, 0));
         }
         bool dead = s < 0 || s >= nks;
@@ -422,7 +436,7 @@ __device__ __forceinline__ void gemm_tiles(
     struct BSc { uint32_t w[FN][2]; };
     auto load_bsc = [&](int kt) -> BSc {
         if constexpr (FAST) {
-            const int kc = kt < nk ? kt : nk - 1;
+            const int kc = stage_of(kt);
             const int ss = __builtin_amdgcn_readfirstlane((int)((int64_t)kc * N * 8));
             BSc r;
 #pragma unroll
@@ -538,7 +552,17 @@ __device__ __forceinline__ void gemm_tiles(
     auto run_stage = [&](int u, int kt) {
         uint8_t* const ahead = slots[(u + 3) % kSlots];
         ASc& nsa = asc[(u + 1) & 1];
-        const SWords sw = stage_words(asc[u & 1], bsc[u], kt);
+        SWords sw = stage_words(asc[u & 1], bsc[u], kt);
+        if constexpr (GROUP && FAST) {
+            // A stage before the first holds stage 0's bytes: with both scales
+            // 2^-127 its products vanish.  (Branches around such a stage made
+            // the compiler spill hundreds of registers.)
+            const uint32_t keep = kt < 0 ? 0u : ~0u;
+#pragma unroll
+            for (int i = 0; i < FM; ++i) sw.a[i] &= keep;
+#pragma unroll
+            for (int j = 0; j < FN; ++j) sw.b[j] &= keep;
+        }
 #pragma unroll
         for (int s = 0; s < kKS - 1; ++s) {
             read_afrags(u, s + 1, (s + 1) & 1);
@@ -641,7 +665,7 @@ __device__ __forceinline__ void gemm_tiles(
     for (int t = blockIdx.x; t < ntiles; t += gridDim.x) {
         // (an accumulating fast-path launch issues no prologue during its
         // epilogues, which read C: its later tiles take theirs here)
-        if ((!FAST || ACC || GROUP == kRowGroups) && !early) {
+        if ((!FAST || ACC) && !early) {
             if (t != (int)blockIdx.x) {
                 // every wave is done with the previous tile's LDS before it is refilled
                 __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
@@ -685,8 +709,9 @@ __device__ __forceinline__ void gemm_tiles(
         // full: the epilogue then has no partial-tile branch, whose zero-store
         // path made the compiler wait for most of these stores before the
         // next tile's first fragment moves
-        const bool full_tile = GROUP == kRowGroups ? (FAST || (vec_store && en0 + kBN <= N)) && erows == BM
-                                                   : FAST || (vec_store && em0 + BM <= M && en0 + kBN <= N);
+        // (with groups a fast path's partial tile stores through a buffer that
+        // drops what lies outside, so it has no branch either)
+        const bool full_tile = FAST || (vec_store && (GROUP ? erows == BM : em0 + BM <= M) && en0 + kBN <= N);
         early = false;
         if constexpr (!KTAIL && !ACC) {
             // The next tile's first stages go out now, into slots 0..2 (this
@@ -708,6 +733,18 @@ __device__ __forceinline__ void gemm_tiles(
         // four whole rows of the wave's columns (fp32: two 128-byte lines
         // each, written non-temporally); with N % 4 != 0 (rows not 16-byte
         // aligned) elements go one by one.
+        // Groups, fast path: the tile's rows of C as one buffer; this lane's
+        // offset in its first row, out of range for columns past N.  What lies
+        // past the last row is past the buffer's end.
+        constexpr int kOut = OBF16 ? 2 : 4;
+        const uint32_t row_bytes = (uint32_t)N * kOut;
+        const __amdgpu_buffer_rsrc_t rc = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)((uint8_t*)C + (ebase + em0 * N + en0) * kOut), (short)0, (int)((erows * N - en0) * kOut),
+            kBufferWord3);
+        const uint32_t offc = en0 + 64 * wave + (lane & 15) * 4 < N
+                                  ? (uint32_t)(lane >> 4) * row_bytes + (uint32_t)(64 * wave + (lane & 15) * 4) * kOut
+                                  : kOob;
+
         uint8_t* const reg = lds3 + wave * kEpiRegion;
         const int lr = lane >> 4, c4 = (lane & 15) * 4;
 #pragma unroll
@@ -721,6 +758,27 @@ __device__ __forceinline__ void gemm_tiles(
                         make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
                                     acc[i][j][4 * q + 3]);
                 }
+            if constexpr (GROUP && FAST) {
+                float4 f[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    f[k] = *reinterpret_cast<const float4*>(reg + (4 * k + lr) * kEpiRow + c4 * 4);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t o = offc + (uint32_t)(32 * i + 4 * k) * row_bytes;
+                    if constexpr (OBF16) {
+                        typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+                        __builtin_amdgcn_raw_buffer_store_b64(
+                            v2u{bf16_rne(f[k].x) | (bf16_rne(f[k].y) << 16), bf16_rne(f[k].z) | (bf16_rne(f[k].w) << 16)},
+                            rc, o, 0, 0);
+                    } else {
+                        typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+                        __builtin_amdgcn_raw_buffer_store_b128(
+                            __builtin_bit_cast(v4u, f[k]), rc, o, 0, 2);   // non-temporal, as below
+                    }
+                }
+                continue;
+            }
             if (full_tile) {
                 float4 f[8];
 #pragma unroll
@@ -907,11 +965,9 @@ hipError_t launch_row_groups(const uint8_t* aq, const uint8_t* as, const int* of
     const int64_t M = 32 * (rows / 32 + experts), tn = (N + kBN - 1) / kBN;
     const int64_t most = (rows / (32 * FM) + experts) * tn;     // tiles of any split, at most
     const GroupArgs ga{offsets, (int)experts, rows};
-    const bool fast = N % kBN == 0 && K % 1024 == 0 && (K / 256) * (M > N ? M : N) * 8 < (INT64_C(1) << 31);
-    if (fast)
+    // whole stages, rows of whole 16-byte pieces, and offsets within 31 bits
+    if (K % 256 == 0 && N % 4 == 0 && N < (INT64_C(1) << 21) && (K / 256) * (M > N ? M : N) * 8 < (INT64_C(1) << 31))
         return launch_grouped<FM, true, false, kRowGroups>(aq, as, wq, ws, M, N, K, c, out_bf16, most, 0, tn, ga, st);
-    if (K % 256 == 0)
-        return launch_grouped<FM, false, false, kRowGroups>(aq, as, wq, ws, M, N, K, c, out_bf16, most, 0, tn, ga, st);
     return launch_grouped<FM, false, true, kRowGroups>(aq, as, wq, ws, M, N, K, c, out_bf16, most, 0, tn, ga, st);
 }
 }  // namespace
@@ -925,9 +981,9 @@ hipError_t launch_gemm_row_groups(const uint8_t* aq, const uint8_t* as, const in
 hipError_t launch_gemm_depth_groups(const uint8_t* aq, const uint8_t* as, const uint8_t* bq, const uint8_t* bs,
                                     const int* offsets, int64_t experts, int64_t rows, int64_t M, int64_t N, void* c,
                                     int out_bf16, hipStream_t st) {
-    const int64_t K = 32 * (rows / 32 + experts);               // of the grouped layout
+    const int64_t K = 256 * (rows / 256 + experts);             // of the grouped layout
     const int64_t tm = (M + 255) / 256, tn = (N + kBN - 1) / kBN;
-    return launch_grouped<8, false, true, kDepthGroups>(aq, as, bq, bs, M, N, K, c, out_bf16, tm * tn * experts, tm,
+    return launch_grouped<8, true, false, kDepthGroups>(aq, as, bq, bs, M, N, K, c, out_bf16, tm * tn * experts, tm,
                                                         tn, GroupArgs{offsets, (int)experts, rows}, st);
 }
 

@@ -2,12 +2,13 @@
 // operands, from the row offsets alone.
 //
 // offsets[0 .. experts]: expert e owns rows [offsets[e], offsets[e + 1]) of a
-// tensor of `rows` rows.  In a layout with units of U rows (U = 32: a row
-// group of the codes or a 32-token block; U = 256: a scale group) expert e
-// starts at unit offsets[e] / U + e.  Its ceil(count / U) units always fit
-// before the next expert's first one: floor((o + n) / U) + 1 >= floor(o / U) +
-// ceil(n / U).  So no prefix sum over the experts, no plan and no look at the
-// counts on the host is needed, and rows / U + experts units hold any split.
+// tensor of `rows` rows.  In a layout with units of U rows expert e starts at
+// unit offsets[e] / U + e.  Its ceil(count / U) units always fit before the
+// next expert's first one: floor((o + n) / U) + 1 >= floor(o / U) + ceil(n / U).
+// So no prefix sum over the experts, no plan and no look at the counts on the
+// host is needed, and rows / U + experts units hold any split.
+// U is 32 (a row group of the tiled codes) where the rows are the operand's
+// rows, 256 (a stage of the GEMMs) where they are its contraction.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -29,8 +30,9 @@ __device__ __forceinline__ RowRange expert_rows(const int* offsets, int e, int64
     return {lo, hi};
 }
 
-// The expert whose span of 32-row units holds unit p (the last one that
-// starts at or before p; -1 if none does).  Called by whole waves.
+// The expert whose span of U-row units holds unit p (the last one that starts
+// at or before p; -1 if none does).  Called by whole waves.
+template <int U>
 __device__ __forceinline__ int expert_of_unit(const int* offsets, int experts, int64_t rows, int64_t p) {
     const int lane = threadIdx.x & 63;
     int n = 0;
@@ -40,7 +42,7 @@ __device__ __forceinline__ int expert_of_unit(const int* offsets, int experts, i
         if (e < experts) {
             int64_t lo = offsets[e];
             lo = lo < 0 ? 0 : lo > rows ? rows : lo;
-            before = lo / 32 + e <= p;
+            before = lo / U + e <= p;
         }
         n += __popcll(__ballot(before));
     }

@@ -1,6 +1,6 @@
 // quant_grouped.hip -- MXFP4 quantization of rows grouped by expert, along
 // cols (the operands of the forward and Dgrad products), along rows (those of
-// Wgrad: each expert's tokens in 32-token blocks of their own, the last one
+// Wgrad: each expert's tokens in stages of 256 of their own, the last one
 // filled up with zeros) or both from one read.
 //
 // Bound by HBM like the quantizers without groups, and built the same way: a
@@ -8,7 +8,8 @@
 // LDS by DMA in 512-byte row segments (16-byte chunks swizzled by row mod 4 so
 // that both the column reads and the row reads are free of bank conflicts).
 // A unit's rows belong to one expert (grouped.hpp); rows past its last one are
-// out-of-range loads and read as zero.  Along rows a thread owns a column and
+// out-of-range loads and read as zero, so that the rows output holds whole
+// 256-token stages, zeros behind an expert's last token, and Wgrad has no tail.  Along rows a thread owns a column and
 // its 32 values of the unit, along cols one 32-element block of a row.
 #include "fp4_launch.hpp"
 #include "grouped.hpp"
@@ -37,28 +38,35 @@ __global__ __launch_bounds__(kCols) void quant_grouped(
     __shared__ __attribute__((aligned(1024))) uint16_t tile[kUnits][32 * kCols];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t units = rows / 32 + experts, nbc = cols / 32;
+    // units of the cols output, blocks of the rows output
+    const int64_t units = rows / 32 + experts, blocks = 8 * (rows / 256 + experts), nbc = cols / 32;
     const int gx = (cols + kCols - 1) / kCols;
     const int c0 = (int)(blockIdx.x % gx) * kCols;
     const int64_t p0 = (int64_t)(blockIdx.x / gx) * kUnits;
     int64_t r0[kUnits], local[kUnits];
-    int expert[kUnits], left[kUnits];                  // rows of the unit (0: none)
+    int expert[kUnits], left[kUnits];                  // rows of the unit
+    bool live[kUnits];                                 // whether anything is written for it
 #pragma unroll
     for (int t = 0; t < kUnits; ++t) {
         const int64_t p = p0 + t;
         left[t] = 0;
         r0[t] = local[t] = 0;
-        expert[t] = p < units ? expert_of_unit(offsets, experts, rows, p) : -1;
+        live[t] = false;
+        // two blocks of the rows output are of one stage, hence of one expert
+        if (ROWS) expert[t] = t ? expert[0] : expert_of_unit<256>(offsets, experts, rows, p / 8);
+        else expert[t] = p < units ? expert_of_unit<32>(offsets, experts, rows, p) : -1;
         if (expert[t] < 0) continue;
         const RowRange rr = expert_rows(offsets, expert[t], rows);
-        local[t] = p - (rr.lo / 32 + expert[t]);
+        local[t] = p - (ROWS ? 8 * (rr.lo / 256 + expert[t]) : rr.lo / 32 + expert[t]);
         r0[t] = rr.lo + 32 * local[t];
         left[t] = rr.hi - r0[t] >= 32 ? 32 : rr.hi > r0[t] ? (int)(rr.hi - r0[t]) : 0;
         left[t] = __builtin_amdgcn_readfirstlane(left[t]);
+        live[t] = left[t] > 0 || (ROWS && local[t] / 8 * 256 < rr.hi - rr.lo);
     }
+    if (!live[0] && !live[1]) return;
 #pragma unroll
     for (int t = 0; t < kUnits; ++t) {
-        if (left[t] == 0) continue;
+        if (!live[t]) continue;
         const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
             (void*)(x + r0[t] * cols), (short)0, left[t] * cols * 2, 0x00020000);
 #pragma unroll
@@ -77,23 +85,23 @@ __global__ __launch_bounds__(kCols) void quant_grouped(
 #pragma unroll
     for (int q = 0; q < 4; ++q) colpos[q] = (((tid >> 3) ^ q) << 3) | (tid & 7);
     const int col = c0 + tid;
+    uint32_t bytes = 0;
 #pragma unroll
     for (int t = 0; t < kUnits; ++t) {
-        if (left[t] == 0) continue;
-        const int64_t p = p0 + t;
+        if (!live[t]) continue;
         if constexpr (ROWS) {
             if (col < cols) {
+                const int64_t p = p0 + t;
                 float a[32];
 #pragma unroll
                 for (int r = 0; r < 32; ++r)
                     a[r] = __uint_as_float((uint32_t)tile[t][r * kCols + colpos[r & 3]] << 16);
                 uint32_t wd[4];
-                const uint64_t g = ((uint64_t)col * (uint64_t)(32 * units) + (uint64_t)(32 * p)) >> 2;
+                const uint64_t g = ((uint64_t)col * (uint64_t)(32 * blocks) + (uint64_t)(32 * p)) >> 2;
                 const uint32_t byte = quant_block32<HADN, SR>(a, rot.sign_word, rot.norm, sr_rows, g, wd);
-                *reinterpret_cast<uint4*>(codes_r + tiled_offset(col, p, units)) =
+                *reinterpret_cast<uint4*>(codes_r + tiled_offset(col, p, blocks)) =
                     make_uint4(wd[0], wd[1], wd[2], wd[3]);
-                const int64_t sg = (r0[t] - 32 * local[t]) / 256 + expert[t] + local[t] / 8;
-                scales_r[(sg * cols + col) * 8 + (local[t] & 7)] = (uint8_t)byte;
+                bytes |= byte << (8 * t);
             }
         }
         if constexpr (COLS) {
@@ -115,20 +123,26 @@ __global__ __launch_bounds__(kCols) void quant_grouped(
                 const uint64_t g = ((uint64_t)(r0[t] + r) * (uint64_t)cols + (uint64_t)cb) >> 2;
                 const uint32_t byte =
                     quant_block32<ROWS ? 0 : HADN, SR>(a, rot.sign_word, rot.norm, sr_cols, g, wd);
-                const int64_t pr = 32 * p + r, blk = cb / 32;
+                const int64_t first = r0[t] - 32 * local[t];          // the expert's first row
+                const int64_t pr = 32 * (first / 32 + expert[t] + local[t]) + r, blk = cb / 32;
                 *reinterpret_cast<uint4*>(codes_c + tiled_offset(pr, blk, nbc)) =
                     make_uint4(wd[0], wd[1], wd[2], wd[3]);
                 scales_c[((blk >> 3) * (32 * units) + pr) * 8 + (blk & 7)] = (uint8_t)byte;
             }
         }
     }
+    // the two blocks' scales of a column: both blocks are written (a stage is
+    // written whole) and p0 is even
+    if constexpr (ROWS)
+        if (col < cols)
+            *reinterpret_cast<uint16_t*>(scales_r + ((p0 >> 3) * cols + col) * 8 + (p0 & 7)) = (uint16_t)bytes;
 }
 
 template <int HADN, bool SR, bool ROWS, bool COLS>
 hipError_t launch_one(const void* x, const int* offsets, int64_t experts, int64_t rows, int64_t cols, Rotation rot,
                       uint64_t sr_rows, uint64_t sr_cols, uint8_t* cr, uint8_t* sr, uint8_t* cc, uint8_t* sc,
                       hipStream_t st) {
-    const int64_t units = rows / 32 + experts;
+    const int64_t units = ROWS ? 8 * (rows / 256 + experts) : rows / 32 + experts;
     const int64_t blocks = ((cols + kCols - 1) / kCols) * ((units + kUnits - 1) / kUnits);
     return launch(&quant_grouped<HADN, SR, ROWS, COLS>, dim3((unsigned)blocks), dim3(kCols), st, (const uint16_t*)x,
                   offsets, (int)experts, rows, (int)cols, rot, sr_rows, sr_cols, cr, sr, cc, sc);

@@ -275,11 +275,11 @@ int64_t experts_of(const at::Tensor& offsets, const at::Tensor& like) {
 }
 
 Shape grouped_codes(int64_t rows, int64_t cols, int64_t E, bool along_rows) {
-    const int64_t units = FP4_GROUPED_UNITS(rows, E);
-    return along_rows ? Shape{cols / 32, units, 512} : Shape{units, cols / 32, 512};
+    return along_rows ? Shape{cols / 32, 8 * FP4_GROUPED_STAGES(rows, E), 512}
+                      : Shape{FP4_GROUPED_UNITS(rows, E), cols / 32, 512};
 }
 Shape grouped_scales(int64_t rows, int64_t cols, int64_t E, bool along_rows) {
-    return along_rows ? Shape{FP4_GROUPED_SCALE_GROUPS(rows, E), cols, 8}
+    return along_rows ? Shape{FP4_GROUPED_STAGES(rows, E), cols, 8}
                       : scale_shape(32 * FP4_GROUPED_UNITS(rows, E), cols);
 }
 

@@ -425,15 +425,15 @@ fp4_status fp4_gemm_decode(const uint8_t* a, const uint8_t* as, fp4_format fmt, 
  *   along cols (forward, Dgrad): an MXFP4 operand of 32 U rows of `cols`
  *     elements (codes [U][cols/32][512], scales [ceil(cols/256)][32 U][8]);
  *     row offsets[e] + i is the operand's row 32 (offsets[e] / 32 + e) + i.
- *   along rows (Wgrad): codes of `cols` rows of 32 U elements
- *     ([cols/32][U][512]; unit u of expert e, its rows 32 u .. 32 u + 31 with
- *     zeros past the last one, is block offsets[e] / 32 + e + u) and scales
- *     [FP4_GROUPED_SCALE_GROUPS(rows, experts)][cols][8] with the byte of that
- *     unit at group offsets[e] / 256 + e + u / 8, position u % 8.
- * Units, rows and bytes that belong to no row of an expert are not written.
+ *   along rows (Wgrad): an MXFP4 operand of `cols` rows of 256 G elements, G =
+ *     FP4_GROUPED_STAGES(rows, experts) = rows / 256 + experts (codes
+ *     [cols/32][8 G][512], scales [G][cols][8]); row offsets[e] + i of x is the
+ *     element 256 (offsets[e] / 256 + e) + i of each of its rows, and zeros
+ *     fill an expert's last 256 elements.
+ * Units, stages, rows and bytes that belong to no expert are not written.
  */
 #define FP4_GROUPED_UNITS(rows, experts) ((int64_t)(rows) / 32 + (int64_t)(experts))
-#define FP4_GROUPED_SCALE_GROUPS(rows, experts) ((int64_t)(rows) / 256 + (int64_t)(experts))
+#define FP4_GROUPED_STAGES(rows, experts) ((int64_t)(rows) / 256 + (int64_t)(experts))
 
 /*
  * fp4_quantize_grouped -- bf16 x[rows, cols] with rows grouped by expert to
@@ -442,8 +442,8 @@ fp4_status fp4_gemm_decode(const uint8_t* a, const uint8_t* as, fp4_format fmt, 
  * Rotation, rounding and scales as fp4_hadamard_quantize on each expert's rows
  * alone; with both outputs the rotation is the rows output's and the cols
  * output is not rotated.  Stochastic rounding: element (row, col) of the cols
- * output has index row * cols + col (row of x), element i of unit p of column
- * col of the rows output index col * 32 U + 32 p + i.
+ * output has index row * cols + col (row of x), element i of row col of the
+ * rows output index col * 256 G + i.
  * Requirements: cols % 32 == 0, cols < 2^24; 0 < rows < 2^31; 1 <= experts <=
  * 1024; pointers 16-byte aligned (offsets 4).
  */
@@ -475,8 +475,8 @@ fp4_status fp4_gemm_grouped(const uint8_t* a, const uint8_t* as, fp4_format fmt,
  * from dY [rows, N] and X [rows, K] quantized along rows by
  * fp4_quantize_grouped with the same offsets, had, had_n and sign_seed.  dw is
  * [experts, N, K] in `out`, overwritten; that of an expert without rows is zero.
- * Requirements: N % 32 == 0, K % 32 == 0 (the quantizer's); 32 (rows / 32 +
- * experts) < 2^24; at most 2^24 - 1 output tiles of 256 x 256; pointers 16-byte
+ * Requirements: N % 32 == 0, K % 32 == 0 (the quantizer's); 256 (rows / 256 +
+ * experts) < 2^24, and (rows / 256 + experts) max(N, K) < 2^28; at most 2^24 - 1 output tiles of 256 x 256; pointers 16-byte
  * aligned (offsets 4).
  */
 fp4_status fp4_gemm_grouped_wgrad(const uint8_t* dytq, const uint8_t* dyts, const uint8_t* xtq,

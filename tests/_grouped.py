@@ -36,6 +36,18 @@ def padded_rows(rows, offsets):
     return at, rows // 32 + len(offsets) - 1
 
 
+def staged_rows(rows, offsets):
+    """Element of the rows output's contraction of each row of x, -1 for rows
+    of no expert; number of stages; the stages that are written."""
+    at = np.full(rows, -1)
+    used = []
+    for e, (lo, hi) in enumerate(zip(offsets, offsets[1:])):
+        first = lo // 256 + e
+        at[lo:hi] = 256 * first + np.arange(hi - lo)
+        used += range(first, first + (hi - lo + 255) // 256)
+    return at, rows // 256 + len(offsets) - 1, used
+
+
 def random_mx4(rng, rows, K, low=117, high=127):
     codes = rng.integers(0, 256, (rows, K // 2), dtype=np.uint8)
     return codes, rng.integers(low, high, (rows, K // 32), dtype=np.uint8)

@@ -7,7 +7,7 @@ import torch
 
 import fp4_precision_gemms_amd as F
 import oracle as O
-from _grouped import SPLITS, check, dev_offsets, grouped_operand, operand, padded_rows, random_mx4, values
+from _grouped import SPLITS, check, dev_offsets, grouped_operand, operand, random_mx4, staged_rows, values
 from _mx_ref import mxfp4_values
 from _util import bf16_bits, need_gpu, say, to_gpu_bf16
 
@@ -45,13 +45,13 @@ def test_many_rows(split, N, K, out_dtype):
 
 def quantized_rows(bits, rows, offsets, had_n, had, seed, rnd=F.RTN, sr=0):
     """(GPU codes and scales, with every byte that is not written 0xFF; the
-    oracle's values [C, 32 units])."""
+    oracle's values [C, 256 stages])."""
     E = len(offsets) - 1
     out = [torch.full(s, 0xFF, dtype=torch.uint8, device="cuda")
            for s in F.grouped_shapes(rows, bits.shape[1], E, F.AXIS_ROWS)]
     q = F.fp4_quantize_grouped(to_gpu_bf16(bits), dev_offsets(offsets), F.AXIS_ROWS, had_n, had, seed, rnd, sr, out=out)
-    at, units = padded_rows(rows, offsets)
-    full = np.zeros((32 * units, bits.shape[1]), np.uint16)
+    at, stages, _ = staged_rows(rows, offsets)
+    full = np.zeros((256 * stages, bits.shape[1]), np.uint16)
     full[at[at >= 0]] = bits[at >= 0]
     return q, mxfp4_values(*O.quant_mx(full, O.AXIS_ROWS, had_n, had, seed, rnd, sr))
 
@@ -72,6 +72,6 @@ def test_wgrad(split, N, K, out_dtype):
     torch.cuda.synchronize()
     ref, mag = np.zeros((E, N, K)), np.zeros((E, N, K))
     for e, (lo, hi) in enumerate(zip(offsets, offsets[1:])):
-        span = slice(32 * (lo // 32 + e), 32 * (lo // 32 + e + (hi - lo + 31) // 32))
+        span = slice(256 * (lo // 256 + e), 256 * (lo // 256 + e) + hi - lo + (lo - hi) % 32)
         ref[e], mag[e] = vdy[:, span] @ vx[:, span].T, np.abs(vdy[:, span]) @ np.abs(vx[:, span]).T
     check(got, ref, mag)

@@ -6,7 +6,7 @@ import torch
 
 import fp4_precision_gemms_amd as F
 import oracle as O
-from _grouped import SPLITS, dev_offsets, padded_rows
+from _grouped import SPLITS, dev_offsets, padded_rows, staged_rows
 from _util import bf16_bits, need_gpu, say, sentinel_u8, to_gpu_bf16, ungroup_scales, untile_codes
 
 pytestmark = pytest.mark.gpu
@@ -19,20 +19,17 @@ MODES = {"plain": (32, F.HAD_NONE, 0, F.RTN), "had32": (32, F.HAD_DET, 0, F.RTN)
 def check_rows(codes, scales, bits, rows, offsets, mode, seed):
     """Every written byte of the rows output; every other byte still 0xCD."""
     had_n, had, sign_seed, rnd = mode
-    at, units = padded_rows(rows, offsets)
-    full = np.zeros((32 * units, bits.shape[1]), np.uint16)
+    at, stages, used = staged_rows(rows, offsets)
+    C = bits.shape[1]
+    full = np.zeros((256 * stages, C), np.uint16)
     full[at[at >= 0]] = bits[at >= 0]
     rc, rs = O.quant_mx(full, O.AXIS_ROWS, had_n, had, sign_seed, rnd, seed)
-    C = bits.shape[1]
-    used = np.unique(at[at >= 0] // 32)
-    want = np.full((C, units, 16), 0xCD, np.uint8)
-    want[:, used] = rc.reshape(C, units, 16)[:, used]
-    assert np.array_equal(untile_codes(codes.cpu().numpy(), C).reshape(C, units, 16), want)
-    ws = np.full(tuple(scales.shape), 0xCD, np.uint8)
-    for e, (lo, hi) in enumerate(zip(offsets, offsets[1:])):
-        for u in range((hi - lo + 31) // 32):
-            ws[lo // 256 + e + u // 8, :, u % 8] = rs[:, lo // 32 + e + u]
-    assert np.array_equal(scales.cpu().numpy(), ws)
+    want = np.full((C, stages, 128), 0xCD, np.uint8)
+    want[:, used] = rc.reshape(C, stages, 128)[:, used]
+    assert np.array_equal(untile_codes(codes.cpu().numpy(), C).reshape(C, stages, 128), want)
+    ws = np.full((C, stages, 8), 0xCD, np.uint8)
+    ws[:, used] = rs.reshape(C, stages, 8)[:, used]
+    assert np.array_equal(scales.cpu().numpy(), ws.transpose(1, 0, 2))
 
 
 def check_cols(codes, scales, bits, rows, offsets, mode, seed):
