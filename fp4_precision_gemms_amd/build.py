@@ -29,7 +29,7 @@ CALIB_LIB_PATH = os.path.join(HERE, "libfp4calib.so")
 BINDING_PATH = os.path.join(HERE, "_torch_binding.so")
 
 SOURCES = ["fp4_abi.cpp", "quant_mx.hip", "gemm_mx.hip", "nvfp4.hip", "norm_mx.hip", "gemm_few.hip",
-           "quant_grouped.hip"]
+           "gemm_depth.hip", "quant_grouped.hip"]
 CALIB_SOURCES = ["calib_mfma.hip"]
 ARCH = "gfx950"
 

@@ -291,7 +291,11 @@ fp4_status fp4_gemm_grouped(const uint8_t* a, const uint8_t* as, fp4_format fmt,
     if (!offsets) return FP4_ERR_NULL;
     if (const fp4_status s = check_grouped_product(a, as, fmt, wq, ws, experts, rows, N, K, c, out)) return s;
     if (!aligned4(offsets)) return FP4_ERR_ALIGN;
-    if (fmt == FP4_FMT_MXFP4 && fp4dev::many_rows(rows, experts))
+    // Over 32 rows an expert on average the few-row kernel, which reads the
+    // weights once per 64 rows, is the slower one (40 experts of 736 x 1120:
+    // 12.2 against 12.7 us at 50 rows, 16.5 and 13.0 at 100; 8 experts of 14336
+    // x 4096: 78 and 46 us at 64).
+    if (fmt == FP4_FMT_MXFP4 && rows > 32 * experts && fp4dev::row_groups_fit(experts, rows, N, K))
         return from_hip(fp4dev::launch_gemm_row_groups(a, as, offsets, experts, rows, wq, ws, N, K, c,
                                                        out == FP4_OUT_BF16, (hipStream_t)stream));
     return from_hip(fp4dev::launch_gemm_few(a, as, fmt == FP4_FMT_MXFP8, offsets, wq, ws, rows, experts, N, K, c,
@@ -313,8 +317,12 @@ fp4_status fp4_gemm_grouped_wgrad(const uint8_t* dytq, const uint8_t* dyts, cons
     if (!aligned16(dytq) || !aligned16(dyts) || !aligned16(xtq) || !aligned16(xts) || !aligned4(offsets) ||
         !aligned16(dw))
         return FP4_ERR_ALIGN;
-    return from_hip(fp4dev::launch_gemm_depth_groups(dytq, dyts, xtq, xts, offsets, experts, rows, N, K, dw,
-                                                     out == FP4_OUT_BF16, (hipStream_t)stream));
+    // Up to 1024 rows an expert on average the small tiles (32 experts of 2048
+    // x 2048, bf16: 70 against 112 us at 100 rows, 126 and 134 at 800; 8 experts
+    // of 14336 x 4096: 482 and 504 us at 1024, 769 and 671 at 2048).
+    auto* const run = rows <= 1024 * experts ? &fp4dev::launch_gemm_depth_short : &fp4dev::launch_gemm_depth_groups;
+    return from_hip(run(dytq, dyts, xtq, xts, offsets, experts, rows, N, K, dw, out == FP4_OUT_BF16,
+                        (hipStream_t)stream));
 }
 
 const char* fp4_status_string(fp4_status status) {

@@ -79,18 +79,19 @@ hipError_t launch_gemm_few(const uint8_t* a, const uint8_t* as, int a_e4m3, cons
                            const uint8_t* ws, int64_t rows, int64_t experts, int64_t N, int64_t K, void* c,
                            int out_bf16, hipStream_t st);
 
-// Whether a grouped product takes the large tiles: over 64 rows an expert on
-// average the few-row kernel reads the weights more than once.
-inline bool many_rows(int64_t rows, int64_t experts) { return rows > 64 * experts; }
-
-// The same for many MXFP4 rows per expert; and dW_e = A_e B_e^T, each expert a
-// span of the contraction (rows) of A and B, C [experts, M, N].
+// C[rows, N], each expert's MXFP4 rows times its weight on the large tiles;
+// and C [experts, M, N], each expert its span of A's and B's contraction: on
+// the large tiles, or on small ones where an expert's span is short.
+bool row_groups_fit(int64_t experts, int64_t rows, int64_t N, int64_t K);
 hipError_t launch_gemm_row_groups(const uint8_t* aq, const uint8_t* as, const int* offsets, int64_t experts,
                                   int64_t rows, const uint8_t* wq, const uint8_t* ws, int64_t N, int64_t K, void* c,
                                   int out_bf16, hipStream_t st);
 hipError_t launch_gemm_depth_groups(const uint8_t* aq, const uint8_t* as, const uint8_t* bq, const uint8_t* bs,
                                     const int* offsets, int64_t experts, int64_t rows, int64_t M, int64_t N, void* c,
                                     int out_bf16, hipStream_t st);
+hipError_t launch_gemm_depth_short(const uint8_t* aq, const uint8_t* as, const uint8_t* bq, const uint8_t* bs,
+                                   const int* offsets, int64_t experts, int64_t rows, int64_t M, int64_t N, void* c,
+                                   int out_bf16, hipStream_t st);
 
 // MXFP4 quantization of rows grouped by expert, along rows (codes_r) and / or
 // along cols (codes_c).

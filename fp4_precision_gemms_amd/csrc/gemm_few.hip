@@ -32,35 +32,13 @@
 #include "fp4_device.hpp"
 #include "fp4_launch.hpp"
 #include "grouped.hpp"
+#include "mx_mfma.hpp"
 
 namespace fp4dev {
 namespace {
 
-typedef int v4i __attribute__((ext_vector_type(4)));
-typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-
-constexpr int kBufferWord3 = 0x00020000;   // raw buffer, 32-bit data format
-constexpr uint32_t kOob = 0x80000000u;     // a buffer offset past any range: reads zero
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int64_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, kBufferWord3);
-}
-__device__ __forceinline__ v4i load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-    return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
-}
-
-// Bytes of the scale word of blocks first .. first + 3 that lie past the last
-// block set to 127 (2^0): their codes read as zero, and a stray 0xFF (NaN)
-// would not.
-__device__ __forceinline__ uint32_t past_end_to_one(uint32_t w, int first, int nb) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (first + i >= nb) w = (w & ~(0xFFu << (8 * i))) | (127u << (8 * i));
-    return w;
-}
 
 // A block's 32 elements times 2^(byte - 127) as bf16, 8 consecutive ones per
 // vector.  Byte 255 gives NaN and byte 0 2^-127 (the conversions take the
@@ -131,7 +109,7 @@ __global__ __launch_bounds__(64 * W) void gemm_few(
     SB += (int64_t)e * groups * N * 8;
     const int nleft = (int)((N - n0) < 16 * NT ? (N - n0) : 16 * NT);
     const __amdgpu_buffer_rsrc_t rb =
-        buffer(B + (n0 / 32) * gstride, ((n0 + nleft + 31) / 32 - n0 / 32) * gstride);
+        raw_buffer(B + (n0 / 32) * gstride, ((n0 + nleft + 31) / 32 - n0 / 32) * gstride);
     uint32_t offb[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -143,14 +121,14 @@ __global__ __launch_bounds__(64 * W) void gemm_few(
         const int mleft = (int)((hi - m0) < 16 * MT ? (hi - m0) : 16 * MT);
         const int64_t p0 = first + (m0 - lo);          // the tile's first row in the A operand
         const __amdgpu_buffer_rsrc_t ra =
-            A8 ? buffer(A + p0 * K, (int64_t)mleft * K)
-               : buffer(A + (p0 / 32) * gstride, (((p0 & 31) + mleft + 31) / 32) * gstride);
-        const __amdgpu_buffer_rsrc_t rsa = buffer(SA + (A8 ? p0 * nb : 0), A8 ? (int64_t)mleft * nb : 0);
+            A8 ? raw_buffer(A + p0 * K, (int64_t)mleft * K)
+               : raw_buffer(A + (p0 / 32) * gstride, (((p0 & 31) + mleft + 31) / 32) * gstride);
+        const __amdgpu_buffer_rsrc_t rsa = raw_buffer(SA + (A8 ? p0 * nb : 0), A8 ? (int64_t)mleft * nb : 0);
         auto load = [&](int g) {
             Group<A8, MT, NT> t;
             const int b0 = 8 * g + quad;
             const bool in[2] = {b0 < nb, b0 + 4 < nb};
-            const __amdgpu_buffer_rsrc_t rsb = buffer(SB + ((int64_t)g * N + n0) * 8, nleft * 8);
+            const __amdgpu_buffer_rsrc_t rsb = raw_buffer(SB + ((int64_t)g * N + n0) * 8, nleft * 8);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -179,7 +157,7 @@ __global__ __launch_bounds__(64 * W) void gemm_few(
                     for (int s = 0; s < 2; ++s)
                         t.a[i][s][0] = load16(ra, in[s] ? o + (uint32_t)(b0 + 4 * s) * 512 : kOob);
                     const auto v = __builtin_amdgcn_raw_buffer_load_b64(
-                        buffer(SA + ((int64_t)g * arows + p0) * 8, mleft * 8), m * 8, 0, 0);
+                        raw_buffer(SA + ((int64_t)g * arows + p0) * 8, mleft * 8), m * 8, 0, 0);
                     t.as[i] = make_uint2(v[0], v[1]);
                 }
             }
@@ -190,13 +168,13 @@ __global__ __launch_bounds__(64 * W) void gemm_few(
             if (8 * g + 8 > nb) {
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
-                    t.ws[j] = make_uint2(past_end_to_one(t.ws[j].x, 8 * g, nb),
-                                         past_end_to_one(t.ws[j].y, 8 * g + 4, nb));
+                    t.ws[j] = make_uint2(mask_scale_word(t.ws[j].x, 8 * g, nb),
+                                         mask_scale_word(t.ws[j].y, 8 * g + 4, nb));
                 if constexpr (!A8)
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
-                        t.as[i] = make_uint2(past_end_to_one(t.as[i].x, 8 * g, nb),
-                                             past_end_to_one(t.as[i].y, 8 * g + 4, nb));
+                        t.as[i] = make_uint2(mask_scale_word(t.as[i].x, 8 * g, nb),
+                                             mask_scale_word(t.as[i].y, 8 * g + 4, nb));
             }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {

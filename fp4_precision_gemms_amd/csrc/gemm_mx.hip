@@ -53,22 +53,16 @@
 #include "fp4_device.hpp"
 #include "fp4_launch.hpp"
 #include "grouped.hpp"
+#include "mx_mfma.hpp"
 
 #include <atomic>
 
 namespace fp4dev {
 namespace {
 
-typedef int v4i __attribute__((ext_vector_type(4)));
-typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v16f __attribute__((ext_vector_type(16)));
-typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void_t;
 
 constexpr int kXcds = 8;
-constexpr int kBufferWord3 = 0x00020000;   // raw buffer, 32-bit data format
-constexpr uint32_t kOob = 0x80000000u;     // a buffer offset past any range: reads zero
-
 // s_waitcnt immediate: vmcnt(n) with lgkmcnt(0).
 constexpr int wait_vm_lgkm0(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0070; }
 
@@ -96,23 +90,6 @@ __device__ __forceinline__ void dma4_to_lds(__amdgpu_buffer_rsrc_t rsrc, void* l
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void_t*)lds_dst, 4, voff, soff, 0, 0);
 }
 
-// Scaled FP4 MFMA (32x32x64, both operands E2M1, fp32 accumulate) taking the
-// E8M0 scales from byte S of the scale registers.
-template <int S>
-__device__ __forceinline__ v16f mfma_fp4(v8i b, v8i a, v16f c, uint32_t sb, uint32_t sa) {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, 4, 4, S, (int)sb, S, (int)sa);
-}
-
-// The scale word a lane feeds the MFMAs of one 256-k stage: the stage's 8
-// block scales of its row are bytes 0..7 of (hi:lo); k-step s uses block
-// 2 s + (lane / 32), so lane half h keeps bytes h, 2 + h, 4 + h, 6 + h, and
-// k-step s reads byte s of the word -- one byte permute per stage instead of
-// a shift before every MFMA.  Formed when the stage starts: at load time it
-// would wait for loads issued stages ahead.
-__device__ __forceinline__ uint32_t stage_scale_word(uint32_t lo, uint32_t hi, int h) {
-    return __builtin_amdgcn_perm(hi, lo, h ? 0x07050301u : 0x06040200u);
-}
-
 // Maps the hardware block index to a (tile_m, tile_n) pair: XCD-contiguous
 // runs of logical tiles, grouped GM tile-rows at a time.
 template <int GM>
@@ -126,16 +103,6 @@ __device__ __forceinline__ void tile_of_block(int b, int nb, int tm, int tn, int
     const int r = t - group * per_group;
     tile_m = first_m + r % gm;
     tile_n = r / gm;
-}
-
-// Bytes of a scale word for blocks first .. first+3 that lie at or past nb
-// (the unused tail of the last k-group) set to 127 (2^0; their codes are
-// zero).
-__device__ __forceinline__ uint32_t mask_scale_word(uint32_t w, int64_t first, int64_t nb) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (first + i >= nb) w = (w & ~(0xFFu << (8 * i))) | (127u << (8 * i));
-    return w;
 }
 
 // A 16-byte store of C marked non-temporal: with whole 128-byte lines per
@@ -166,18 +133,13 @@ constexpr int kEpiRegion = 32 * kEpiRow;        // 32 rows per wave
 // with a B of its own; M is the row count of A's grouped layout, a tile never
 // crosses into the next expert, and FAST's full tiles hold for the columns and
 // the contraction only.  kDepthGroups -- each expert owns whole stages of the
-// contraction and an output [M, N] of its own.  With groups FAST means its
-// loads alone: the contraction is a multiple of 256 and tiles may be partial
-// (code rows past the operand read as zero, scale rows as whatever follows
-// them: they reach no output that is stored); stages before the first are
-// clamped like those past the last, and take scales that make them vanish.
+// contraction and an output [M, N] of its own.  Groups take FAST's loads, with
+// tiles that may be partial (code rows past the operand read as zero, scale
+// rows as whatever follows them: they reach no output that is stored) and any
+// contraction: stages before the first are clamped like those past the last,
+// and take scales that make them vanish, like the last stage's blocks past the
+// end.
 enum { kNoGroups = 0, kRowGroups = 1, kDepthGroups = 2 };
-
-struct GroupArgs {
-    const int* offsets;
-    int experts;
-    int64_t rows;         // of the tensor that the offsets split
-};
 
 // One int per expert in LDS; Which tells several arrays apart.
 template <int Which>
@@ -202,7 +164,7 @@ __device__ __forceinline__ void gemm_tiles(
     constexpr int kVmStage = FM + (FAST ? 1 : 2) + 2 * kKS + 2;
     static_assert(FM >= 4 && FM <= 8, "tile rows");
     static_assert(!(FAST && KTAIL), "the fast path has no contraction tail");
-    static_assert(GROUP != kDepthGroups || FAST, "an expert's span is whole stages");
+    static_assert(!GROUP || FAST, "groups take the fast loads");
     constexpr int kWaitStage = 2 * kVmStage - 2;
     static_assert(kWaitStage <= 63, "vmcnt range");
     static_assert(kSlots * kSlot <= 160 * 1024, "LDS");
@@ -549,15 +511,20 @@ __device__ __forceinline__ void gemm_tiles(
     // One stage from slot u (its k-step 0 fragments and scales already in
     // registers).  Stage kt + 3 is loaded into slot (u + 3) mod 4, B scales
     // of stage kt + 2 into the B scale ring, B k-steps 8 ahead into the B ring.
+    // Groups, fast path: the bytes of the last stage's scale words (byte s:
+    // block 2 s + h of the stage) that are of blocks of the operand.
+    const int last_bytes = GROUP == kRowGroups ? (int)(nb - 8 * (nk - 1) - h + 1) / 2 : 4;
+    const uint32_t last_keep = last_bytes >= 4 ? ~0u : (1u << (8 * last_bytes)) - 1;
     auto run_stage = [&](int u, int kt) {
         uint8_t* const ahead = slots[(u + 3) % kSlots];
         ASc& nsa = asc[(u + 1) & 1];
         SWords sw = stage_words(asc[u & 1], bsc[u], kt);
         if constexpr (GROUP && FAST) {
-            // A stage before the first holds stage 0's bytes: with both scales
-            // 2^-127 its products vanish.  (Branches around such a stage made
-            // the compiler spill hundreds of registers.)
-            const uint32_t keep = kt < 0 ? 0u : ~0u;
+            // A stage before the first holds stage 0's bytes, and blocks past
+            // the last one whatever follows: with both scales 2^-127 their
+            // products vanish.  (Branches around a stage made the compiler
+            // spill hundreds of registers.)
+            const uint32_t keep = kt < 0 ? 0u : kt == nk - 1 ? last_keep : ~0u;
 #pragma unroll
             for (int i = 0; i < FM; ++i) sw.a[i] &= keep;
 #pragma unroll
@@ -735,9 +702,12 @@ __device__ __forceinline__ void gemm_tiles(
         // aligned) elements go one by one.
         // Groups, fast path: the tile's rows of C as one buffer; this lane's
         // offset in its first row, out of range for columns past N.  What lies
-        // past the last row is past the buffer's end.
+        // past the last row is past the buffer's end.  Non-temporal where
+        // the rows are whole lines, in bf16 too: 8 experts of 14336 x 4096, 128-row tiles, 512 rows each 156 us
+        // against 180 with plain stores.
         constexpr int kOut = OBF16 ? 2 : 4;
         const uint32_t row_bytes = (uint32_t)N * kOut;
+        const bool lines = row_bytes % 128 == 0;
         const __amdgpu_buffer_rsrc_t rc = __builtin_amdgcn_make_buffer_rsrc(
             (void*)((uint8_t*)C + (ebase + em0 * N + en0) * kOut), (short)0, (int)((erows * N - en0) * kOut),
             kBufferWord3);
@@ -768,13 +738,15 @@ __device__ __forceinline__ void gemm_tiles(
                     const uint32_t o = offc + (uint32_t)(32 * i + 4 * k) * row_bytes;
                     if constexpr (OBF16) {
                         typedef uint32_t v2u __attribute__((ext_vector_type(2)));
-                        __builtin_amdgcn_raw_buffer_store_b64(
-                            v2u{bf16_rne(f[k].x) | (bf16_rne(f[k].y) << 16), bf16_rne(f[k].z) | (bf16_rne(f[k].w) << 16)},
-                            rc, o, 0, 0);
+                        const v2u v{bf16_rne(f[k].x) | (bf16_rne(f[k].y) << 16),
+                                    bf16_rne(f[k].z) | (bf16_rne(f[k].w) << 16)};
+                        if (lines) __builtin_amdgcn_raw_buffer_store_b64(v, rc, o, 0, 2);
+                        else __builtin_amdgcn_raw_buffer_store_b64(v, rc, o, 0, 0);
                     } else {
                         typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-                        __builtin_amdgcn_raw_buffer_store_b128(
-                            __builtin_bit_cast(v4u, f[k]), rc, o, 0, 2);   // non-temporal, as below
+                        const v4u v = __builtin_bit_cast(v4u, f[k]);
+                        if (lines) __builtin_amdgcn_raw_buffer_store_b128(v, rc, o, 0, 2);
+                        else __builtin_amdgcn_raw_buffer_store_b128(v, rc, o, 0, 0);
                     }
                 }
                 continue;
@@ -862,12 +834,12 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_tn(
     gemm_tiles<FM, GM, FAST, KTAIL, OBF16, ACC, kNoGroups>(A, SA, B, SB, M, N, K, C, tiles_m, tiles_n, GroupArgs{});
 }
 
-template <int FM, int GM, bool FAST, bool KTAIL, bool OBF16, int GROUP>
+template <int FM, int GM, bool OBF16, int GROUP>
 __global__ __launch_bounds__(kThreads) void gemm_mx_grouped(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ SA, const uint8_t* __restrict__ B,
     const uint8_t* __restrict__ SB, int64_t M, int64_t N, int64_t K, void* __restrict__ C,
     int tiles_m, int tiles_n, const GroupArgs ga) {
-    gemm_tiles<FM, GM, FAST, KTAIL, OBF16, false, GROUP>(A, SA, B, SB, M, N, K, C, tiles_m, tiles_n, ga);
+    gemm_tiles<FM, GM, true, false, OBF16, false, GROUP>(A, SA, B, SB, M, N, K, C, tiles_m, tiles_n, ga);
 }
 
 // Compute units of each device, queried once per device (concurrent first
@@ -946,36 +918,43 @@ hipError_t launch_gemm_mx(const uint8_t* aq, const uint8_t* as, const uint8_t* b
 }
 
 namespace {
-template <int FM, bool FAST, bool KTAIL, int GROUP>
+template <int FM, int GROUP>
 hipError_t launch_grouped(const uint8_t* aq, const uint8_t* as, const uint8_t* bq, const uint8_t* bs, int64_t M,
                           int64_t N, int64_t K, void* c, int out_bf16, int64_t most, int64_t tm, int64_t tn,
                           const GroupArgs& ga, hipStream_t st) {
     const int64_t cus = cu_count();
     const dim3 grid((unsigned)(most < cus ? most : cus));
-    return out_bf16 ? launch(&gemm_mx_grouped<FM, kGroupRows, FAST, KTAIL, true, GROUP>, grid, dim3(kThreads), st, aq,
-                             as, bq, bs, M, N, K, c, (int)tm, (int)tn, ga)
-                    : launch(&gemm_mx_grouped<FM, kGroupRows, FAST, KTAIL, false, GROUP>, grid, dim3(kThreads), st, aq,
-                             as, bq, bs, M, N, K, c, (int)tm, (int)tn, ga);
+    return out_bf16 ? launch(&gemm_mx_grouped<FM, kGroupRows, true, GROUP>, grid, dim3(kThreads), st, aq, as, bq, bs,
+                             M, N, K, c, (int)tm, (int)tn, ga)
+                    : launch(&gemm_mx_grouped<FM, kGroupRows, false, GROUP>, grid, dim3(kThreads), st, aq, as, bq, bs,
+                             M, N, K, c, (int)tm, (int)tn, ga);
 }
 
-template <int FM>
-hipError_t launch_row_groups(const uint8_t* aq, const uint8_t* as, const int* offsets, int64_t experts, int64_t rows,
-                             const uint8_t* wq, const uint8_t* ws, int64_t N, int64_t K, void* c, int out_bf16,
-                             hipStream_t st) {
-    const int64_t M = 32 * (rows / 32 + experts), tn = (N + kBN - 1) / kBN;
-    const int64_t most = (rows / (32 * FM) + experts) * tn;     // tiles of any split, at most
-    const GroupArgs ga{offsets, (int)experts, rows};
-    // whole stages, rows of whole 16-byte pieces, and offsets within 31 bits
-    if (K % 256 == 0 && N % 4 == 0 && N < (INT64_C(1) << 21) && (K / 256) * (M > N ? M : N) * 8 < (INT64_C(1) << 31))
-        return launch_grouped<FM, true, false, kRowGroups>(aq, as, wq, ws, M, N, K, c, out_bf16, most, 0, tn, ga, st);
-    return launch_grouped<FM, false, true, kRowGroups>(aq, as, wq, ws, M, N, K, c, out_bf16, most, 0, tn, ga, st);
-}
 }  // namespace
+
+// Whether the large tiles' 32-bit offsets hold: rows of C in whole 16-byte
+// pieces, a tile of C and an operand's scales within 2 GiB.
+bool row_groups_fit(int64_t experts, int64_t rows, int64_t N, int64_t K) {
+    const int64_t M = 32 * (rows / 32 + experts);
+    return N % 4 == 0 && N < (INT64_C(1) << 21) && (K + 255) / 256 * (M > N ? M : N) * 8 < (INT64_C(1) << 31);
+}
 
 hipError_t launch_gemm_row_groups(const uint8_t* aq, const uint8_t* as, const int* offsets, int64_t experts,
                                   int64_t rows, const uint8_t* wq, const uint8_t* ws, int64_t N, int64_t K, void* c,
                                   int out_bf16, hipStream_t st) {
-    return launch_row_groups<8>(aq, as, offsets, experts, rows, wq, ws, N, K, c, out_bf16, st);
+    const int64_t M = 32 * (rows / 32 + experts), tn = (N + kBN - 1) / kBN, cus = cu_count();
+    const GroupArgs ga{offsets, (int)experts, rows};
+    // Tile rows: rounds of the persistent grid times a tile's time, with half a
+    // tile per expert for its last one.  A tile of 128 rows takes 0.53-0.62 of
+    // one of 256 (it loads as much of B): 8 experts of 14336 x 4096, 256 rows
+    // each 92 against 100 us, 2048 rows 574 against 526; 32 experts of 2048 x
+    // 2048, 200 rows 33 against 40.
+    auto rounds = [&](int64_t bm) { return ((rows / bm + (experts + 1) / 2) * tn + cus - 1) / cus; };
+    if (58 * rounds(128) < 100 * rounds(256))
+        return launch_grouped<4, kRowGroups>(aq, as, wq, ws, M, N, K, c, out_bf16, (rows / 128 + experts) * tn, 0, tn,
+                                             ga, st);
+    return launch_grouped<8, kRowGroups>(aq, as, wq, ws, M, N, K, c, out_bf16, (rows / 256 + experts) * tn, 0, tn, ga,
+                                         st);
 }
 
 hipError_t launch_gemm_depth_groups(const uint8_t* aq, const uint8_t* as, const uint8_t* bq, const uint8_t* bs,
@@ -983,8 +962,8 @@ hipError_t launch_gemm_depth_groups(const uint8_t* aq, const uint8_t* as, const 
                                     int out_bf16, hipStream_t st) {
     const int64_t K = 256 * (rows / 256 + experts);             // of the grouped layout
     const int64_t tm = (M + 255) / 256, tn = (N + kBN - 1) / kBN;
-    return launch_grouped<8, true, false, kDepthGroups>(aq, as, bq, bs, M, N, K, c, out_bf16, tm * tn * experts, tm,
-                                                        tn, GroupArgs{offsets, (int)experts, rows}, st);
+    return launch_grouped<8, kDepthGroups>(aq, as, bq, bs, M, N, K, c, out_bf16, tm * tn * experts, tm, tn,
+                                           GroupArgs{offsets, (int)experts, rows}, st);
 }
 
 }  // namespace fp4dev

@@ -22,6 +22,14 @@ struct RowRange {
     int64_t lo, hi;
 };
 
+// What a grouped product needs besides its operands; `rows` are those of the
+// tensor that the offsets split.
+struct GroupArgs {
+    const int* offsets;
+    int experts;
+    int64_t rows;
+};
+
 // Rows of expert e, clamped to the tensor whatever the offsets say.
 __device__ __forceinline__ RowRange expert_rows(const int* offsets, int e, int64_t rows) {
     int64_t lo = offsets[e], hi = offsets[e + 1];

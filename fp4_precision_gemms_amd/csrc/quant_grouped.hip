@@ -4,13 +4,15 @@
 // filled up with zeros) or both from one read.
 //
 // Bound by HBM like the quantizers without groups, and built the same way: a
-// workgroup takes two consecutive 32-row units x 256 columns, moved global ->
+// workgroup takes one or two consecutive 32-row units x 256 columns, global ->
 // LDS by DMA in 512-byte row segments (16-byte chunks swizzled by row mod 4 so
 // that both the column reads and the row reads are free of bank conflicts).
 // A unit's rows belong to one expert (grouped.hpp); rows past its last one are
 // out-of-range loads and read as zero, so that the rows output holds whole
-// 256-token stages, zeros behind an expert's last token, and Wgrad has no tail.  Along rows a thread owns a column and
-// its 32 values of the unit, along cols one 32-element block of a row.
+// 256-token stages, zeros behind an expert's last token, and Wgrad has no tail.
+// Along rows a thread owns a column and its 32 values of the unit, along cols
+// one 32-element block of a row.  [16384, 4096] over 8 experts along cols 37 us
+// (4.6 TB/s), along rows 40; [16384, 14336] both ways 142 us (5.0 TB/s).
 #include "fp4_launch.hpp"
 #include "grouped.hpp"
 #include "mx_device.hpp"
@@ -20,7 +22,7 @@ namespace {
 
 typedef __attribute__((address_space(3))) void lds_void_t;
 
-constexpr int kCols = 256, kUnits = 2;
+constexpr int kCols = 256;
 constexpr uint32_t kOob = 0x80000000u;
 
 struct Rotation {
@@ -30,7 +32,7 @@ struct Rotation {
 
 // HADN: rotation size along the axis (0 = none); with both outputs it is the
 // rows output's and the cols output is not rotated.
-template <int HADN, bool SR, bool ROWS, bool COLS>
+template <int HADN, bool SR, bool ROWS, bool COLS, int kUnits>
 __global__ __launch_bounds__(kCols) void quant_grouped(
     const uint16_t* __restrict__ x, const int* __restrict__ offsets, int experts, int64_t rows, int cols,
     Rotation rot, uint64_t sr_rows, uint64_t sr_cols, uint8_t* __restrict__ codes_r, uint8_t* __restrict__ scales_r,
@@ -63,10 +65,10 @@ __global__ __launch_bounds__(kCols) void quant_grouped(
         left[t] = __builtin_amdgcn_readfirstlane(left[t]);
         live[t] = left[t] > 0 || (ROWS && local[t] / 8 * 256 < rr.hi - rr.lo);
     }
-    if (!live[0] && !live[1]) return;
+    if (!live[0] && !live[kUnits - 1]) return;
 #pragma unroll
     for (int t = 0; t < kUnits; ++t) {
-        if (!live[t]) continue;
+        if (left[t] == 0) continue;
         const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
             (void*)(x + r0[t] * cols), (short)0, left[t] * cols * 2, 0x00020000);
 #pragma unroll
@@ -92,13 +94,15 @@ __global__ __launch_bounds__(kCols) void quant_grouped(
         if constexpr (ROWS) {
             if (col < cols) {
                 const int64_t p = p0 + t;
-                float a[32];
+                uint32_t wd[4] = {}, byte = 0;             // what a block of zeros gives
+                if (left[t] > 0) {
+                    float a[32];
 #pragma unroll
-                for (int r = 0; r < 32; ++r)
-                    a[r] = __uint_as_float((uint32_t)tile[t][r * kCols + colpos[r & 3]] << 16);
-                uint32_t wd[4];
-                const uint64_t g = ((uint64_t)col * (uint64_t)(32 * blocks) + (uint64_t)(32 * p)) >> 2;
-                const uint32_t byte = quant_block32<HADN, SR>(a, rot.sign_word, rot.norm, sr_rows, g, wd);
+                    for (int r = 0; r < 32; ++r)
+                        a[r] = __uint_as_float((uint32_t)tile[t][r * kCols + colpos[r & 3]] << 16);
+                    const uint64_t g = ((uint64_t)col * (uint64_t)(32 * blocks) + (uint64_t)(32 * p)) >> 2;
+                    byte = quant_block32<HADN, SR>(a, rot.sign_word, rot.norm, sr_rows, g, wd);
+                }
                 *reinterpret_cast<uint4*>(codes_r + tiled_offset(col, p, blocks)) =
                     make_uint4(wd[0], wd[1], wd[2], wd[3]);
                 bytes |= byte << (8 * t);
@@ -131,21 +135,31 @@ __global__ __launch_bounds__(kCols) void quant_grouped(
             }
         }
     }
-    // the two blocks' scales of a column: both blocks are written (a stage is
-    // written whole) and p0 is even
+    // a column's scales: all blocks are written (a stage is written whole)
     if constexpr (ROWS)
-        if (col < cols)
-            *reinterpret_cast<uint16_t*>(scales_r + ((p0 >> 3) * cols + col) * 8 + (p0 & 7)) = (uint16_t)bytes;
+        if (col < cols) {
+            uint8_t* const s = scales_r + ((p0 >> 3) * cols + col) * 8 + (p0 & 7);
+            if constexpr (kUnits == 2) *reinterpret_cast<uint16_t*>(s) = (uint16_t)bytes;
+            else *s = (uint8_t)bytes;
+        }
 }
+
+// Units per workgroup: two (pairs of codes and scale bytes leave together),
+// one where that leaves CUs idle and a unit's latency is the time (1999 rows
+// over 40 experts, 736 and 1120 columns: 8.2 and 6.8 us, 14.3 and 15.1 with two).
+constexpr int64_t kFewWorkgroups = 1024;
 
 template <int HADN, bool SR, bool ROWS, bool COLS>
 hipError_t launch_one(const void* x, const int* offsets, int64_t experts, int64_t rows, int64_t cols, Rotation rot,
                       uint64_t sr_rows, uint64_t sr_cols, uint8_t* cr, uint8_t* sr, uint8_t* cc, uint8_t* sc,
                       hipStream_t st) {
     const int64_t units = ROWS ? 8 * (rows / 256 + experts) : rows / 32 + experts;
-    const int64_t blocks = ((cols + kCols - 1) / kCols) * ((units + kUnits - 1) / kUnits);
-    return launch(&quant_grouped<HADN, SR, ROWS, COLS>, dim3((unsigned)blocks), dim3(kCols), st, (const uint16_t*)x,
-                  offsets, (int)experts, rows, (int)cols, rot, sr_rows, sr_cols, cr, sr, cc, sc);
+    const int64_t gx = (cols + kCols - 1) / kCols;
+    if (gx * units / 2 < kFewWorkgroups)
+        return launch(&quant_grouped<HADN, SR, ROWS, COLS, 1>, dim3((unsigned)(gx * units)), dim3(kCols), st,
+                      (const uint16_t*)x, offsets, (int)experts, rows, (int)cols, rot, sr_rows, sr_cols, cr, sr, cc, sc);
+    return launch(&quant_grouped<HADN, SR, ROWS, COLS, 2>, dim3((unsigned)(gx * ((units + 1) / 2))), dim3(kCols), st,
+                  (const uint16_t*)x, offsets, (int)experts, rows, (int)cols, rot, sr_rows, sr_cols, cr, sr, cc, sc);
 }
 
 template <int HADN, bool SR, typename... A>
