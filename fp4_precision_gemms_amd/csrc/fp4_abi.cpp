@@ -317,10 +317,10 @@ fp4_status fp4_gemm_grouped_wgrad(const uint8_t* dytq, const uint8_t* dyts, cons
     if (!aligned16(dytq) || !aligned16(dyts) || !aligned16(xtq) || !aligned16(xts) || !aligned4(offsets) ||
         !aligned16(dw))
         return FP4_ERR_ALIGN;
-    // Up to 1024 rows an expert on average the small tiles (32 experts of 2048
-    // x 2048, bf16: 70 against 112 us at 100 rows, 126 and 134 at 800; 8 experts
-    // of 14336 x 4096: 482 and 504 us at 1024, 769 and 671 at 2048).
-    auto* const run = rows <= 1024 * experts ? &fp4dev::launch_gemm_depth_short : &fp4dev::launch_gemm_depth_groups;
+    // Up to 512 rows an expert on average the small tiles (32 experts of 2048 x
+    // 2048, bf16: 65 against 75 us at 250 rows, 84 and 91 at 500, 108 and 103 at
+    // 800; 8 experts of 14336 x 4096: 283 and 286 us at 512, 435 and 378 at 1024).
+    auto* const run = rows <= 512 * experts ? &fp4dev::launch_gemm_depth_short : &fp4dev::launch_gemm_depth_groups;
     return from_hip(run(dytq, dyts, xtq, xts, offsets, experts, rows, N, K, dw, out == FP4_OUT_BF16,
                         (hipStream_t)stream));
 }

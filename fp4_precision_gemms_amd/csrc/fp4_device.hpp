@@ -21,6 +21,12 @@ __device__ __forceinline__ uint32_t bf16_rne(float f) {
     if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0x7FC0u;
     return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
 }
+// Two values at once by V_CVT_PK_BF16_F32: the same rounding, a NaN stays a NaN.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    typedef float v2f __attribute__((ext_vector_type(2)));
+    typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{lo, hi}, v2b));
+}
 __device__ __forceinline__ float bf16_value(uint32_t b) { return __uint_as_float(b << 16); }
 
 // ---------------------------------------------------------------------------

@@ -1,5 +1,5 @@
 // gemm_depth.hip -- the weight gradients dW_e = dY_e^T X_e of experts with up to
-// some hundred tokens each, on small tiles.
+// a few hundred tokens each, on small tiles.
 //
 // The 256 x 256 tiles of gemm_mx.hip take one workgroup per CU and some 10 us
 // from the first load to the last store; with a few stages of contraction most
@@ -12,9 +12,11 @@
 //   - V_MFMA_SCALE_F32_32X32X64_F8F6F4 as in gemm_mx.hip, B first, so that the
 //     accumulators hold C^T and leave through a wave's own LDS region as whole
 //     128-byte lines, stored non-temporally where the rows of C are whole lines
-//     (32 experts of 2048 x 2048 with 50 tokens: 67 us, 88 with plain stores).
-// Bound by the output's bytes for few tokens (8 x 14336 x 4096 in bf16, 64
-// tokens an expert: 221 us, 4.3 TB/s), by the loads through L1 for many (a wave
+//     (32 experts of 2048 x 2048 with 50 tokens: 67 us, 88 with plain stores), in
+//     bf16 through V_CVT_PK_BF16_F32 and 16 bytes a lane (50 us; 8 bytes a lane
+//     and integer rounding took 63).
+// Bound by the output's bytes for few tokens (8 x 14336 x 4096 in bf16, 256
+// tokens an expert: 194 us, 4.8 TB/s), by the loads through L1 for many (a wave
 // loads 16 KB a stage for 16 MFMAs: 1024 cycles of a CU's L1 for four waves,
 // 512 of MFMA).  64 x 128 a wave loads a quarter less but leaves two
 // workgroups a CU: 75 us against 70 for 32 x 2048 x 2048 and 100 tokens.
@@ -26,7 +28,7 @@
 namespace fp4dev {
 namespace {
 
-typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 constexpr int kTile = 128;
 constexpr int kRow = 64 * 4 + 16;          // a staged row of 64 fp32 columns, padded
@@ -40,18 +42,30 @@ __device__ __forceinline__ void put(T* p, T v) {
 }
 
 // C[e][m, n] for one expert's tile; K: elements per row of the grouped layout.
-// Workgroups: column tiles fastest, gx of them (a multiple of 8, so that a
-// column tile stays on one XCD), then row tiles, then experts.
+// Workgroups go round-robin over the 8 XCDs.  From 16 experts on (`per_xcd`) an
+// expert's tiles all run on one XCD, whose L2 then holds its operands and joins
+// the lines of C that two tiles share (40 experts of 736 x 1120: 21 us, 30 with
+// the tiles spread); fewer experts would leave XCDs idle behind the longest, so
+// there the column tiles, gx of them (a multiple of 8), are spread (8 experts
+// of 14336 x 4096, 1024 tokens: 489 against 603 us).
+constexpr int64_t kPerXcdExperts = 16;
+
 template <bool OBF16, bool LINES>
 __global__ __launch_bounds__(256) void gemm_mx_depth(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ SA, const uint8_t* __restrict__ B,
     const uint8_t* __restrict__ SB, int64_t M, int64_t N, int64_t K, void* __restrict__ C, int tiles_m, int gx,
-    const GroupArgs ga) {
+    int per_xcd, const GroupArgs ga) {
     __shared__ __attribute__((aligned(16))) uint8_t stage[4][32 * kRow];
     const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int y = blockIdx.x / gx, e = y / tiles_m;
-    const int64_t n0 = (int64_t)(blockIdx.x % gx) * kTile + 64 * (wave >> 1);
+    int b = blockIdx.x;
+    if (per_xcd) {
+        const int per = gx * tiles_m, i = b >> 3;
+        b = (i / per * 8 + (b & 7)) * per + i % per;
+    }
+    const int y = b / gx, e = y / tiles_m;
+    if (e >= ga.experts) return;
+    const int64_t n0 = (int64_t)(b % gx) * kTile + 64 * (wave >> 1);
     const int64_t m0 = (int64_t)(y % tiles_m) * kTile + 64 * (wave & 1);
     if (n0 >= N || m0 >= M) return;                    // a wave of its own: no barrier below
     const RowRange r = expert_rows(ga.offsets, e, ga.rows);
@@ -110,10 +124,11 @@ __global__ __launch_bounds__(256) void gemm_mx_depth(
 
     // register t of acc[i][j] in lane l is row m = 32 i + l mod 32, column n =
     // 32 j + 8 (t / 4) + 4 (l / 32) + t mod 4: staged 32 rows at a time, read
-    // back as four consecutive n per lane, 16 lanes per row (M and N are
+    // back and stored 16 bytes a lane (8 bf16 or 4 fp32 of a row; M and N are
     // multiples of 32)
+    constexpr int kPer = OBF16 ? 8 : 4, kLanes = 64 / kPer;     // columns a lane, lanes a row
     uint8_t* const reg = stage[wave];
-    const int lr = lane >> 4, c4 = (lane & 15) * 4;
+    const int lr = lane / kLanes, c = lane % kLanes * kPer;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         if (32 * i >= rows) break;
@@ -125,16 +140,18 @@ __global__ __launch_bounds__(256) void gemm_mx_depth(
                     make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int row = 4 * k + lr;
-            const v4f f = *reinterpret_cast<const v4f*>(reg + row * kRow + c4 * 4);
-            if (c4 >= cols) continue;
-            const int64_t at = ((int64_t)e * M + m0 + 32 * i + row) * N + n0 + c4;
-            if constexpr (OBF16)
-                put<LINES>(reinterpret_cast<v2u*>(reinterpret_cast<uint16_t*>(C) + at),
-                           v2u{bf16_rne(f[0]) | (bf16_rne(f[1]) << 16), bf16_rne(f[2]) | (bf16_rne(f[3]) << 16)});
-            else
-                put<LINES>(reinterpret_cast<v4f*>(reinterpret_cast<float*>(C) + at), f);
+        for (int k = 0; k < kLanes / 2; ++k) {
+            const int row = 64 / kLanes * k + lr;
+            const v4f* const f = reinterpret_cast<const v4f*>(reg + row * kRow + c * 4);
+            if (c >= cols) continue;
+            const int64_t at = ((int64_t)e * M + m0 + 32 * i + row) * N + n0 + c;
+            if constexpr (OBF16) {
+                const v4f a = f[0], b = f[1];
+                put<LINES>(reinterpret_cast<v4u*>(reinterpret_cast<uint16_t*>(C) + at),
+                           v4u{bf16_pair(a[0], a[1]), bf16_pair(a[2], a[3]), bf16_pair(b[0], b[1]), bf16_pair(b[2], b[3])});
+            } else {
+                put<LINES>(reinterpret_cast<v4f*>(reinterpret_cast<float*>(C) + at), f[0]);
+            }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
@@ -146,13 +163,14 @@ hipError_t launch_gemm_depth_short(const uint8_t* aq, const uint8_t* as, const u
                                    const int* offsets, int64_t experts, int64_t rows, int64_t M, int64_t N, void* c,
                                    int out_bf16, hipStream_t st) {
     const int64_t K = 256 * (rows / 256 + experts), tm = (M + kTile - 1) / kTile;
-    const int64_t gx = ((N + kTile - 1) / kTile + 7) / 8 * 8;
+    const bool per_xcd = experts >= kPerXcdExperts;
+    const int64_t cols = (N + kTile - 1) / kTile, gx = per_xcd ? cols : (cols + 7) / 8 * 8;
     const GroupArgs ga{offsets, (int)experts, rows};
-    const dim3 grid((unsigned)(gx * tm * experts));
+    const dim3 grid((unsigned)(gx * tm * (per_xcd ? (experts + 7) / 8 * 8 : experts)));
     const bool lines = N * (out_bf16 ? 2 : 4) % 128 == 0;
     auto* const k = out_bf16 ? (lines ? &gemm_mx_depth<true, true> : &gemm_mx_depth<true, false>)
                              : (lines ? &gemm_mx_depth<false, true> : &gemm_mx_depth<false, false>);
-    return launch(k, grid, dim3(256), st, aq, as, bq, bs, M, N, K, c, (int)tm, (int)gx, ga);
+    return launch(k, grid, dim3(256), st, aq, as, bq, bs, M, N, K, c, (int)tm, (int)gx, (int)per_xcd, ga);
 }
 
 }  // namespace fp4dev

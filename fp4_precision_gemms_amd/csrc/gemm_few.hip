@@ -238,8 +238,7 @@ __global__ __launch_bounds__(64 * W) void gemm_few(
             if constexpr (OBF16) {
                 uint16_t* p = reinterpret_cast<uint16_t*>(C) + at;
                 if (whole) {
-                    *reinterpret_cast<uint2*>(p) = make_uint2(bf16_rne(s[0]) | (bf16_rne(s[1]) << 16),
-                                                              bf16_rne(s[2]) | (bf16_rne(s[3]) << 16));
+                    *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3]));
                 } else {
                     for (int k = 0; k < 4 && n + k < nleft; ++k) p[k] = (uint16_t)bf16_rne(s[k]);
                 }

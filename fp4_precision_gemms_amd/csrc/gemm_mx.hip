@@ -56,6 +56,7 @@
 #include "mx_mfma.hpp"
 
 #include <atomic>
+#include <type_traits>
 
 namespace fp4dev {
 namespace {
@@ -136,9 +137,9 @@ constexpr int kEpiRegion = 32 * kEpiRow;        // 32 rows per wave
 // contraction and an output [M, N] of its own.  Groups take FAST's loads, with
 // tiles that may be partial (code rows past the operand read as zero, scale
 // rows as whatever follows them: they reach no output that is stored) and any
-// contraction: stages before the first are clamped like those past the last,
-// and take scales that make them vanish, like the last stage's blocks past the
-// end.
+// contraction: stages before the first are clamped like those past the last;
+// row groups give them, and the last stage's blocks past the end, scales that
+// make them vanish, depth groups do not multiply them.
 enum { kNoGroups = 0, kRowGroups = 1, kDepthGroups = 2 };
 
 // One int per expert in LDS; Which tells several arrays apart.
@@ -511,19 +512,19 @@ __device__ __forceinline__ void gemm_tiles(
     // One stage from slot u (its k-step 0 fragments and scales already in
     // registers).  Stage kt + 3 is loaded into slot (u + 3) mod 4, B scales
     // of stage kt + 2 into the B scale ring, B k-steps 8 ahead into the B ring.
-    // Groups, fast path: the bytes of the last stage's scale words (byte s:
-    // block 2 s + h of the stage) that are of blocks of the operand.
-    const int last_bytes = GROUP == kRowGroups ? (int)(nb - 8 * (nk - 1) - h + 1) / 2 : 4;
+    // Row groups: the bytes of the last stage's scale words (byte s: block
+    // 2 s + h of the stage) that are of blocks of the operand.
+    const int last_bytes = (int)(nb - 8 * (nk - 1) - h + 1) / 2;
     const uint32_t last_keep = last_bytes >= 4 ? ~0u : (1u << (8 * last_bytes)) - 1;
-    auto run_stage = [&](int u, int kt) {
+    // (Without `live`: its loads alone.)
+    auto run_stage = [&](int u, int kt, bool live = true) {
         uint8_t* const ahead = slots[(u + 3) % kSlots];
         ASc& nsa = asc[(u + 1) & 1];
         SWords sw = stage_words(asc[u & 1], bsc[u], kt);
-        if constexpr (GROUP && FAST) {
+        if constexpr (GROUP == kRowGroups) {
             // A stage before the first holds stage 0's bytes, and blocks past
             // the last one whatever follows: with both scales 2^-127 their
-            // products vanish.  (Branches around a stage made the compiler
-            // spill hundreds of registers.)
+            // products vanish.
             const uint32_t keep = kt < 0 ? 0u : kt == nk - 1 ? last_keep : ~0u;
 #pragma unroll
             for (int i = 0; i < FM; ++i) sw.a[i] &= keep;
@@ -533,7 +534,7 @@ __device__ __forceinline__ void gemm_tiles(
 #pragma unroll
         for (int s = 0; s < kKS - 1; ++s) {
             read_afrags(u, s + 1, (s + 1) & 1);
-            mfmas(s, s & 1, (4 * u + s) % kRing, sw);
+            if (live) mfmas(s, s & 1, (4 * u + s) % kRing, sw);
 #pragma unroll
             for (int j = 0; j < FN; ++j) fb[(4 * u + s) % kRing][j] = load_b(4 * kt + s + kRing, j);
             dma_a(kt + 3, ahead, kdma(s), kdma(s + 1), s == 0);
@@ -561,7 +562,7 @@ __device__ __forceinline__ void gemm_tiles(
         barrier_after_wait();
         read_ascales((u + 1) % kSlots, kt + 1, nsa);
         read_afrags((u + 1) % kSlots, 0, 0);
-        mfmas(kKS - 1, 1, (4 * u + 3) % kRing, sw);
+        if (live) mfmas(kKS - 1, 1, (4 * u + 3) % kRing, sw);
 #pragma unroll
         for (int j = 0; j < FN; ++j) fb[(4 * u + 3) % kRing][j] = load_b(4 * kt + 3 + kRing, j);
         constexpr int kM = FM * FN, kDs = 2 * FM;
@@ -607,7 +608,9 @@ __device__ __forceinline__ void gemm_tiles(
     constexpr int kPro = FN + 2 * kKS * FN + 2 * (FM + (FAST ? 1 : 2)) + FN;
     // stores of a full tile's epilogue per wave (32-row pieces, 4 rows per
     // store instruction)
-    constexpr int kEpiStores = FM * 8;
+    // (16 bytes a lane and 8 rows per store with groups and a bf16 output)
+    constexpr int kEpiRows = GROUP && OBF16 ? 8 : 4;
+    constexpr int kEpiStores = FM * (32 / kEpiRows);
 
     bool early = false;   // this tile's prologue was issued during the previous epilogue
     // Staggered start: workgroup b begins b x 64 cycles late (about 8 us for
@@ -658,13 +661,25 @@ __device__ __forceinline__ void gemm_tiles(
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
         read_ascales(0, kfirst, asc[0]);
         read_afrags(0, 0, 0);
-        for (int kt = kfirst; kt < nk; kt += kSlots) {
-            run_stage(0, kt);
-            run_stage(1, kt + 1);
-            run_stage(2, kt + 2);
-            run_stage(3, kt + 3);
-        }
-
+        // The tile's stages and its epilogue, after `dead` stages before the
+        // first that are loads only (their slots and registers hold nothing of
+        // the tile).
+        auto tile = [&](auto dead) {
+            constexpr int D = decltype(dead)::value;
+            int kt = kfirst;
+            if constexpr (D > 0) {
+                run_stage(0, kt, false);
+                run_stage(1, kt + 1, D < 2);
+                run_stage(2, kt + 2, D < 3);
+                run_stage(3, kt + 3);
+                kt += kSlots;
+            }
+            for (; kt < nk; kt += kSlots) {
+                run_stage(0, kt);
+                run_stage(1, kt + 1);
+                run_stage(2, kt + 2);
+                run_stage(3, kt + 3);
+            }
         // the prefetches past the last stage must land before the slots are
         // refilled (and before the workgroup goes away)
         __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
@@ -711,8 +726,9 @@ __device__ __forceinline__ void gemm_tiles(
         const __amdgpu_buffer_rsrc_t rc = __builtin_amdgcn_make_buffer_rsrc(
             (void*)((uint8_t*)C + (ebase + em0 * N + en0) * kOut), (short)0, (int)((erows * N - en0) * kOut),
             kBufferWord3);
-        const uint32_t offc = en0 + 64 * wave + (lane & 15) * 4 < N
-                                  ? (uint32_t)(lane >> 4) * row_bytes + (uint32_t)(64 * wave + (lane & 15) * 4) * kOut
+        const int er = lane / (64 / kEpiRows), ec = lane % (64 / kEpiRows) * kEpiRows;
+        const uint32_t offc = en0 + 64 * wave + ec < N
+                                  ? (uint32_t)er * row_bytes + (uint32_t)(64 * wave + ec) * kOut
                                   : kOob;
 
         uint8_t* const reg = lds3 + wave * kEpiRegion;
@@ -729,25 +745,26 @@ __device__ __forceinline__ void gemm_tiles(
                                     acc[i][j][4 * q + 3]);
                 }
             if constexpr (GROUP && FAST) {
-                float4 f[8];
+                // 16 bytes a lane: 8 bf16 or 4 fp32 of a row (bf16 with integer
+                // rounding and 8 bytes a lane: 540 us where this takes 496, 8
+                // experts of 2048 rows, 14336 x 4096)
+                typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+                v4u o[kEpiStores / FM];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    f[k] = *reinterpret_cast<const float4*>(reg + (4 * k + lr) * kEpiRow + c4 * 4);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t o = offc + (uint32_t)(32 * i + 4 * k) * row_bytes;
+                for (int k = 0; k < kEpiStores / FM; ++k) {
+                    const v4f* const f = reinterpret_cast<const v4f*>(reg + (kEpiRows * k + er) * kEpiRow + ec * 4);
                     if constexpr (OBF16) {
-                        typedef uint32_t v2u __attribute__((ext_vector_type(2)));
-                        const v2u v{bf16_rne(f[k].x) | (bf16_rne(f[k].y) << 16),
-                                    bf16_rne(f[k].z) | (bf16_rne(f[k].w) << 16)};
-                        if (lines) __builtin_amdgcn_raw_buffer_store_b64(v, rc, o, 0, 2);
-                        else __builtin_amdgcn_raw_buffer_store_b64(v, rc, o, 0, 0);
+                        const v4f a = f[0], b = f[1];
+                        o[k] = v4u{bf16_pair(a[0], a[1]), bf16_pair(a[2], a[3]), bf16_pair(b[0], b[1]), bf16_pair(b[2], b[3])};
                     } else {
-                        typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-                        const v4u v = __builtin_bit_cast(v4u, f[k]);
-                        if (lines) __builtin_amdgcn_raw_buffer_store_b128(v, rc, o, 0, 2);
-                        else __builtin_amdgcn_raw_buffer_store_b128(v, rc, o, 0, 0);
+                        o[k] = __builtin_bit_cast(v4u, f[0]);
                     }
+                }
+#pragma unroll
+                for (int k = 0; k < kEpiStores / FM; ++k) {
+                    const uint32_t at = offc + (uint32_t)(32 * i + kEpiRows * k) * row_bytes;
+                    if (lines) __builtin_amdgcn_raw_buffer_store_b128(o[k], rc, at, 0, 2);
+                    else __builtin_amdgcn_raw_buffer_store_b128(o[k], rc, at, 0, 0);
                 }
                 continue;
             }
@@ -822,6 +839,23 @@ __device__ __forceinline__ void gemm_tiles(
                     }
                 }
             }
+        }
+        };
+        if constexpr (GROUP == kDepthGroups) {
+            // An expert's stages are rarely a multiple of four, and up to three
+            // multiplied in vain cost: 8 experts of 2048 tokens, 14336 x 4096
+            // 632 us with them, 581 without.  Each count has code of its own
+            // from the first stage to the last store: where the accumulators of
+            // two paths met, the compiler spilled hundreds of registers.  (Row
+            // groups, with more registers in use, lost 5-10 % this way.)
+            switch (-kfirst) {
+                case 1: tile(std::integral_constant<int, 1>{}); break;
+                case 2: tile(std::integral_constant<int, 2>{}); break;
+                case 3: tile(std::integral_constant<int, 3>{}); break;
+                default: tile(std::integral_constant<int, 0>{}); break;
+            }
+        } else {
+            tile(std::integral_constant<int, 0>{});
         }
     }
 }
@@ -936,7 +970,7 @@ hipError_t launch_grouped(const uint8_t* aq, const uint8_t* as, const uint8_t* b
 // pieces, a tile of C and an operand's scales within 2 GiB.
 bool row_groups_fit(int64_t experts, int64_t rows, int64_t N, int64_t K) {
     const int64_t M = 32 * (rows / 32 + experts);
-    return N % 4 == 0 && N < (INT64_C(1) << 21) && (K + 255) / 256 * (M > N ? M : N) * 8 < (INT64_C(1) << 31);
+    return N % 8 == 0 && N < (INT64_C(1) << 21) && (K + 255) / 256 * (M > N ? M : N) * 8 < (INT64_C(1) << 31);
 }
 
 hipError_t launch_gemm_row_groups(const uint8_t* aq, const uint8_t* as, const int* offsets, int64_t experts,

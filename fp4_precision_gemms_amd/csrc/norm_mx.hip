@@ -45,7 +45,7 @@ __device__ __forceinline__ void unpack8(const uint4& w, float* a) {
 __device__ __forceinline__ uint4 pack8(const float* a) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = bf16_rne(a[2 * i]) | (bf16_rne(a[2 * i + 1]) << 16);
+    for (int i = 0; i < 4; ++i) w[i] = bf16_pair(a[2 * i], a[2 * i + 1]);
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
