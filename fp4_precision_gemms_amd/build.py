@@ -86,7 +86,7 @@ def _link_binding(obj: str) -> None:
 
     tmp = BINDING_PATH + ".tmp%d" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-shared", "-fPIC", obj, "-o", tmp,
-           "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python",
+           "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python",
            "-L", HERE, "-l:" + os.path.basename(LIB_PATH), "-Wl,-rpath,$ORIGIN"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:

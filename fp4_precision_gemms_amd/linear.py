@@ -18,12 +18,20 @@ backward needs (X^T and W^T codes), not the bf16 tensors.  Inputs and the
 weight are bf16; Y, dX and dW are returned in bf16 (each the fp32 GEMM
 result rounded to nearest even by the GEMM kernel).  This module only
 sequences library calls; all arithmetic runs in libfp4.so.
+
+MXFP4NormLinear puts the norm that feeds such a layer in front of it (residual
+added, output quantized without a pass of its own), MXFP4GroupedLinear is the
+layer of a mixture of experts: rows sorted by expert, one weight each.
 """
 from __future__ import annotations
 
 import torch
 
-from . import HAD_DET, HAD_NONE, OUT_BF16, RTN, fp4_gemm_mx, fp4_hadamard_quantize_dual
+from . import (AXIS_ROWS, FMT_MXFP4, HAD_DET, HAD_NONE, OUT_BF16, RTN, code_shape, fp4_gemm_grouped,
+               fp4_gemm_grouped_wgrad, fp4_gemm_mx, fp4_hadamard_quantize, fp4_hadamard_quantize_dual,
+               fp4_quantize_grouped_dual, fp4_rmsnorm_backward, fp4_rmsnorm_quantize, scale_shape)
+
+_SR_COLS = 0x9E3779B97F4A7C15      # tells the SR stream of the Dgrad operand from the Wgrad one's
 
 
 class MXFP4LinearFunction(torch.autograd.Function):
@@ -55,7 +63,7 @@ class MXFP4LinearFunction(torch.autograd.Function):
         # (Dgrad); the gradient may be rounded stochastically
         dytq, dyts, dyq, dys = fp4_hadamard_quantize_dual(dy, had_n, had, sign_seed, grad_rounding,
                                                           sr_seed, 32, HAD_NONE, 0, grad_rounding,
-                                                          sr_seed ^ 0x9E3779B97F4A7C15)
+                                                          sr_seed ^ _SR_COLS)
         dx = fp4_gemm_mx(dyq, dys, wtq, wts, out_dtype=OUT_BF16)       # [T, K]
         dw = fp4_gemm_mx(dytq, dyts, xtq, xts, out_dtype=OUT_BF16)     # [N, K]
         return dx, dw, None, None, None, None, None
@@ -78,3 +86,123 @@ class MXFP4Linear(torch.nn.Module):
     def forward(self, x):
         return MXFP4LinearFunction.apply(x, self.weight, self.had, self.had_n, self.sign_seed,
                                          self.grad_rounding, self.sr_seed)
+
+
+class MXFP4NormLinearFunction(torch.autograd.Function):
+    """(y, h) with h = x + residual and y = rmsnorm(h) w^T: x and residual
+    [T, K], norm weight [K], w [N, K] (all bf16, T, K and N multiples of 32).
+    The norm leaves its output quantized for Fprop; Wgrad's operand is
+    quantized from the norm rounded to bf16, rotated.  Both roundings are
+    passed straight through to the norm's gradient."""
+
+    @staticmethod
+    def forward(ctx, x, residual, norm_weight, w, eps: float = 1e-5, had: int = HAD_DET, had_n: int = 32,
+                sign_seed: int = 0, grad_rounding: int = RTN, sr_seed: int = 0):
+        ctx.set_materialize_grads(False)
+        x, w = x.contiguous(), w.contiguous()
+        residual = None if residual is None else residual.contiguous()
+        n = torch.empty_like(x)
+        nq, ns, h, rstd = fp4_rmsnorm_quantize(x, norm_weight, residual, eps, FMT_MXFP4, y=n)
+        ntq, nts = fp4_hadamard_quantize(n, AXIS_ROWS, had_n, had, sign_seed)
+        wtq, wts, wq, ws = fp4_hadamard_quantize_dual(w)
+        y = fp4_gemm_mx(nq, ns, wq, ws, out_dtype=OUT_BF16)
+        ctx.save_for_backward(h, rstd, norm_weight, ntq, nts, wtq, wts)
+        ctx.cfg = (residual is not None, had, had_n, sign_seed, grad_rounding, sr_seed)
+        return y, h
+
+    @staticmethod
+    def backward(ctx, dy, dh):
+        h, rstd, norm_weight, ntq, nts, wtq, wts = ctx.saved_tensors
+        added, had, had_n, sign_seed, grad_rounding, sr_seed = ctx.cfg
+        dh = None if dh is None else dh.to(torch.bfloat16).contiguous()
+        if dy is None:                 # y took no part
+            return (dh, dh if added else None) + (None,) * 8
+        dy = dy.to(torch.bfloat16).contiguous()
+        dytq, dyts, dyq, dys = fp4_hadamard_quantize_dual(dy, had_n, had, sign_seed, grad_rounding, sr_seed,
+                                                          rnd_cols=grad_rounding, sr_seed_cols=sr_seed ^ _SR_COLS)
+        dn = fp4_gemm_mx(dyq, dys, wtq, wts, out_dtype=OUT_BF16)
+        dw = fp4_gemm_mx(dytq, dyts, ntq, nts, out_dtype=OUT_BF16)
+        dx, dnorm = fp4_rmsnorm_backward(dn, h, norm_weight, rstd, dh)
+        return (dx, dx if added else None, dnorm.to(norm_weight.dtype), dw) + (None,) * 6
+
+
+class MXFP4NormLinear(torch.nn.Module):
+    """Residual addition, root-mean-square norm and a bias-free MXFP4 linear
+    layer: forward(x, residual) gives (y, h), h the new residual stream."""
+
+    def __init__(self, in_features: int, out_features: int, eps: float = 1e-5, had: int = HAD_DET, had_n: int = 32,
+                 grad_rounding: int = RTN, device=None):
+        super().__init__()
+        self.norm_weight = torch.nn.Parameter(torch.ones(in_features, dtype=torch.bfloat16, device=device))
+        self.weight = torch.nn.Parameter(torch.empty(out_features, in_features, dtype=torch.bfloat16, device=device))
+        self.eps, self.had, self.had_n, self.grad_rounding = eps, had, had_n, grad_rounding
+        self.sign_seed = 0
+        self.sr_seed = 0
+
+    def forward(self, x, residual=None):
+        return MXFP4NormLinearFunction.apply(x, residual, self.norm_weight, self.weight, self.eps, self.had,
+                                             self.had_n, self.sign_seed, self.grad_rounding, self.sr_seed)
+
+
+def quantize_experts(w: torch.Tensor):
+    """Both operands of each of the experts' weights w [E, N, K] (bf16, N and K
+    multiples of 32), as fp4_gemm_grouped takes them: (wtq, wts) for Dgrad,
+    (wq, ws) for the forward product."""
+    E, N, K = w.shape
+    shapes = (code_shape(K, N), scale_shape(K, N), code_shape(N, K), scale_shape(N, K))
+    out = tuple(torch.empty((E, *s), dtype=torch.uint8, device=w.device) for s in shapes)
+    for e in range(E):
+        fp4_hadamard_quantize_dual(w[e], out=[t[e] for t in out])
+    return out
+
+
+class MXFP4GroupedLinearFunction(torch.autograd.Function):
+    """y[r] = x[r] w[e]^T for the rows r of expert e: x [T, K] with rows sorted
+    by expert, offsets int32 [E + 1], w [E, N, K] (bf16, N and K multiples of
+    32).  Rows of no expert give zero rows of y and of x's gradient if `padded`
+    (else those are not set), and reach no weight."""
+
+    @staticmethod
+    def forward(ctx, x, offsets, w, padded: bool = False, had: int = HAD_DET, had_n: int = 32, sign_seed: int = 0,
+                grad_rounding: int = RTN, sr_seed: int = 0):
+        x, w = x.contiguous(), w.contiguous()
+        xtq, xts, xq, xs = fp4_quantize_grouped_dual(x, offsets, had_n, had, sign_seed)
+        wtq, wts, wq, ws = quantize_experts(w)
+        y = fp4_gemm_grouped(xq, xs, offsets, wq, ws, x.shape[0], out=_rows(x, w.shape[1], padded))
+        ctx.save_for_backward(offsets, xtq, xts, wtq, wts)
+        ctx.cfg = (x.shape[0], w.shape[2], padded, had, had_n, sign_seed, grad_rounding, sr_seed)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        offsets, xtq, xts, wtq, wts = ctx.saved_tensors
+        rows, K, padded, had, had_n, sign_seed, grad_rounding, sr_seed = ctx.cfg
+        dy = dy.to(torch.bfloat16).contiguous()
+        dytq, dyts, dyq, dys = fp4_quantize_grouped_dual(dy, offsets, had_n, had, sign_seed, grad_rounding, sr_seed,
+                                                         sr_seed ^ _SR_COLS)
+        dx = fp4_gemm_grouped(dyq, dys, offsets, wtq, wts, rows, out=_rows(dy, K, padded))
+        dw = fp4_gemm_grouped_wgrad(dytq, dyts, xtq, xts, offsets, rows)
+        return dx, None, dw, None, None, None, None, None, None
+
+
+def _rows(like: torch.Tensor, cols: int, padded: bool) -> torch.Tensor:
+    return (like.new_zeros if padded else like.new_empty)((like.shape[0], cols))
+
+
+class MXFP4GroupedLinear(torch.nn.Module):
+    """The bias-free linear layers of `experts` experts, whose products run in
+    MXFP4: forward(x, offsets) with the rows of x sorted by expert.  `padded`:
+    x may hold rows of no expert (see MXFP4GroupedLinearFunction)."""
+
+    def __init__(self, experts: int, in_features: int, out_features: int, padded: bool = False, had: int = HAD_DET,
+                 had_n: int = 32, grad_rounding: int = RTN, device=None):
+        super().__init__()
+        self.weight = torch.nn.Parameter(torch.empty(experts, out_features, in_features, dtype=torch.bfloat16,
+                                                     device=device))
+        self.padded, self.had, self.had_n, self.grad_rounding = padded, had, had_n, grad_rounding
+        self.sign_seed = 0
+        self.sr_seed = 0
+
+    def forward(self, x, offsets):
+        return MXFP4GroupedLinearFunction.apply(x, offsets, self.weight, self.padded, self.had, self.had_n,
+                                                self.sign_seed, self.grad_rounding, self.sr_seed)
