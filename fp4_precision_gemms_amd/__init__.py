@@ -413,6 +413,10 @@ def fp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor
     """(dx bf16 [rows, cols], dw fp32 [cols]) of the norm from dy and the h and
     rstd of the forward pass; `dh`: the gradient that reaches h past the norm
     (see include/fp4.h).  `out`: optional preallocated (dx, dw); dx may be dh."""
+    if workspace is None and stream is not None:
+        # a workspace of this call's own must outlive it on `stream`
+        workspace = torch.empty(fp4_rmsnorm_workspace_bytes(*dy.shape), dtype=torch.uint8, device=dy.device)
+        workspace.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream))
     return _native().rmsnorm_backward(dy, h, weight, rstd, dh, out, workspace, _stream_of(stream, dy))
 
 

@@ -28,8 +28,8 @@ LIB_PATH = os.path.join(HERE, "libfp4.so")
 CALIB_LIB_PATH = os.path.join(HERE, "libfp4calib.so")
 BINDING_PATH = os.path.join(HERE, "_torch_binding.so")
 
-SOURCES = ["fp4_abi.cpp", "quant_mx.hip", "gemm_mx.hip", "nvfp4.hip", "norm_mx.hip", "gemm_few.hip",
-           "gemm_depth.hip", "quant_grouped.hip"]
+SOURCES = ["fp4_abi.cpp", "fp4_abi_ops.cpp", "quant_mx.hip", "gemm_mx.hip", "nvfp4.hip", "norm_mx.hip", "gemm_few.hip",
+           "gemm_grouped.hip", "gemm_depth.hip", "quant_grouped.hip"]
 CALIB_SOURCES = ["calib_mfma.hip"]
 ARCH = "gfx950"
 

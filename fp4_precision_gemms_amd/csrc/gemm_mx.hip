@@ -52,59 +52,11 @@
 //     the tile boundaries of the 256 workgroups do not coincide.
 #include "fp4_device.hpp"
 #include "fp4_launch.hpp"
-#include "grouped.hpp"
+#include "gemm_tile.hpp"
 #include "mx_mfma.hpp"
-
-#include <atomic>
-#include <type_traits>
 
 namespace fp4dev {
 namespace {
-
-typedef __attribute__((address_space(3))) void lds_void_t;
-
-constexpr int kXcds = 8;
-// s_waitcnt immediate: vmcnt(n) with lgkmcnt(0).
-constexpr int wait_vm_lgkm0(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0070; }
-
-// Workgroup barrier without the workgroup-scope release fence of
-// __syncthreads(), which would wait for every outstanding LDS DMA: the caller
-// has already waited (s_waitcnt) for exactly the DMA the barrier publishes.
-// The wavefront-scope fences emit no code; they keep the compiler from moving
-// memory accesses across the barrier.
-__device__ __forceinline__ void barrier_after_wait() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
-// Wave-wide DMA: each lane's 16 (or 4) bytes at (voff + soff) of the buffer
-// go to LDS at lds_dst + 16 (or 4) * lane; lds_dst must be wave-uniform.
-__device__ __forceinline__ void dma16_to_lds(__amdgpu_buffer_rsrc_t rsrc, void* lds_dst,
-                                             uint32_t voff, int soff) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void_t*)lds_dst, 16, voff, soff, 0, 0);
-}
-__device__ __forceinline__ void dma4_to_lds(__amdgpu_buffer_rsrc_t rsrc, void* lds_dst,
-                                            uint32_t voff, int soff) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void_t*)lds_dst, 4, voff, soff, 0, 0);
-}
-
-// Maps the hardware block index to a (tile_m, tile_n) pair: XCD-contiguous
-// runs of logical tiles, grouped GM tile-rows at a time.
-template <int GM>
-__device__ __forceinline__ void tile_of_block(int b, int nb, int tm, int tn, int& tile_m, int& tile_n) {
-    const int xcd = b % kXcds, idx = b / kXcds;
-    const int full = nb / kXcds, rem = nb % kXcds;
-    const int t = xcd * full + (xcd < rem ? xcd : rem) + idx;
-    const int per_group = GM * tn;
-    const int group = t / per_group, first_m = group * GM;
-    const int gm = (tm - first_m) < GM ? (tm - first_m) : GM;
-    const int r = t - group * per_group;
-    tile_m = first_m + r % gm;
-    tile_n = r / gm;
-}
 
 // A 16-byte store of C marked non-temporal: with whole 128-byte lines per
 // instruction the output streams to HBM during the GEMM instead of sitting
@@ -129,31 +81,11 @@ constexpr int kEpiRegion = 32 * kEpiRow;        // 32 rows per wave
 // the ring), so no lane ever reads out of range; the prefetches past the
 // last stage re-load the last stage (never read) and each stage's offset is
 // a scalar added to per-tile descriptors.
-//
-// GROUP (grouped.hpp): kRowGroups -- the rows of A and C belong to experts, each
-// with a B of its own; M is the row count of A's grouped layout, a tile never
-// crosses into the next expert, and FAST's full tiles hold for the columns and
-// the contraction only.  kDepthGroups -- each expert owns whole stages of the
-// contraction and an output [M, N] of its own.  Groups take FAST's loads, with
-// tiles that may be partial (code rows past the operand read as zero, scale
-// rows as whatever follows them: they reach no output that is stored) and any
-// contraction: stages before the first are clamped like those past the last;
-// row groups give them, and the last stage's blocks past the end, scales that
-// make them vanish, depth groups do not multiply them.
-enum { kNoGroups = 0, kRowGroups = 1, kDepthGroups = 2 };
-
-// One int per expert in LDS; Which tells several arrays apart.
-template <int Which>
-__device__ __forceinline__ int* expert_ints() {
-    __shared__ int v[kMaxExperts];
-    return v;
-}
-
-template <int FM, int GM, bool FAST, bool KTAIL, bool OBF16, bool ACC, int GROUP>
-__device__ __forceinline__ void gemm_tiles(
+template <int FM, int GM, bool FAST, bool KTAIL, bool OBF16, bool ACC>
+__global__ __launch_bounds__(kThreads) void gemm_mx_tn(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ SA, const uint8_t* __restrict__ B,
     const uint8_t* __restrict__ SB, int64_t M, int64_t N, int64_t K, void* __restrict__ C,
-    int tiles_m, int tiles_n, const GroupArgs ga) {
+    int tiles_m, int tiles_n) {
     constexpr int BM = 32 * FM, FN = 2;
     constexpr int kACodes = FM * 4096;                 // FM row groups x 8 chunks of 512 B
     constexpr int kAScales = 2048;                     // 8 scale DMAs of 32 rows x 8 B
@@ -165,7 +97,6 @@ __device__ __forceinline__ void gemm_tiles(
     constexpr int kVmStage = FM + (FAST ? 1 : 2) + 2 * kKS + 2;
     static_assert(FM >= 4 && FM <= 8, "tile rows");
     static_assert(!(FAST && KTAIL), "the fast path has no contraction tail");
-    static_assert(!GROUP || FAST, "groups take the fast loads");
     constexpr int kWaitStage = 2 * kVmStage - 2;
     static_assert(kWaitStage <= 63, "vmcnt range");
     static_assert(kSlots * kSlot <= 160 * 1024, "LDS");
@@ -180,56 +111,14 @@ __device__ __forceinline__ void gemm_tiles(
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // wave-uniform
     const int h = lane >> 5, l32 = lane & 31;
-    int ntiles = tiles_m * tiles_n;
-    int64_t nb = K / 32;                               // blocks per row
-    int nks = (int)((nb + 1) / 2);                     // MFMA k-steps (K < 2^24)
-    int nk = (int)((nb + 7) / 8);                      // 256-k stages
+    const int ntiles = tiles_m * tiles_n;
+    const int64_t nb = K / 32;                         // blocks per row
+    const int nks = (int)((nb + 1) / 2);               // MFMA k-steps (K < 2^24)
+    const int nk = (int)((nb + 7) / 8);                // 256-k stages
     // leading all-zero stages round the stage count up to a multiple of the
     // ring (the loop below handles four stages per iteration)
-    int kfirst = -((kSlots - nk % kSlots) % kSlots);
+    const int kfirst = -((kSlots - nk % kSlots) % kSlots);
     const uint32_t gstride = (uint32_t)(nb * 512);     // bytes per 32-row group of codes
-    if constexpr (GROUP == kRowGroups) {
-        // the experts' row tiles, counted up: ends[e] of them belong to
-        // experts 0 .. e
-        int* const los = expert_ints<0>();
-        int* const his = expert_ints<1>();
-        int* const ends = expert_ints<2>();
-        if (wave == 0) {
-            int before = 0;
-            for (int base = 0; base < ga.experts; base += 64) {
-                const int e = base + lane;
-                int n = 0;
-                if (e < ga.experts) {
-                    const RowRange r = expert_rows(ga.offsets, e, ga.rows);
-                    los[e] = (int)r.lo;
-                    his[e] = (int)r.hi;
-                    n = (int)((r.hi - r.lo + BM - 1) / BM);
-                }
-#pragma unroll
-                for (int o = 1; o < 64; o <<= 1) {
-                    const int v = __shfl_up(n, o);
-                    if (lane >= o) n += v;
-                }
-                n += before;
-                if (e < ga.experts) ends[e] = n;
-                before = __shfl(n, 63);
-            }
-        }
-        __syncthreads();
-        tiles_m = __builtin_amdgcn_readfirstlane(ends[ga.experts - 1]);
-        ntiles = tiles_m * tiles_n;
-        if ((int)blockIdx.x >= ntiles) return;
-    } else if constexpr (GROUP == kDepthGroups) {
-        int* const los = expert_ints<0>();
-        int* const his = expert_ints<1>();
-        for (int e = tid; e < ga.experts; e += kThreads) {
-            const RowRange r = expert_rows(ga.offsets, e, ga.rows);
-            los[e] = (int)r.lo;
-            his[e] = (int)r.hi;
-        }
-        __syncthreads();
-        ntiles *= ga.experts;
-    }
 
     // Per-lane parts of the buffer offsets (the stage / k-step part goes in
     // the scalar offset): A chunk d of this wave's k-step (wave) of a stage,
@@ -243,11 +132,6 @@ __device__ __forceinline__ void gemm_tiles(
     const bool half_tail = KTAIL && (nb & 1) && h == 1;
 
     int64_t m0 = 0, n0 = 0, rows_a = 0, rows_b = 0;
-    // the tile's first row in C, and what comes before its expert's output
-    int64_t c0 = 0, cbase = 0;
-    // per-expert parts of the scale addresses
-    const uint8_t* sa_tile = SA;
-    const uint8_t* sb_tile = SB;
     __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)A, (short)0, 0, kBufferWord3);
     __amdgpu_buffer_rsrc_t rb = ra, rsa = ra, rsb = ra;   // rsa, rsb: FAST scale descriptors
     // FAST: lane parts of the scale offsets (A: 16 bytes of this wave's
@@ -258,83 +142,26 @@ __device__ __forceinline__ void gemm_tiles(
     for (int j = 0; j < FN; ++j) offsb[j] = (uint32_t)((64 * wave + 32 * j + l32) * 8);
     auto set_tile = [&](int t) {
         int tile_m, tile_n;
-        int e = 0;
-        if constexpr (GROUP == kDepthGroups) {
-            // experts one after another; an expert's tiles spread over all XCDs
-            const int per = tiles_m * tiles_n;
-            e = t / per;
-            tile_of_block<GM>(t - e * per, per, tiles_m, tiles_n, tile_m, tile_n);
-        } else {
-            tile_of_block<GM>(t, ntiles, tiles_m, tiles_n, tile_m, tile_n);
-        }
+        tile_of_block<GM>(t, ntiles, tiles_m, tiles_n, tile_m, tile_n);
         tile_m = __builtin_amdgcn_readfirstlane(tile_m);
         tile_n = __builtin_amdgcn_readfirstlane(tile_n);
         m0 = (int64_t)tile_m * BM;
         n0 = (int64_t)tile_n * kBN;
         rows_a = (M - m0) < BM ? (M - m0) : BM;
         rows_b = (N - n0) < kBN ? (N - n0) : kBN;
-        c0 = m0;
-        if constexpr (GROUP == kRowGroups) {
-            const int* const ends = expert_ints<2>();
-            for (int base = 0; base < ga.experts; base += 64)
-                e += __popcll(__ballot(base + lane < ga.experts && ends[base + lane] <= tile_m));
-            e = __builtin_amdgcn_readfirstlane(e);
-            const int first = e ? __builtin_amdgcn_readfirstlane(ends[e - 1]) : 0;
-            const int lo = __builtin_amdgcn_readfirstlane(expert_ints<0>()[e]);
-            const int hi = __builtin_amdgcn_readfirstlane(expert_ints<1>()[e]);
-            const int64_t local = (int64_t)(tile_m - first) * BM;
-            m0 = 32 * ((int64_t)lo / 32 + e) + local;
-            c0 = lo + local;
-            rows_a = (hi - c0) < BM ? (hi - c0) : BM;
-            ra = __builtin_amdgcn_make_buffer_rsrc((void*)(A + (m0 / 32) * (int64_t)gstride), (short)0,
-                                                   (int)(((rows_a + 31) / 32) * (int64_t)gstride), kBufferWord3);
-            const int64_t groups = (N + 31) / 32;      // of an expert's B
-            rb = __builtin_amdgcn_make_buffer_rsrc((void*)(B + (e * groups + n0 / 32) * (int64_t)gstride), (short)0,
-                                                   (int)(((rows_b + 31) / 32) * (int64_t)gstride), kBufferWord3);
-            sb_tile = SB + (int64_t)e * nk * N * 8;
-        } else if constexpr (GROUP == kDepthGroups) {
-            e = __builtin_amdgcn_readfirstlane(e);
-            const int lo = __builtin_amdgcn_readfirstlane(expert_ints<0>()[e]);
-            const int hi = __builtin_amdgcn_readfirstlane(expert_ints<1>()[e]);
-            nk = (hi - lo + 255) / 256;
-            nb = 8 * nk;
-            nks = 4 * nk;
-            kfirst = -((kSlots - nk % kSlots) % kSlots);
-            const int64_t q0 = lo / 256 + e;
-            cbase = (int64_t)e * M * N;
-            sa_tile = SA + q0 * M * 8;
-            sb_tile = SB + q0 * N * 8;
-            // an expert's span of each 32-row group: up to its last stage (one
-            // without rows still loads a stage, which stays unused)
-            const int64_t span = (nk ? nk : 1) * 4096;
-            ra = __builtin_amdgcn_make_buffer_rsrc(
-                (void*)(A + (m0 / 32) * (int64_t)gstride + q0 * 4096), (short)0,
-                (int)(((rows_a + 31) / 32 - 1) * (int64_t)gstride + span), kBufferWord3);
-            rb = __builtin_amdgcn_make_buffer_rsrc(
-                (void*)(B + (n0 / 32) * (int64_t)gstride + q0 * 4096), (short)0,
-                (int)(((rows_b + 31) / 32 - 1) * (int64_t)gstride + span), kBufferWord3);
-        } else {
         // the tile's row groups of each operand; groups past the operand's
         // last one are out of range and read as zero
         ra = __builtin_amdgcn_make_buffer_rsrc((void*)(A + (m0 / 32) * (int64_t)gstride), (short)0,
                                                (int)(((rows_a + 31) / 32) * (int64_t)gstride), kBufferWord3);
         rb = __builtin_amdgcn_make_buffer_rsrc((void*)(B + (n0 / 32) * (int64_t)gstride), (short)0,
                                                (int)(((rows_b + 31) / 32) * (int64_t)gstride), kBufferWord3);
-        }
         if constexpr (FAST) {
             // stage q of the tile's rows starts q R 8 bytes further on
-            rsa = __builtin_amdgcn_make_buffer_rsrc((void*)(sa_tile + m0 * 8), (short)0,
-                                                    (int)(((int64_t)(GROUP && nk == 0 ? 1 : nk) * M - m0) * 8), kBufferWord3);
-            rsb = __builtin_amdgcn_make_buffer_rsrc((void*)(sb_tile + n0 * 8), (short)0,
-                                                    (int)(((int64_t)(GROUP && nk == 0 ? 1 : nk) * N - n0) * 8), kBufferWord3);
+            rsa = __builtin_amdgcn_make_buffer_rsrc((void*)(SA + m0 * 8), (short)0,
+                                                    (int)(((int64_t)nk * M - m0) * 8), kBufferWord3);
+            rsb = __builtin_amdgcn_make_buffer_rsrc((void*)(SB + n0 * 8), (short)0,
+                                                    (int)(((int64_t)nk * N - n0) * 8), kBufferWord3);
         }
-    };
-
-    // FAST: the stage loaded in place of stage kt, which may lie past the last
-    // one (or before the first, with groups; an expert without rows has none)
-    auto stage_of = [&](int kt) {
-        if (GROUP) return kt < 0 ? 0 : kt < nk ? kt : nk ? nk - 1 : 0;
-        return kt < nk ? kt : nk - 1;
     };
 
     // ---- loads ---------------------------------------------------------
@@ -343,7 +170,7 @@ __device__ __forceinline__ void gemm_tiles(
     // `scales`.  A stage outside [0, nk) is all zero.
     auto dma_a = [&](int kt, uint8_t* slot, int d0, int d1, bool scales) {
         if constexpr (FAST) {
-            const int kc = stage_of(kt);
+            const int kc = kt < nk ? kt : nk - 1;
             const int soff = __builtin_amdgcn_readfirstlane((4 * kc + wave) * 1024);
 #pragma unroll
             for (int d = 0; d < FM; ++d)
@@ -374,7 +201,7 @@ __device__ __forceinline__ void gemm_tiles(
         if (scales) {
             const int64_t q = zero ? 0 : kt;
             const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-                (void*)(sa_tile + (q * M + m0) * 8), (short)0, (int)(rows_a * 8), kBufferWord3);
+                (void*)(SA + (q * M + m0) * 8), (short)0, (int)(rows_a * 8), kBufferWord3);
             const uint32_t zoob = zero ? kOob : 0u;
             dma4_to_lds(rs, slot + kACodes + wave * 256, (uint32_t)(wave * 256 + lane * 4) | zoob, 0);
             dma4_to_lds(rs, slot + kACodes + (wave + 4) * 256,
@@ -384,8 +211,7 @@ __device__ __forceinline__ void gemm_tiles(
     // B fragment j of k-step s (global index) into registers.
     auto load_b = [&](int s, int j) -> v4i {
         if constexpr (FAST) {
-            const int soff = GROUP ? __builtin_amdgcn_readfirstlane((s < 0 ? 0 : s < nks ? s : nks ? nks - 1 : 0) * 1024)
-                                   : __builtin_amdgcn_readfirstlane((s < nks ? s : nks - 1) * 1024);
+            const int soff = __builtin_amdgcn_readfirstlane((s < nks ? s : nks - 1) * 1024);
             return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rb, offb[j], soff, 0));
         }
         bool dead = s < 0 || s >= nks;
@@ -399,7 +225,7 @@ __device__ __forceinline__ void gemm_tiles(
     struct BSc { uint32_t w[FN][2]; };
     auto load_bsc = [&](int kt) -> BSc {
         if constexpr (FAST) {
-            const int kc = stage_of(kt);
+            const int kc = kt < nk ? kt : nk - 1;
             const int ss = __builtin_amdgcn_readfirstlane((int)((int64_t)kc * N * 8));
             BSc r;
 #pragma unroll
@@ -413,7 +239,7 @@ __device__ __forceinline__ void gemm_tiles(
         const bool zero = kt < 0 || kt >= nk;
         const int64_t q = zero ? 0 : kt;
         const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-            (void*)(sb_tile + (q * N + n0) * 8), (short)0, (int)(rows_b * 8), kBufferWord3);
+            (void*)(SB + (q * N + n0) * 8), (short)0, (int)(rows_b * 8), kBufferWord3);
         BSc r;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
@@ -512,29 +338,14 @@ __device__ __forceinline__ void gemm_tiles(
     // One stage from slot u (its k-step 0 fragments and scales already in
     // registers).  Stage kt + 3 is loaded into slot (u + 3) mod 4, B scales
     // of stage kt + 2 into the B scale ring, B k-steps 8 ahead into the B ring.
-    // Row groups: the bytes of the last stage's scale words (byte s: block
-    // 2 s + h of the stage) that are of blocks of the operand.
-    const int last_bytes = (int)(nb - 8 * (nk - 1) - h + 1) / 2;
-    const uint32_t last_keep = last_bytes >= 4 ? ~0u : (1u << (8 * last_bytes)) - 1;
-    // (Without `live`: its loads alone.)
-    auto run_stage = [&](int u, int kt, bool live = true) {
+    auto run_stage = [&](int u, int kt) {
         uint8_t* const ahead = slots[(u + 3) % kSlots];
         ASc& nsa = asc[(u + 1) & 1];
-        SWords sw = stage_words(asc[u & 1], bsc[u], kt);
-        if constexpr (GROUP == kRowGroups) {
-            // A stage before the first holds stage 0's bytes, and blocks past
-            // the last one whatever follows: with both scales 2^-127 their
-            // products vanish.
-            const uint32_t keep = kt < 0 ? 0u : kt == nk - 1 ? last_keep : ~0u;
-#pragma unroll
-            for (int i = 0; i < FM; ++i) sw.a[i] &= keep;
-#pragma unroll
-            for (int j = 0; j < FN; ++j) sw.b[j] &= keep;
-        }
+        const SWords sw = stage_words(asc[u & 1], bsc[u], kt);
 #pragma unroll
         for (int s = 0; s < kKS - 1; ++s) {
             read_afrags(u, s + 1, (s + 1) & 1);
-            if (live) mfmas(s, s & 1, (4 * u + s) % kRing, sw);
+            mfmas(s, s & 1, (4 * u + s) % kRing, sw);
 #pragma unroll
             for (int j = 0; j < FN; ++j) fb[(4 * u + s) % kRing][j] = load_b(4 * kt + s + kRing, j);
             dma_a(kt + 3, ahead, kdma(s), kdma(s + 1), s == 0);
@@ -562,7 +373,7 @@ __device__ __forceinline__ void gemm_tiles(
         barrier_after_wait();
         read_ascales((u + 1) % kSlots, kt + 1, nsa);
         read_afrags((u + 1) % kSlots, 0, 0);
-        if (live) mfmas(kKS - 1, 1, (4 * u + 3) % kRing, sw);
+        mfmas(kKS - 1, 1, (4 * u + 3) % kRing, sw);
 #pragma unroll
         for (int j = 0; j < FN; ++j) fb[(4 * u + 3) % kRing][j] = load_b(4 * kt + 3 + kRing, j);
         constexpr int kM = FM * FN, kDs = 2 * FM;
@@ -608,9 +419,7 @@ __device__ __forceinline__ void gemm_tiles(
     constexpr int kPro = FN + 2 * kKS * FN + 2 * (FM + (FAST ? 1 : 2)) + FN;
     // stores of a full tile's epilogue per wave (32-row pieces, 4 rows per
     // store instruction)
-    // (16 bytes a lane and 8 rows per store with groups and a bf16 output)
-    constexpr int kEpiRows = GROUP && OBF16 ? 8 : 4;
-    constexpr int kEpiStores = FM * (32 / kEpiRows);
+    constexpr int kEpiStores = FM * 8;
 
     bool early = false;   // this tile's prologue was issued during the previous epilogue
     // Staggered start: workgroup b begins b x 64 cycles late (about 8 us for
@@ -661,39 +470,24 @@ __device__ __forceinline__ void gemm_tiles(
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
         read_ascales(0, kfirst, asc[0]);
         read_afrags(0, 0, 0);
-        // The tile's stages and its epilogue, after `dead` stages before the
-        // first that are loads only (their slots and registers hold nothing of
-        // the tile).
-        auto tile = [&](auto dead) {
-            constexpr int D = decltype(dead)::value;
-            int kt = kfirst;
-            if constexpr (D > 0) {
-                run_stage(0, kt, false);
-                run_stage(1, kt + 1, D < 2);
-                run_stage(2, kt + 2, D < 3);
-                run_stage(3, kt + 3);
-                kt += kSlots;
-            }
-            for (; kt < nk; kt += kSlots) {
-                run_stage(0, kt);
-                run_stage(1, kt + 1);
-                run_stage(2, kt + 2);
-                run_stage(3, kt + 3);
-            }
+        for (int kt = kfirst; kt < nk; kt += kSlots) {
+            run_stage(0, kt);
+            run_stage(1, kt + 1);
+            run_stage(2, kt + 2);
+            run_stage(3, kt + 3);
+        }
+
         // the prefetches past the last stage must land before the slots are
         // refilled (and before the workgroup goes away)
         __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
         __syncthreads();                                // all fragment reads of the tile are done
-        // the tile the epilogue writes: rows em0 .. em0 + erows - 1 of C
-        const int64_t em0 = c0, en0 = n0, ebase = cbase, erows = rows_a;
+        const int64_t em0 = m0, en0 = n0;               // the tile the epilogue writes
         const bool vec_store = (N % 4) == 0;
         // workgroup-uniform; constant on the fast path, whose tiles are all
         // full: the epilogue then has no partial-tile branch, whose zero-store
         // path made the compiler wait for most of these stores before the
         // next tile's first fragment moves
-        // (with groups a fast path's partial tile stores through a buffer that
-        // drops what lies outside, so it has no branch either)
-        const bool full_tile = FAST || (vec_store && (GROUP ? erows == BM : em0 + BM <= M) && en0 + kBN <= N);
+        const bool full_tile = FAST || (vec_store && em0 + BM <= M && en0 + kBN <= N);
         early = false;
         if constexpr (!KTAIL && !ACC) {
             // The next tile's first stages go out now, into slots 0..2 (this
@@ -715,22 +509,6 @@ __device__ __forceinline__ void gemm_tiles(
         // four whole rows of the wave's columns (fp32: two 128-byte lines
         // each, written non-temporally); with N % 4 != 0 (rows not 16-byte
         // aligned) elements go one by one.
-        // Groups, fast path: the tile's rows of C as one buffer; this lane's
-        // offset in its first row, out of range for columns past N.  What lies
-        // past the last row is past the buffer's end.  Non-temporal where
-        // the rows are whole lines, in bf16 too: 8 experts of 14336 x 4096, 128-row tiles, 512 rows each 156 us
-        // against 180 with plain stores.
-        constexpr int kOut = OBF16 ? 2 : 4;
-        const uint32_t row_bytes = (uint32_t)N * kOut;
-        const bool lines = row_bytes % 128 == 0;
-        const __amdgpu_buffer_rsrc_t rc = __builtin_amdgcn_make_buffer_rsrc(
-            (void*)((uint8_t*)C + (ebase + em0 * N + en0) * kOut), (short)0, (int)((erows * N - en0) * kOut),
-            kBufferWord3);
-        const int er = lane / (64 / kEpiRows), ec = lane % (64 / kEpiRows) * kEpiRows;
-        const uint32_t offc = en0 + 64 * wave + ec < N
-                                  ? (uint32_t)er * row_bytes + (uint32_t)(64 * wave + ec) * kOut
-                                  : kOob;
-
         uint8_t* const reg = lds3 + wave * kEpiRegion;
         const int lr = lane >> 4, c4 = (lane & 15) * 4;
 #pragma unroll
@@ -744,30 +522,6 @@ __device__ __forceinline__ void gemm_tiles(
                         make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
                                     acc[i][j][4 * q + 3]);
                 }
-            if constexpr (GROUP && FAST) {
-                // 16 bytes a lane: 8 bf16 or 4 fp32 of a row (bf16 with integer
-                // rounding and 8 bytes a lane: 540 us where this takes 496, 8
-                // experts of 2048 rows, 14336 x 4096)
-                typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-                v4u o[kEpiStores / FM];
-#pragma unroll
-                for (int k = 0; k < kEpiStores / FM; ++k) {
-                    const v4f* const f = reinterpret_cast<const v4f*>(reg + (kEpiRows * k + er) * kEpiRow + ec * 4);
-                    if constexpr (OBF16) {
-                        const v4f a = f[0], b = f[1];
-                        o[k] = v4u{bf16_pair(a[0], a[1]), bf16_pair(a[2], a[3]), bf16_pair(b[0], b[1]), bf16_pair(b[2], b[3])};
-                    } else {
-                        o[k] = __builtin_bit_cast(v4u, f[0]);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < kEpiStores / FM; ++k) {
-                    const uint32_t at = offc + (uint32_t)(32 * i + kEpiRows * k) * row_bytes;
-                    if (lines) __builtin_amdgcn_raw_buffer_store_b128(o[k], rc, at, 0, 2);
-                    else __builtin_amdgcn_raw_buffer_store_b128(o[k], rc, at, 0, 0);
-                }
-                continue;
-            }
             if (full_tile) {
                 float4 f[8];
 #pragma unroll
@@ -779,7 +533,7 @@ __device__ __forceinline__ void gemm_tiles(
                     const int64_t n = en0 + 64 * wave + c4;
                     float v[4] = {f[k].x, f[k].y, f[k].z, f[k].w};
                     if constexpr (OBF16) {
-                        uint2* p = reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(C) + ebase + m * N + n);
+                        uint2* p = reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(C) + m * N + n);
                         if constexpr (ACC) {
                             const uint2 o = *p;
                             v[0] += bf16_value(o.x & 0xFFFFu); v[1] += bf16_value(o.x >> 16);
@@ -788,7 +542,7 @@ __device__ __forceinline__ void gemm_tiles(
                         *p = make_uint2(bf16_rne(v[0]) | (bf16_rne(v[1]) << 16),
                                         bf16_rne(v[2]) | (bf16_rne(v[3]) << 16));
                     } else {
-                        float* p = reinterpret_cast<float*>(C) + ebase + m * N + n;
+                        float* p = reinterpret_cast<float*>(C) + m * N + n;
                         if constexpr (ACC) {
                             const float4 o = *reinterpret_cast<const float4*>(p);
                             v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
@@ -803,10 +557,10 @@ __device__ __forceinline__ void gemm_tiles(
                 const int row = 4 * k + lr;
                 const float4 f = *reinterpret_cast<const float4*>(reg + row * kEpiRow + c4 * 4);
                 const int64_t m = em0 + i * 32 + row, n = en0 + 64 * wave + c4;
-                if ((GROUP ? m >= em0 + erows : m >= M) || n >= N) continue;
+                if (m >= M || n >= N) continue;
                 float v[4] = {f.x, f.y, f.z, f.w};
                 if constexpr (OBF16) {
-                    uint16_t* crow = reinterpret_cast<uint16_t*>(C) + ebase + m * N;
+                    uint16_t* crow = reinterpret_cast<uint16_t*>(C) + m * N;
                     if (vec_store && n + 4 <= N) {
                         uint2* p = reinterpret_cast<uint2*>(crow + n);
                         if constexpr (ACC) {
@@ -824,7 +578,7 @@ __device__ __forceinline__ void gemm_tiles(
                         }
                     }
                 } else {
-                    float* crow = reinterpret_cast<float*>(C) + ebase + m * N;
+                    float* crow = reinterpret_cast<float*>(C) + m * N;
                     if (vec_store && n + 4 <= N) {
                         if constexpr (ACC) {
                             const float4 o = *reinterpret_cast<const float4*>(crow + n);
@@ -840,60 +594,8 @@ __device__ __forceinline__ void gemm_tiles(
                 }
             }
         }
-        };
-        if constexpr (GROUP == kDepthGroups) {
-            // An expert's stages are rarely a multiple of four, and up to three
-            // multiplied in vain cost: 8 experts of 2048 tokens, 14336 x 4096
-            // 632 us with them, 581 without.  Each count has code of its own
-            // from the first stage to the last store: where the accumulators of
-            // two paths met, the compiler spilled hundreds of registers.  (Row
-            // groups, with more registers in use, lost 5-10 % this way.)
-            switch (-kfirst) {
-                case 1: tile(std::integral_constant<int, 1>{}); break;
-                case 2: tile(std::integral_constant<int, 2>{}); break;
-                case 3: tile(std::integral_constant<int, 3>{}); break;
-                default: tile(std::integral_constant<int, 0>{}); break;
-            }
-        } else {
-            tile(std::integral_constant<int, 0>{});
-        }
     }
 }
-
-template <int FM, int GM, bool FAST, bool KTAIL, bool OBF16, bool ACC>
-__global__ __launch_bounds__(kThreads) void gemm_mx_tn(
-    const uint8_t* __restrict__ A, const uint8_t* __restrict__ SA, const uint8_t* __restrict__ B,
-    const uint8_t* __restrict__ SB, int64_t M, int64_t N, int64_t K, void* __restrict__ C,
-    int tiles_m, int tiles_n) {
-    gemm_tiles<FM, GM, FAST, KTAIL, OBF16, ACC, kNoGroups>(A, SA, B, SB, M, N, K, C, tiles_m, tiles_n, GroupArgs{});
-}
-
-template <int FM, int GM, bool OBF16, int GROUP>
-__global__ __launch_bounds__(kThreads) void gemm_mx_grouped(
-    const uint8_t* __restrict__ A, const uint8_t* __restrict__ SA, const uint8_t* __restrict__ B,
-    const uint8_t* __restrict__ SB, int64_t M, int64_t N, int64_t K, void* __restrict__ C,
-    int tiles_m, int tiles_n, const GroupArgs ga) {
-    gemm_tiles<FM, GM, true, false, OBF16, false, GROUP>(A, SA, B, SB, M, N, K, C, tiles_m, tiles_n, ga);
-}
-
-// Compute units of each device, queried once per device (concurrent first
-// calls may both query; they store the same value).
-int cu_count() {
-    static std::atomic<int> counts[64];
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-    int n = counts[dev].load(std::memory_order_relaxed);
-    if (n == 0) {
-        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
-            n = 256;
-        counts[dev].store(n, std::memory_order_relaxed);
-    }
-    return n;
-}
-
-// Tile-rows per group of the block order (each XCD runs 32 tiles at a time):
-// groups of 2 to 4 rows measured best on the gate/up and q_proj shapes.
-constexpr int kGroupRows = 4;
 
 template <int FM, bool FAST, bool KTAIL, bool OBF16, bool ACC>
 hipError_t launch_one(const uint8_t* aq, const uint8_t* as, const uint8_t* bq, const uint8_t* bs,
@@ -949,55 +651,6 @@ hipError_t launch_gemm_mx(const uint8_t* aq, const uint8_t* as, const uint8_t* b
     };
     if (cost(224) < cost(256)) return launch_out<7>(aq, as, bq, bs, M, N, K, c, out_bf16, accumulate, st);
     return launch_out<8>(aq, as, bq, bs, M, N, K, c, out_bf16, accumulate, st);
-}
-
-namespace {
-template <int FM, int GROUP>
-hipError_t launch_grouped(const uint8_t* aq, const uint8_t* as, const uint8_t* bq, const uint8_t* bs, int64_t M,
-                          int64_t N, int64_t K, void* c, int out_bf16, int64_t most, int64_t tm, int64_t tn,
-                          const GroupArgs& ga, hipStream_t st) {
-    const int64_t cus = cu_count();
-    const dim3 grid((unsigned)(most < cus ? most : cus));
-    return out_bf16 ? launch(&gemm_mx_grouped<FM, kGroupRows, true, GROUP>, grid, dim3(kThreads), st, aq, as, bq, bs,
-                             M, N, K, c, (int)tm, (int)tn, ga)
-                    : launch(&gemm_mx_grouped<FM, kGroupRows, false, GROUP>, grid, dim3(kThreads), st, aq, as, bq, bs,
-                             M, N, K, c, (int)tm, (int)tn, ga);
-}
-
-}  // namespace
-
-// Whether the large tiles' 32-bit offsets hold: rows of C in whole 16-byte
-// pieces, a tile of C and an operand's scales within 2 GiB.
-bool row_groups_fit(int64_t experts, int64_t rows, int64_t N, int64_t K) {
-    const int64_t M = 32 * (rows / 32 + experts);
-    return N % 8 == 0 && N < (INT64_C(1) << 21) && (K + 255) / 256 * (M > N ? M : N) * 8 < (INT64_C(1) << 31);
-}
-
-hipError_t launch_gemm_row_groups(const uint8_t* aq, const uint8_t* as, const int* offsets, int64_t experts,
-                                  int64_t rows, const uint8_t* wq, const uint8_t* ws, int64_t N, int64_t K, void* c,
-                                  int out_bf16, hipStream_t st) {
-    const int64_t M = 32 * (rows / 32 + experts), tn = (N + kBN - 1) / kBN, cus = cu_count();
-    const GroupArgs ga{offsets, (int)experts, rows};
-    // Tile rows: rounds of the persistent grid times a tile's time, with half a
-    // tile per expert for its last one.  A tile of 128 rows takes 0.53-0.62 of
-    // one of 256 (it loads as much of B): 8 experts of 14336 x 4096, 256 rows
-    // each 92 against 100 us, 2048 rows 574 against 526; 32 experts of 2048 x
-    // 2048, 200 rows 33 against 40.
-    auto rounds = [&](int64_t bm) { return ((rows / bm + (experts + 1) / 2) * tn + cus - 1) / cus; };
-    if (58 * rounds(128) < 100 * rounds(256))
-        return launch_grouped<4, kRowGroups>(aq, as, wq, ws, M, N, K, c, out_bf16, (rows / 128 + experts) * tn, 0, tn,
-                                             ga, st);
-    return launch_grouped<8, kRowGroups>(aq, as, wq, ws, M, N, K, c, out_bf16, (rows / 256 + experts) * tn, 0, tn, ga,
-                                         st);
-}
-
-hipError_t launch_gemm_depth_groups(const uint8_t* aq, const uint8_t* as, const uint8_t* bq, const uint8_t* bs,
-                                    const int* offsets, int64_t experts, int64_t rows, int64_t M, int64_t N, void* c,
-                                    int out_bf16, hipStream_t st) {
-    const int64_t K = 256 * (rows / 256 + experts);             // of the grouped layout
-    const int64_t tm = (M + 255) / 256, tn = (N + kBN - 1) / kBN;
-    return launch_grouped<8, kDepthGroups>(aq, as, bq, bs, M, N, K, c, out_bf16, tm * tn * experts, tm, tn,
-                                           GroupArgs{offsets, (int)experts, rows}, st);
 }
 
 }  // namespace fp4dev

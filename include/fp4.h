@@ -462,7 +462,9 @@ fp4_status fp4_quantize_grouped(const void* x_bf16, const int32_t* offsets, int6
  * (FP4_CODE_BYTES(N, K) and FP4_SCALE_BYTES(N, K) bytes each).  C row-major
  * [rows, N] in `out`; rows of no expert are left as they were.  The forward
  * product takes W along cols; Dgrad is the same call with dY and W^T (W along
- * rows).  Requirements as for fp4_gemm_decode and fp4_quantize_grouped.
+ * rows).  MXFP8 rows take the kernel made for few rows, whatever their number.
+ * Requirements as for fp4_gemm_decode and fp4_quantize_grouped; experts (rows /
+ * 128 + 1) ceil(N / 256) < 2^31.
  */
 fp4_status fp4_gemm_grouped(const uint8_t* a, const uint8_t* as, fp4_format fmt,
                             const int32_t* offsets, int64_t experts, int64_t rows,
@@ -476,7 +478,7 @@ fp4_status fp4_gemm_grouped(const uint8_t* a, const uint8_t* as, fp4_format fmt,
  * fp4_quantize_grouped with the same offsets, had, had_n and sign_seed.  dw is
  * [experts, N, K] in `out`, overwritten; that of an expert without rows is zero.
  * Requirements: N % 32 == 0, K % 32 == 0 (the quantizer's); 256 (rows / 256 +
- * experts) < 2^24, and (rows / 256 + experts) max(N, K) < 2^28; at most 2^24 - 1 output tiles of 256 x 256; pointers 16-byte
+ * experts) < 2^24, and (rows / 256 + experts) max(N, K) < 2^28, K < 2^21; at most 2^24 - 1 output tiles of 256 x 256; pointers 16-byte
  * aligned (offsets 4).
  */
 fp4_status fp4_gemm_grouped_wgrad(const uint8_t* dytq, const uint8_t* dyts, const uint8_t* xtq,

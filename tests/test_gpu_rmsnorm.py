@@ -240,6 +240,9 @@ def test_another_stream_and_a_captured_graph():
         side = work()
     torch.cuda.current_stream().wait_stream(s)
     torch.cuda.synchronize()
+    given = F.fp4_rmsnorm_backward(dy, side[2], gw, side[3], stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(given[0], want[4]) and torch.equal(given[1], want[5])
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         caught = work()

@@ -102,7 +102,8 @@ def test_gemm_grouped_errors(L):
     for name in ("a", "s", "w", "ws", "c"):
         assert call(**{name: MIS}) == ERR_ALIGN, name
     assert call(off=A + 2) == ERR_ALIGN
-    for bad in (dict(E=0), dict(E=2000), dict(rows=0), dict(N=0), dict(K=40), dict(K=2 ** 24), dict(rows=2 ** 31)):
+    for bad in (dict(E=0), dict(E=2000), dict(rows=0), dict(N=0), dict(K=40), dict(K=2 ** 24), dict(rows=2 ** 31),
+                dict(E=1024, rows=2 ** 20, N=2 ** 20)):
         assert call(**bad) == ERR_SHAPE, bad
 
 
@@ -147,5 +148,5 @@ def test_gemm_grouped_wgrad_errors(L):
     assert call(off=None) == ERR_NULL and call(c=None) == ERR_NULL
     assert call(off=A + 2) == ERR_ALIGN and call(c=MIS) == ERR_ALIGN
     for bad in (dict(E=0), dict(E=1025), dict(rows=0), dict(rows=2 ** 24), dict(N=48), dict(K=16), dict(N=0),
-                dict(N=2 ** 20, K=2 ** 20)):
+                dict(N=2 ** 20, K=2 ** 20), dict(K=2 ** 21), dict(rows=2 ** 23, N=2 ** 14)):
         assert call(**bad) == ERR_SHAPE, bad
