@@ -10,11 +10,12 @@
 //     of a 64-element k-step being one contiguous kilobyte per wave load; a
 //     256-element stage is loaded at once;
 //   - V_MFMA_SCALE_F32_32X32X64_F8F6F4 as in gemm_mx.hip, B first, so that the
-//     accumulators hold C^T and leave through a wave's own LDS region as whole
-//     128-byte lines, stored non-temporally where the rows of C are whole lines
-//     (32 experts of 2048 x 2048 with 50 tokens: 67 us, 88 with plain stores), in
-//     bf16 through V_CVT_PK_BF16_F32 and 16 bytes a lane (50 us; 8 bytes a lane
-//     and integer rounding took 63).
+//     accumulators hold C^T and leave through a wave's own LDS region as row
+//     segments, stored non-temporally (32 experts of 2048 x 2048 with 50
+//     tokens: 67 us, 88 with plain stores; also where the rows are no whole lines:
+//     20 experts of 3200 x 2976 with 400 tokens 122 us against 187), in bf16
+//     through V_CVT_PK_BF16_F32 and 16 bytes a lane (50 us; 8 bytes a lane and
+//     integer rounding took 63).
 // Bound by the output's bytes for few tokens (8 x 14336 x 4096 in bf16, 256
 // tokens an expert: 194 us, 4.8 TB/s), by the loads through L1 for many (a wave
 // loads 16 KB a stage for 16 MFMAs: 1024 cycles of a CU's L1 for four waves,
@@ -33,14 +34,6 @@ typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 constexpr int kTile = 128;
 constexpr int kRow = 64 * 4 + 16;          // a staged row of 64 fp32 columns, padded
 
-// LINES: non-temporal, for whole 128-byte lines only (parts of one would each
-// be written to memory).
-template <bool LINES, typename T>
-__device__ __forceinline__ void put(T* p, T v) {
-    if constexpr (LINES) __builtin_nontemporal_store(v, p);
-    else *p = v;
-}
-
 // C[e][m, n] for one expert's tile; K: elements per row of the grouped layout.
 // Workgroups go round-robin over the 8 XCDs.  From 16 experts on (`per_xcd`) an
 // expert's tiles all run on one XCD, whose L2 then holds its operands and joins
@@ -50,7 +43,7 @@ __device__ __forceinline__ void put(T* p, T v) {
 // of 14336 x 4096, 1024 tokens: 489 against 603 us).
 constexpr int64_t kPerXcdExperts = 16;
 
-template <bool OBF16, bool LINES>
+template <bool OBF16>
 __global__ __launch_bounds__(256) void gemm_mx_depth(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ SA, const uint8_t* __restrict__ B,
     const uint8_t* __restrict__ SB, int64_t M, int64_t N, int64_t K, void* __restrict__ C, int tiles_m, int gx,
@@ -147,10 +140,11 @@ __global__ __launch_bounds__(256) void gemm_mx_depth(
             const int64_t at = ((int64_t)e * M + m0 + 32 * i + row) * N + n0 + c;
             if constexpr (OBF16) {
                 const v4f a = f[0], b = f[1];
-                put<LINES>(reinterpret_cast<v4u*>(reinterpret_cast<uint16_t*>(C) + at),
-                           v4u{bf16_pair(a[0], a[1]), bf16_pair(a[2], a[3]), bf16_pair(b[0], b[1]), bf16_pair(b[2], b[3])});
+                __builtin_nontemporal_store(
+                    v4u{bf16_pair(a[0], a[1]), bf16_pair(a[2], a[3]), bf16_pair(b[0], b[1]), bf16_pair(b[2], b[3])},
+                    reinterpret_cast<v4u*>(reinterpret_cast<uint16_t*>(C) + at));
             } else {
-                put<LINES>(reinterpret_cast<v4f*>(reinterpret_cast<float*>(C) + at), f[0]);
+                __builtin_nontemporal_store(f[0], reinterpret_cast<v4f*>(reinterpret_cast<float*>(C) + at));
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -167,9 +161,7 @@ hipError_t launch_gemm_depth_short(const uint8_t* aq, const uint8_t* as, const u
     const int64_t cols = (N + kTile - 1) / kTile, gx = per_xcd ? cols : (cols + 7) / 8 * 8;
     const GroupArgs ga{offsets, (int)experts, rows};
     const dim3 grid((unsigned)(gx * tm * (per_xcd ? (experts + 7) / 8 * 8 : experts)));
-    const bool lines = N * (out_bf16 ? 2 : 4) % 128 == 0;
-    auto* const k = out_bf16 ? (lines ? &gemm_mx_depth<true, true> : &gemm_mx_depth<true, false>)
-                             : (lines ? &gemm_mx_depth<false, true> : &gemm_mx_depth<false, false>);
+    auto* const k = out_bf16 ? &gemm_mx_depth<true> : &gemm_mx_depth<false>;
     return launch(k, grid, dim3(256), st, aq, as, bq, bs, M, N, K, c, (int)tm, (int)gx, (int)per_xcd, ga);
 }
 

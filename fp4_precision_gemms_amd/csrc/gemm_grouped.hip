@@ -471,12 +471,12 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_grouped(
 
             // The tile's rows of C as one buffer; this lane's offset in its
             // first row, out of range for columns past N.  What lies past the
-            // last row is past the buffer's end.  Non-temporal where the rows
-            // are whole 128-byte lines (8 experts of 512 rows, 14336 x 4096, in
-            // bf16 on 128-row tiles: 156 us, 180 with plain stores).
+            // last row is past the buffer's end.  Non-temporal (8 experts of
+            // 512 rows, 14336 x 4096, in bf16 on 128-row tiles: 156 us, 180 with
+            // plain stores; 8 of 2000 rows and 8160 x 4064, whose rows are no
+            // whole lines: 271 and 303, their weight gradient 321 and 372).
             const int er = lane / (64 / kEpiRows), ec = lane % (64 / kEpiRows) * kEpiRows;
             const uint32_t row_bytes = (uint32_t)N * kOut;
-            const bool lines = row_bytes % 128 == 0;
             const __amdgpu_buffer_rsrc_t rc = raw_buffer(
                 (uint8_t*)C + (cbase + c0 * N + n0) * kOut, (rows_a * N - n0) * kOut);
             const uint32_t offc = n0 + 64 * wave + ec < N
@@ -522,8 +522,7 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_grouped(
 #pragma unroll
                 for (int k = 0; k < 32 / kEpiRows; ++k) {
                     const uint32_t at = offc + (uint32_t)(32 * i + kEpiRows * k) * row_bytes;
-                    if (lines) __builtin_amdgcn_raw_buffer_store_b128(o[k], rc, at, 0, 2);
-                    else __builtin_amdgcn_raw_buffer_store_b128(o[k], rc, at, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(o[k], rc, at, 0, 2);
                 }
             }
         };
