@@ -17,9 +17,11 @@
 // (MXFP4) for the codes.  Each element is read once and kept in registers
 // (bf16 pairs) across the reduction.
 //
-// Backward, with g = dy w and c = sum_j g_j h_j over the row:
-//     dx = r g - h r^3 c / C (+ dh)          (dh: the gradient that reaches h past the norm)
-//     dw = sum over rows of dy h r
+// Backward, with g = dy w, n = h r and c = sum_j g_j n_j over the row:
+//     dx = r (g - n c / C) (+ dh)            (dh: the gradient that reaches h past the norm)
+//     dw = sum over rows of dy n
+// By way of n, of order one, and not of h and r^3, which leave binary32 when
+// the row's scale does not: rows of 1e-13 or 1e13 already.
 // (the quantization is passed straight through).  A workgroup walks over rows
 // with its columns' part of dw in registers, so dy and h are read once; the
 // parts of all workgroups are summed in a fixed order by a second kernel.
@@ -257,8 +259,9 @@ __global__ __launch_bounds__(TPR) void rmsnorm_back(
             unpack8(wv[i], w);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
+                b[k] *= r1;
                 s += (a[k] * w[k]) * b[k];
-                acc[i][k] += a[k] * (b[k] * r1);
+                acc[i][k] += a[k] * b[k];
             }
         }
         s = wave_sum(s);
@@ -271,7 +274,7 @@ __global__ __launch_bounds__(TPR) void rmsnorm_back(
 #pragma unroll
             for (int i = 0; i < kWaves; ++i) s += part[turn][i];
         }
-        const float k3 = r1 * r1 * r1 * (s * inv_cols);
+        s *= inv_cols;
         const int64_t base = row * nch;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -284,7 +287,7 @@ __global__ __launch_bounds__(TPR) void rmsnorm_back(
             if constexpr (DH) unpack8(e1[i], e);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                a[k] = r1 * (a[k] * w[k]) - b[k] * k3;
+                a[k] = r1 * (a[k] * w[k] - (b[k] * r1) * s);
                 if constexpr (DH) a[k] += e[k];
             }
             dx[base + c] = pack8(a);

@@ -375,8 +375,8 @@ fp4_status fp4_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16,
 /*
  * fp4_rmsnorm_backward -- gradients of y = h r weight (the quantization is
  * passed straight through), from dy bf16 [rows, cols], the h and rstd of the
- * forward pass and the weight.  With g = dy weight and c = sum_j g_j h_j:
- *   dx = bf16(r g - h r^3 c / C + dh), dh (bf16, may be NULL) the gradient
+ * forward pass and the weight.  With g = dy weight and c = sum_j g_j h_j r:
+ *   dx = bf16(r (g - h r c / C) + dh), dh (bf16, may be NULL) the gradient
  *        that reaches h past the norm; dx is the gradient of x and of the
  *        residual alike, and may be dh itself (in place) but no other input;
  *   dw[cols] = sum over rows of dy h r, fp32, summed in an order that depends

@@ -254,3 +254,22 @@ def test_another_stream_and_a_captured_graph():
         for a, b, c in zip(want, caught, side):
             assert torch.equal(a, b) and torch.equal(a, c), i
         work()
+
+
+@pytest.mark.parametrize("scale", [1e-18, 1e18, 1e30])
+def test_backward_of_rows_far_from_one(scale):
+    """h so small or large that r^3, or c = sum g h, leaves binary32: dx is the
+    gradient all the same (eps = 0)."""
+    need_gpu()
+    rows, cols = 7, 352
+    rng = np.random.default_rng(12)
+    h = R.to_bf16(rng.standard_normal((rows, cols)) * scale)
+    w = R.to_bf16(1 + 0.1 * rng.standard_normal(cols))
+    dy = R.to_bf16(rng.standard_normal((rows, cols)))
+    h0, rstd, _ = R.rmsnorm(h, None, w, 0.0)
+    assert np.array_equal(h0, h) and np.isfinite(rstd).all() and (rstd > 2.0 ** -126).all()
+    dx, dw = F.fp4_rmsnorm_backward(bf(dy), bf(h), bf(w), torch.from_numpy(rstd).cuda())
+    torch.cuda.synchronize()
+    ref, near, dwref, dwsize = back_reference(dy, h, w, rstd, None)
+    assert (np.abs(dx.double().cpu().numpy() - ref) <= near).all()
+    assert (np.abs(dw.double().cpu().numpy() - dwref) <= 64 * U32 * dwsize).all()
