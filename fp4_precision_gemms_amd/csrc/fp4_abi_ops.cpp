@@ -1,6 +1,8 @@
 // fp4_abi_ops.cpp -- the C ABI's norm, few-row and grouped entry points
 // (declared in include/fp4.h): argument validation, then dispatch to the HIP
-// launchers, with no HIP call before every argument has been checked.
+// launchers, with no HIP call before every argument has been checked.  Shapes
+// come before pointers: an empty batch, whose pointers are NULL, is refused for
+// its shape.
 #include "fp4.h"
 
 #include <hip/hip_runtime.h>
@@ -25,8 +27,8 @@ fp4_status fp4_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16, c
                                 float* rstd, void* y_bf16, uint8_t* codes, uint8_t* scales, void* stream) {
     if (fmt != FP4_FMT_MXFP4 && fmt != FP4_FMT_MXFP8) return FP4_ERR_ENUM;
     if (!(eps >= 0.0)) return FP4_ERR_ENUM;
-    if (!x_bf16 || !weight_bf16 || !codes || !scales || (residual_bf16 && !h_bf16)) return FP4_ERR_NULL;
     if (const fp4_status s = check_norm_shape(rows, cols)) return s;
+    if (!x_bf16 || !weight_bf16 || !codes || !scales || (residual_bf16 && !h_bf16)) return FP4_ERR_NULL;
     if (!aligned16(x_bf16) || !aligned16(residual_bf16) || !aligned16(weight_bf16) || !aligned16(h_bf16) ||
         !aligned4(rstd) || !aligned16(y_bf16) || !aligned16(codes) || !aligned16(scales))
         return FP4_ERR_ALIGN;
@@ -44,8 +46,8 @@ fp4_status fp4_rmsnorm_backward(const void* dy_bf16, const void* h_bf16, const v
                                 const float* rstd, const void* dh_bf16, int64_t rows, int64_t cols,
                                 void* dx_bf16, float* dw, void* workspace, size_t workspace_bytes,
                                 void* stream) {
-    if (!dy_bf16 || !h_bf16 || !weight_bf16 || !rstd || !dx_bf16 || !dw) return FP4_ERR_NULL;
     if (const fp4_status s = check_norm_shape(rows, cols)) return s;
+    if (!dy_bf16 || !h_bf16 || !weight_bf16 || !rstd || !dx_bf16 || !dw) return FP4_ERR_NULL;
     if (!workspace || workspace_bytes < fp4_rmsnorm_workspace_bytes(rows, cols)) return FP4_ERR_WORKSPACE;
     if (!aligned16(dy_bf16) || !aligned16(h_bf16) || !aligned16(weight_bf16) || !aligned4(rstd) ||
         !aligned16(dh_bf16) || !aligned16(dx_bf16) || !aligned16(dw) || !aligned16(workspace))
@@ -62,7 +64,6 @@ fp4_status check_grouped_product(const uint8_t* a, const uint8_t* as, fp4_format
                                  const void* c, fp4_out_dtype out) {
     if (fmt != FP4_FMT_MXFP4 && fmt != FP4_FMT_MXFP8) return FP4_ERR_ENUM;
     if (out != FP4_OUT_F32 && out != FP4_OUT_BF16) return FP4_ERR_ENUM;
-    if (!a || !as || !wq || !ws || !c) return FP4_ERR_NULL;
     if (rows <= 0 || N <= 0 || K <= 0 || K % 32 || K >= kMaxContraction || rows > INT32_MAX || N > INT32_MAX ||
         experts <= 0 || experts > kMaxExperts)
         return FP4_ERR_SHAPE;
@@ -71,6 +72,7 @@ fp4_status check_grouped_product(const uint8_t* a, const uint8_t* as, fp4_format
         return FP4_ERR_SHAPE;
     // tiles are counted in 32 bits, also where offsets out of order overlap
     if (experts * (rows / 128 + 1) * ((N + 255) / 256) > INT32_MAX) return FP4_ERR_SHAPE;
+    if (!a || !as || !wq || !ws || !c) return FP4_ERR_NULL;
     if (!aligned16(a) || !aligned16(as) || !aligned16(wq) || !aligned16(ws) || !aligned16(c)) return FP4_ERR_ALIGN;
     return FP4_OK;
 }
@@ -91,12 +93,12 @@ fp4_status fp4_quantize_grouped(const void* x_bf16, const int32_t* offsets, int6
     if (had != FP4_HAD_NONE && had != FP4_HAD_DET && had != FP4_HAD_SIGNED) return FP4_ERR_ENUM;
     if (had != FP4_HAD_NONE && had_n != 16 && had_n != 32) return FP4_ERR_ENUM;
     if (rnd != FP4_RTN && rnd != FP4_SR) return FP4_ERR_ENUM;
-    if (!x_bf16 || !offsets || (!codes_rows && !codes_cols) || !codes_rows != !scales_rows ||
-        !codes_cols != !scales_cols)
-        return FP4_ERR_NULL;
     if (rows <= 0 || rows > INT32_MAX || cols <= 0 || cols % 32 || cols >= kMaxContraction || experts <= 0 ||
         experts > kMaxExperts || ((cols + 255) / 256) * (rows / 32 + 8 * experts) > INT32_MAX)
         return FP4_ERR_SHAPE;
+    if (!x_bf16 || !offsets || (!codes_rows && !codes_cols) || !codes_rows != !scales_rows ||
+        !codes_cols != !scales_cols)
+        return FP4_ERR_NULL;
     if (!aligned16(x_bf16) || !aligned4(offsets) || !aligned16(codes_rows) || !aligned16(scales_rows) ||
         !aligned16(codes_cols) || !aligned16(scales_cols))
         return FP4_ERR_ALIGN;
@@ -108,8 +110,8 @@ fp4_status fp4_quantize_grouped(const void* x_bf16, const int32_t* offsets, int6
 fp4_status fp4_gemm_grouped(const uint8_t* a, const uint8_t* as, fp4_format fmt, const int32_t* offsets,
                             int64_t experts, int64_t rows, const uint8_t* wq, const uint8_t* ws, int64_t N,
                             int64_t K, void* c, fp4_out_dtype out, void* stream) {
-    if (!offsets) return FP4_ERR_NULL;
     if (const fp4_status s = check_grouped_product(a, as, fmt, wq, ws, experts, rows, N, K, c, out)) return s;
+    if (!offsets) return FP4_ERR_NULL;
     if (!aligned4(offsets)) return FP4_ERR_ALIGN;
     // Over 32 rows an expert on average the few-row kernel, which reads the
     // weights once per 64 rows, is the slower one (40 experts of 736 x 1120:
@@ -126,7 +128,6 @@ fp4_status fp4_gemm_grouped_wgrad(const uint8_t* dytq, const uint8_t* dyts, cons
                                   const uint8_t* xts, const int32_t* offsets, int64_t experts, int64_t rows,
                                   int64_t N, int64_t K, void* dw, fp4_out_dtype out, void* stream) {
     if (out != FP4_OUT_F32 && out != FP4_OUT_BF16) return FP4_ERR_ENUM;
-    if (!dytq || !dyts || !xtq || !xts || !offsets || !dw) return FP4_ERR_NULL;
     if (rows <= 0 || N <= 0 || K <= 0 || N % 32 || K % 32 || rows > INT32_MAX || N > INT32_MAX || K > INT32_MAX ||
         experts <= 0 || experts > kMaxExperts || 256 * (rows / 256 + experts) >= kMaxContraction ||
         (rows / 256 + experts) * (N > K ? N : K) >= (INT64_C(1) << 28) || K >= (INT64_C(1) << 21))
@@ -134,6 +135,7 @@ fp4_status fp4_gemm_grouped_wgrad(const uint8_t* dytq, const uint8_t* dyts, cons
     if (!product_ok(N, K) || !product_ok(N * K, experts) ||
         ((N + 255) / 256) * ((K + 255) / 256) >= kMaxTiles / experts)
         return FP4_ERR_SHAPE;
+    if (!dytq || !dyts || !xtq || !xts || !offsets || !dw) return FP4_ERR_NULL;
     if (!aligned16(dytq) || !aligned16(dyts) || !aligned16(xtq) || !aligned16(xts) || !aligned4(offsets) ||
         !aligned16(dw))
         return FP4_ERR_ALIGN;

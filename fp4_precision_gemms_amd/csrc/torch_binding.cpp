@@ -11,6 +11,7 @@
 // package's Fp4Error.
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/utils/object_ptr.h>
 
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
@@ -132,13 +133,14 @@ PyObject* tuple(const T&... t) {
     return r;
 }
 
-// items of an `out` argument
-std::vector<PyObject*> items(PyObject* o, Py_ssize_t n) {
-    PyObject* f = PySequence_Fast(o, "out must be a sequence of tensors");
+// The items of an `out` argument: any sequence or iterator of tensors.
+std::vector<at::Tensor> items(PyObject* o, Py_ssize_t n) {
+    const THPObjectPtr f(PySequence_Fast(o, "out must be a sequence of tensors"));
     if (!f) throw python_error();
-    std::vector<PyObject*> v(PySequence_Fast_ITEMS(f), PySequence_Fast_ITEMS(f) + PySequence_Fast_GET_SIZE(f));
-    Py_DECREF(f);                   // the caller's object keeps the items
-    if ((Py_ssize_t)v.size() != n) fail(PyExc_ValueError, "out must hold %d tensors, got %d", (int)n, (int)v.size());
+    if (PySequence_Fast_GET_SIZE(f.get()) != n)
+        fail(PyExc_ValueError, "out must hold %d tensors, got %d", (int)n, (int)PySequence_Fast_GET_SIZE(f.get()));
+    std::vector<at::Tensor> v;
+    for (Py_ssize_t i = 0; i < n; ++i) v.push_back(tensor(PySequence_Fast_GET_ITEM(f.get(), i), "output"));
     return v;
 }
 
@@ -296,7 +298,7 @@ PyObject* quantize_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& off = tensor(a[1], "offsets");
     const int64_t rows = x.size(0), cols = x.size(1), E = experts_of(off, x), axes = integer(a[2]);
     const c10::DeviceGuard guard(x.device());
-    std::vector<PyObject*> given;
+    std::vector<at::Tensor> given;
     if (a[9] != Py_None) given = items(a[9], axes == 3 ? 4 : 2);
     at::Tensor out[4];
     int m = 0;

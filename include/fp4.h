@@ -28,7 +28,8 @@
  *   - Pointers are device pointers (hipMalloc / torch CUDA tensors) owned by
  *     the caller, 16-byte aligned, tensors contiguous row-major.  The library
  *     allocates nothing in these calls and keeps no state between calls,
- *     except the device workspace the caller passes to nvfp4_quantize.
+ *     except the device workspace the caller passes to nvfp4_quantize and
+ *     fp4_rmsnorm_backward.
  *   - `stream` is a hipStream_t (NULL = the null stream).  Every call only
  *     enqueues work on it and returns; results are ready when the stream is.
  *   - Arguments are validated before any HIP call.  The status code is the
