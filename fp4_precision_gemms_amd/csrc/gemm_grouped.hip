@@ -18,11 +18,11 @@
 //   - Loads have no tails: code rows past the operand read as zero, scale rows
 //     as whatever follows them (they reach no output that is stored), stages
 //     past the last or before the first as the nearest one.
-//   - A contraction that is no multiple of four stages starts with up to three
-//     that are not of the tile.  Row groups multiply them with scales of 2^-127
-//     on both sides, so that they vanish, like the last stage's blocks past the
-//     operand's end.  Depth groups, whose experts are rarely a multiple of four
-//     stages long, do not multiply them: see the tile loop.
+//   - A contraction that is no multiple of four stages.  Row groups, all of one
+//     length, have a kernel for each remainder, whose tiles start at another
+//     slot of the ring.  An expert's depth is known on the device only, so depth
+//     groups start with up to three stages that are not of the tile, load but
+//     do not multiply them: see the tile loop.
 //   - The epilogue stores through a buffer that ends with the tile's last row,
 //     16 bytes a lane, so a partial tile takes no branch and the next tile's
 //     first stages are always in flight by then.
@@ -65,7 +65,9 @@ __device__ __forceinline__ int* expert_ints() {
 
 // M: rows of A's scale layout; K: elements per row of A's and B's layouts;
 // tiles_m: row tiles of an expert's output (depth groups).
-template <int FM, bool OBF16, int GROUP>
+// PHASE: the ring slot of a tile's first stage, for row groups such that the
+// last one falls into slot 3 (0 for depth groups).
+template <int FM, bool OBF16, int GROUP, int PHASE>
 __global__ __launch_bounds__(kThreads) void gemm_mx_grouped(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ SA, const uint8_t* __restrict__ B,
     const uint8_t* __restrict__ SB, int64_t M, int64_t N, int64_t K, void* __restrict__ C, int tiles_m,
@@ -96,11 +98,11 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_grouped(
     const int64_t nb = K / 32;                         // blocks per row of the layout
     const uint32_t gstride = (uint32_t)(nb * 512);     // bytes per 32-row group of codes
     int ntiles;
-    // of the tile: k-steps, 256-k stages, and the first of the stages whose
-    // count is rounded up to a multiple of the ring (0 or less)
+    // of the tile: k-steps, 256-k stages, and the first of the stages (depth
+    // groups: 0 or less, their count rounded up to a multiple of the ring)
     int nks = (int)((nb + 1) / 2);
     int nk = (int)((nb + 7) / 8);
-    int kfirst = -((kSlots - nk % kSlots) % kSlots);
+    int kfirst = 0;
     if constexpr (GROUP == kRowGroups) {
         // ends[e]: row tiles of experts 0 .. e
         int* const los = expert_ints<0>();
@@ -262,8 +264,8 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_grouped(
     // ---- registers -----------------------------------------------------
     v16f acc[FM][FN];
     v4i fa[2][FM];                 // A fragments of two k-steps (k-step parity)
-    v4i fb[kRing][FN];             // B fragments, k-step s in fb[s mod 8]
-    BSc bsc[kSlots];               // B scales, stage kt in bsc[(kt - kfirst) mod 4]
+    v4i fb[kRing][FN];             // B fragments, k-step s in fb[(s + 4 PHASE) mod 8]
+    BSc bsc[kSlots];               // B scales, stage kt in bsc[(kt - kfirst + PHASE) mod 4]
     struct ASc { uint32_t w[FM][2]; };
     ASc asc[2];                    // A scales of the current and next stage
 
@@ -302,10 +304,9 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_grouped(
 #pragma unroll
         for (int j = 0; j < FN; ++j) w.b[j] = stage_scale_word(sb.w[j][0], sb.w[j][1], h);
         if constexpr (GROUP == kRowGroups) {
-            // A stage before the first holds stage 0's bytes, and blocks past
-            // the last one whatever follows: with both scales 2^-127 their
-            // products vanish.
-            const uint32_t keep = kt < 0 ? 0u : kt == nk - 1 ? last_keep : ~0u;
+            // Blocks past the last one hold whatever follows: with both scales
+            // 2^-127 their products vanish.
+            const uint32_t keep = kt == nk - 1 ? last_keep : ~0u;
 #pragma unroll
             for (int i = 0; i < FM; ++i) w.a[i] &= keep;
 #pragma unroll
@@ -389,28 +390,28 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_grouped(
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    // The first stages of a tile: A stages kfirst .. kfirst+2 into slots
-    // 0..2, B scales of the first two stages, B k-steps of the first two
+    // The first stages of a tile: A stages kfirst .. kfirst+2 into the slots
+    // from PHASE on, B scales of the first two stages, B k-steps of the first two
     // stages, in stage order, so that the wait for stage kfirst counts
     // everything after its A part (the scheduling barriers keep this order).
     auto prologue = [&]() FP4_INLINE {
-        dma_a(kfirst, slots[0], 0, FM, true);
+        dma_a(kfirst, slots[PHASE], 0, FM, true);
         __builtin_amdgcn_sched_barrier(0);
-        bsc[0] = load_bsc(kfirst);
+        bsc[PHASE] = load_bsc(kfirst);
 #pragma unroll
         for (int s = 0; s < kKS; ++s)
 #pragma unroll
-            for (int j = 0; j < FN; ++j) fb[s][j] = load_b(4 * kfirst + s, j);
+            for (int j = 0; j < FN; ++j) fb[(4 * PHASE + s) % kRing][j] = load_b(4 * kfirst + s, j);
         __builtin_amdgcn_sched_barrier(0);
-        dma_a(kfirst + 1, slots[1], 0, FM, true);
+        dma_a(kfirst + 1, slots[(PHASE + 1) % kSlots], 0, FM, true);
         __builtin_amdgcn_sched_barrier(0);
-        bsc[1] = load_bsc(kfirst + 1);
+        bsc[(PHASE + 1) % kSlots] = load_bsc(kfirst + 1);
 #pragma unroll
         for (int s = kKS; s < 2 * kKS; ++s)
 #pragma unroll
-            for (int j = 0; j < FN; ++j) fb[s][j] = load_b(4 * kfirst + s, j);
+            for (int j = 0; j < FN; ++j) fb[(4 * PHASE + s) % kRing][j] = load_b(4 * kfirst + s, j);
         __builtin_amdgcn_sched_barrier(0);
-        dma_a(kfirst + 2, slots[2], 0, FM, true);
+        dma_a(kfirst + 2, slots[(PHASE + 2) % kSlots], 0, FM, true);
         __builtin_amdgcn_sched_barrier(0);
     };
     // VMEM issued after stage kfirst's A part in the prologue: its B scales,
@@ -443,13 +444,18 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_grouped(
             for (int j = 0; j < FN; ++j)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-        read_ascales(0, asc[0]);
-        read_afrags(0, 0, 0);
+        read_ascales(PHASE, asc[PHASE & 1]);
+        read_afrags(PHASE, 0, 0);
         // The tile's stages and its epilogue, after `dead` stages that are not
         // of the tile (loads only).
         auto tile = [&](auto dead) FP4_INLINE {
             constexpr int D = decltype(dead)::value;
             int kt = kfirst;
+            if constexpr (PHASE > 0) {
+                if constexpr (PHASE < 2) run_stage(1, kt++);
+                if constexpr (PHASE < 3) run_stage(2, kt++);
+                run_stage(3, kt++);
+            }
             if constexpr (D > 0) {
                 run_stage(0, kt, false);
                 run_stage(1, kt + 1, D < 2);
@@ -483,8 +489,8 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_grouped(
                                       ? (uint32_t)er * row_bytes + (uint32_t)(64 * wave + ec) * kOut
                                       : kOob;
 
-            // The next tile's first stages go out now, into slots 0..2 (this
-            // epilogue stages in slot 3); waited for at the next tile's start.
+            // The next tile's first stages go out now, into three slots (this
+            // epilogue stages in the fourth); waited for at the next tile's start.
             const int tn = t + (int)gridDim.x;
             if (tn < ntiles) {
                 set_tile(tn);
@@ -493,9 +499,9 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_grouped(
 
             // acc[i][j] holds C^T of a 32x32 tile: register r of lane l is
             // n = 8 (r / 4) + 4 (l / 32) + r mod 4, m = l mod 32.  Each wave
-            // stages 32 rows x its 64 columns at a time in its quarter of slot
-            // 3 (rows padded by 16 bytes), then reads back whole row segments.
-            uint8_t* const reg = lds3 + wave * kEpiRegion;
+            // stages 32 rows x its 64 columns at a time in its quarter of that
+            // slot (rows padded by 16 bytes), then reads back whole row segments.
+            uint8_t* const reg = slots[(PHASE + 3) % kSlots] + wave * kEpiRegion;
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
 #pragma unroll
@@ -531,8 +537,7 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_grouped(
             // tokens, 14336 x 4096 632 us with them, 581 without.  Each count
             // has code of its own from the first stage to the last store: where
             // the accumulators of two paths met, the compiler spilled hundreds
-            // of registers.  (Row groups, with more registers in use, lost 5-10 %
-            // this way.)
+            // of registers.
             switch (-kfirst) {
                 case 1: tile(std::integral_constant<int, 1>{}); break;
                 case 2: tile(std::integral_constant<int, 2>{}); break;
@@ -545,14 +550,24 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_grouped(
     }
 }
 
-template <int FM, int GROUP>
+template <int FM, int GROUP, int PHASE>
 hipError_t launch_grouped(const uint8_t* aq, const uint8_t* as, const uint8_t* bq, const uint8_t* bs, int64_t M,
                           int64_t N, int64_t K, void* c, int out_bf16, int64_t most, int64_t tm, int64_t tn,
                           const GroupArgs& ga, hipStream_t st) {
     const int64_t cus = cu_count();
     const dim3 grid((unsigned)(most < cus ? most : cus));
-    auto* const k = out_bf16 ? &gemm_mx_grouped<FM, true, GROUP> : &gemm_mx_grouped<FM, false, GROUP>;
+    auto* const k = out_bf16 ? &gemm_mx_grouped<FM, true, GROUP, PHASE> : &gemm_mx_grouped<FM, false, GROUP, PHASE>;
     return launch(k, grid, dim3(kThreads), st, aq, as, bq, bs, M, N, K, c, (int)tm, (int)tn, ga);
+}
+
+template <int FM, typename... T>
+hipError_t launch_rows(int64_t stages, T... a) {
+    switch (stages % kSlots) {
+        case 1: return launch_grouped<FM, kRowGroups, 3>(a...);
+        case 2: return launch_grouped<FM, kRowGroups, 2>(a...);
+        case 3: return launch_grouped<FM, kRowGroups, 1>(a...);
+        default: return launch_grouped<FM, kRowGroups, 0>(a...);
+    }
 }
 
 }  // namespace
@@ -568,6 +583,7 @@ hipError_t launch_gemm_row_groups(const uint8_t* aq, const uint8_t* as, const in
                                   int64_t rows, const uint8_t* wq, const uint8_t* ws, int64_t N, int64_t K, void* c,
                                   int out_bf16, hipStream_t st) {
     const int64_t M = 32 * (rows / 32 + experts), tn = (N + kBN - 1) / kBN, cus = cu_count();
+    const int64_t stages = (K + 255) / 256;
     const GroupArgs ga{offsets, (int)experts, rows};
     // Tile rows: rounds of the persistent grid times a tile's time, with half a
     // tile per expert for its last one.  A tile of 128 rows takes 0.53-0.62 of
@@ -576,9 +592,9 @@ hipError_t launch_gemm_row_groups(const uint8_t* aq, const uint8_t* as, const in
     // 2048, 200 rows 33 against 40.
     auto rounds = [&](int64_t bm) { return ((rows / bm + (experts + 1) / 2) * tn + cus - 1) / cus; };
     if (58 * rounds(128) < 100 * rounds(256))
-        return launch_grouped<4, kRowGroups>(aq, as, wq, ws, M, N, K, c, out_bf16, (rows / 128 + experts) * tn, 0, tn,
+        return launch_rows<4>(stages, aq, as, wq, ws, M, N, K, c, out_bf16, (rows / 128 + experts) * tn, 0, tn,
                                              ga, st);
-    return launch_grouped<8, kRowGroups>(aq, as, wq, ws, M, N, K, c, out_bf16, (rows / 256 + experts) * tn, 0, tn, ga,
+    return launch_rows<8>(stages, aq, as, wq, ws, M, N, K, c, out_bf16, (rows / 256 + experts) * tn, 0, tn, ga,
                                          st);
 }
 
@@ -587,7 +603,7 @@ hipError_t launch_gemm_depth_groups(const uint8_t* aq, const uint8_t* as, const 
                                     int out_bf16, hipStream_t st) {
     const int64_t K = 256 * (rows / 256 + experts);             // of the grouped layout
     const int64_t tm = (M + 255) / 256, tn = (N + kBN - 1) / kBN;
-    return launch_grouped<8, kDepthGroups>(aq, as, bq, bs, M, N, K, c, out_bf16, tm * tn * experts, tm, tn,
+    return launch_grouped<8, kDepthGroups, 0>(aq, as, bq, bs, M, N, K, c, out_bf16, tm * tn * experts, tm, tn,
                                            GroupArgs{offsets, (int)experts, rows}, st);
 }
 

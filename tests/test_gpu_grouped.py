@@ -70,6 +70,30 @@ def test_many_rows_large_tiles(split, N, K, out_dtype):
     check(out, ref, mag)
 
 
+@pytest.mark.parametrize("split,N", [("uneven", 304), ("seventy", 304), ("empty", 2560)])
+@pytest.mark.parametrize("K", [64, 480, 736, 1024, 1120, 1408, 1760, 2048, 2784])
+def test_many_rows_of_each_contraction(split, N, K):
+    """1 to 8 and 11 stages of 256 elements, in the 128-row and in the 256-row
+    tiles."""
+    need_gpu()
+    rows, offsets = {**MANY, **LARGE}[split]
+    E = len(offsets) - 1
+    say("grouped contraction", split, N, K)
+    rng = np.random.default_rng(rows + K)
+    a, ws = random_mx4(rng, rows, K), [random_mx4(rng, N, K) for _ in range(min(E, 3))]
+    ops = [operand(*w) for w in ws]
+    which = [e % len(ws) for e in range(E)]
+    out = F.fp4_gemm_grouped(*grouped_operand(*a, rows, offsets), dev_offsets(offsets),
+                             torch.stack([ops[i][0] for i in which]), torch.stack([ops[i][1] for i in which]), rows,
+                             out=torch.full((rows, N), 77.0, device="cuda"), out_dtype=F.OUT_F32)
+    torch.cuda.synchronize()
+    av, wv = values(*a), [values(*w) for w in ws]
+    ref, mag = np.full((rows, N), 77.0), np.zeros((rows, N))
+    for i, lo, hi in zip(which, offsets, offsets[1:]):
+        ref[lo:hi], mag[lo:hi] = av[lo:hi] @ wv[i].T, np.abs(av[lo:hi]) @ np.abs(wv[i]).T
+    check(out, ref, mag)
+
+
 @pytest.mark.parametrize("split", ["odd", "uneven", "two"])
 def test_nan_blocks_stay_in_their_rows(split):
     """A NaN scale in one row of A, in one weight row of one expert, and a NaN
