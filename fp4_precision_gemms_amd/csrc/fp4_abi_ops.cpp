@@ -113,11 +113,16 @@ fp4_status fp4_gemm_grouped(const uint8_t* a, const uint8_t* as, fp4_format fmt,
     if (const fp4_status s = check_grouped_product(a, as, fmt, wq, ws, experts, rows, N, K, c, out)) return s;
     if (!offsets) return FP4_ERR_NULL;
     if (!aligned4(offsets)) return FP4_ERR_ALIGN;
-    // Over 32 rows an expert on average the few-row kernel, which reads the
-    // weights once per 64 rows, is the slower one (40 experts of 736 x 1120:
-    // 12.2 against 12.7 us at 50 rows, 16.5 and 13.0 at 100; 8 experts of 14336
-    // x 4096: 78 and 46 us at 64).
-    if (fmt == FP4_FMT_MXFP4 && rows > 32 * experts && fp4dev::row_groups_fit(experts, rows, N, K))
+    // Up to 32 rows an expert on average the few-row kernel, which reads the
+    // weights once per 64 rows at most (64 experts of 1408 x 1408: 20.4 against
+    // 29.2 us at 32 rows, 23.0 and 19.6 at 48; 40 of 736 x 1120: 7.6 and 8.6 at
+    // 32, 9.6 and 8.8 at 48).  Few experts with a small output also beyond: the
+    // large tiles, too few of them for the CUs, take the time of one (one expert
+    // of 4096 x 4096: 5.3 against 14.3 us at 64 rows, 12.5 and 14.7 at 256, 22.8
+    // and 15.1 at 512; 4 of them 12.8 and 15.1 at 64, 16.2 and 15.2 at 96; but 32
+    // of 768 x 2048: 11.8 and 10.3 at 40).
+    const bool few = rows <= 32 * experts || (experts <= 16 && rows * N <= (INT64_C(1) << 20));
+    if (fmt == FP4_FMT_MXFP4 && !few && fp4dev::row_groups_fit(experts, rows, N, K))
         return from_hip(fp4dev::launch_gemm_row_groups(a, as, offsets, experts, rows, wq, ws, N, K, c,
                                                        out == FP4_OUT_BF16, (hipStream_t)stream));
     return from_hip(fp4dev::launch_gemm_few(a, as, fmt == FP4_FMT_MXFP8, offsets, wq, ws, rows, experts, N, K, c,

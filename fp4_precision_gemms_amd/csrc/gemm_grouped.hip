@@ -586,11 +586,15 @@ hipError_t launch_gemm_row_groups(const uint8_t* aq, const uint8_t* as, const in
     const int64_t stages = (K + 255) / 256;
     const GroupArgs ga{offsets, (int)experts, rows};
     // Tile rows: rounds of the persistent grid times a tile's time, with half a
-    // tile per expert for its last one.  A tile of 128 rows takes 0.53-0.62 of
+    // tile per expert for its last one, and a whole one where that is all it has
+    // (64 experts of 1408 x 1408, 40 rows each: 20 us, 29 without this).  A tile of 128 rows takes 0.53-0.62 of
     // one of 256 (it loads as much of B): 8 experts of 14336 x 4096, 256 rows
     // each 92 against 100 us, 2048 rows 574 against 526; 32 experts of 2048 x
     // 2048, 200 rows 33 against 40.
-    auto rounds = [&](int64_t bm) { return ((rows / bm + (experts + 1) / 2) * tn + cus - 1) / cus; };
+    auto rounds = [&](int64_t bm) {
+        const int64_t half = rows / bm + (experts + 1) / 2;
+        return ((half > experts ? half : experts) * tn + cus - 1) / cus;
+    };
     if (58 * rounds(128) < 100 * rounds(256))
         return launch_rows<4>(stages, aq, as, wq, ws, M, N, K, c, out_bf16, (rows / 128 + experts) * tn, 0, tn,
                                              ga, st);

@@ -70,11 +70,11 @@ def test_many_rows_large_tiles(split, N, K, out_dtype):
     check(out, ref, mag)
 
 
-@pytest.mark.parametrize("split,N", [("uneven", 304), ("seventy", 304), ("empty", 2560)])
+@pytest.mark.parametrize("split,N", [("uneven", 304), ("uneven", 1304), ("seventy", 304), ("empty", 2560)])
 @pytest.mark.parametrize("K", [64, 480, 736, 1024, 1120, 1408, 1760, 2048, 2784])
 def test_many_rows_of_each_contraction(split, N, K):
-    """1 to 8 and 11 stages of 256 elements, in the 128-row and in the 256-row
-    tiles."""
+    """1 to 8 and 11 stages of 256 elements, in the few-row kernel, the 128-row
+    tiles and the 256-row tiles."""
     need_gpu()
     rows, offsets = {**MANY, **LARGE}[split]
     E = len(offsets) - 1
