@@ -478,9 +478,10 @@ fp4_status fp4_gemm_grouped(const uint8_t* a, const uint8_t* as, fp4_format fmt,
  * from dY [rows, N] and X [rows, K] quantized along rows by
  * fp4_quantize_grouped with the same offsets, had, had_n and sign_seed.  dw is
  * [experts, N, K] in `out`, overwritten; that of an expert without rows is zero.
- * Requirements: N % 32 == 0, K % 32 == 0 (the quantizer's); 256 (rows / 256 +
- * experts) < 2^24, and (rows / 256 + experts) max(N, K) < 2^28, K < 2^21; at most 2^24 - 1 output tiles of 256 x 256; pointers 16-byte
- * aligned (offsets 4).
+ * Requirements: N % 32 == 0, K % 32 == 0 (the quantizer's), K < 2^21; 256
+ * (rows / 256 + experts) < 2^24 and (rows / 256 + experts) max(N, K) < 2^28;
+ * fewer than 2^24 output tiles of 256 x 256; pointers 16-byte aligned (offsets
+ * 4).
  */
 fp4_status fp4_gemm_grouped_wgrad(const uint8_t* dytq, const uint8_t* dyts, const uint8_t* xtq,
                                   const uint8_t* xts, const int32_t* offsets, int64_t experts,
