@@ -71,6 +71,32 @@ def test_grouped_quantizers(split, mode):
         check_cols(*got[2:], bits, rows, offsets, (32, F.HAD_NONE, 0, m[3]), 14)
 
 
+# two units per workgroup; with mostly short experts a stage per workgroup
+WIDE = {"two units": (5000, [7, 7, 2600, 4991], 3104), "stages": (*SPLITS["many"], 1312),
+        "stages of some": (400, [2] + [2 + 9 * i for i in range(30)] + [300] * 60 + [398], 1600)}
+
+
+@pytest.mark.parametrize("split", list(WIDE))
+@pytest.mark.parametrize("mode", ["had16 signed", "had32 sr"])
+def test_grouped_quantizers_of_wide_tensors(split, mode):
+    need_gpu()
+    rows, offsets, cols = WIDE[split]
+    E, m = len(offsets) - 1, MODES[mode]
+    say("quantize grouped, wide", split, mode)
+    bits = bf16_bits(np.random.default_rng(cols).standard_t(4, (rows, cols)))
+    x, off = to_gpu_bf16(bits), dev_offsets(offsets)
+    got = F.fp4_quantize_grouped(x, off, F.AXIS_ROWS, *m, sr_seed=11, out=out(rows, cols, E, F.AXIS_ROWS))
+    both = F.fp4_quantize_grouped_dual(x, off, *m, sr_seed_rows=11, sr_seed_cols=14,
+                                       out=out(rows, cols, E, F.AXIS_ROWS, F.AXIS_COLS))
+    cols_only = F.fp4_quantize_grouped(x, off, F.AXIS_COLS, 32, F.HAD_NONE, 0, m[3], sr_seed=14,
+                                       out=out(rows, cols, E, F.AXIS_COLS))
+    torch.cuda.synchronize()
+    check_rows(*got, bits, rows, offsets, m, 11)
+    check_cols(*cols_only, bits, rows, offsets, (32, F.HAD_NONE, 0, m[3]), 14)
+    for a, b in zip(both, (*got, *cols_only)):
+        assert torch.equal(a, b)
+
+
 def test_non_finite_values():
     need_gpu()
     rows, offsets = SPLITS["odd"]
