@@ -131,8 +131,12 @@ int main() {
     // few rows, many rows, many rows of MXFP8, and sizes the large tiles refuse
     REACHES(fp4_gemm_grouped(q, q, FP4_FMT_MXFP4, off, 8, 8 * 32, q, q, 64, 96, h, FP4_OUT_BF16, nullptr), "few");
     CHECK(g_p == off);
-    REACHES(fp4_gemm_grouped(q, q, FP4_FMT_MXFP4, off, 8, 8 * 32 + 1, q, q, 64, 96, h, FP4_OUT_BF16, nullptr), "rows");
-    CHECK(g_a == 8 && g_b == 257 && g_c == 64 && g_d == 96 && g_i == 1);
+    REACHES(fp4_gemm_grouped(q, q, FP4_FMT_MXFP4, off, 17, 17 * 32 + 1, q, q, 64, 96, h, FP4_OUT_BF16, nullptr), "rows");
+    CHECK(g_a == 17 && g_b == 545 && g_c == 64 && g_d == 96 && g_i == 1);
+    REACHES(fp4_gemm_grouped(q, q, FP4_FMT_MXFP4, off, 17, 17 * 32, q, q, 1 << 20, 96, h, FP4_OUT_BF16, nullptr), "few");
+    // up to 16 experts also 2^20 outputs
+    REACHES(fp4_gemm_grouped(q, q, FP4_FMT_MXFP4, off, 16, 1 << 14, q, q, 64, 96, h, FP4_OUT_BF16, nullptr), "few");
+    REACHES(fp4_gemm_grouped(q, q, FP4_FMT_MXFP4, off, 16, (1 << 14) + 1, q, q, 64, 96, h, FP4_OUT_BF16, nullptr), "rows");
     REACHES(fp4_gemm_grouped(q, q, FP4_FMT_MXFP8, off, 8, 10000, q, q, 64, 96, h, FP4_OUT_BF16, nullptr), "few");
     g_fit = false;
     REACHES(fp4_gemm_grouped(q, q, FP4_FMT_MXFP4, off, 8, 10000, q, q, 63, 96, h, FP4_OUT_BF16, nullptr), "few");
