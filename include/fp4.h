@@ -405,7 +405,8 @@ size_t fp4_rmsnorm_workspace_bytes(int64_t rows, int64_t cols);
  * made for M up to a few dozen, where the weights' bytes are the time.
  * Requirements: K % 32 == 0 and K < 2^24; M, N < 2^31; fewer than 2^24 tiles
  * of 128 x 256 outputs; pointers 16-byte aligned.  A scale byte of 0xFF makes
- * its block NaN.
+ * its block NaN; every other pair of scales gives the products within the fp32
+ * sums' rounding.
  */
 fp4_status fp4_gemm_decode(const uint8_t* a, const uint8_t* as, fp4_format fmt, const uint8_t* wq,
                            const uint8_t* ws, int64_t M, int64_t N, int64_t K, void* c,
