@@ -244,6 +244,9 @@ PyObject* gemm_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     arguments(n, 7);
     const at::Tensor &aq = tensor(a[0], "a codes"), &as = tensor(a[1], "a scales");
     const at::Tensor &wq = tensor(a[2], "w codes"), &ws = tensor(a[3], "w scales");
+    if (aq.dim() != 2 && aq.dim() != 3)
+        fail(PyExc_ValueError, "a codes must have two dimensions (MXFP8) or three (MXFP4), got shape %s",
+             text(aq.sizes()).c_str());
     const fp4_format fmt = aq.dim() == 2 ? FP4_FMT_MXFP8 : FP4_FMT_MXFP4;
     int64_t M, K;
     if (fmt == FP4_FMT_MXFP8) {
