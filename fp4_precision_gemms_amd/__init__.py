@@ -7,6 +7,12 @@ codes out (through ctypes; the norm, grouped and few-row operators, whose
 calls are short, through the CPython functions of csrc/torch_binding.cpp).  Every step of the computation runs in the HIP kernels of the
 library.  torch supplies device memory and the current HIP stream.
 
+A call runs on the current stream of its tensors' device, or on `stream` (a
+torch stream or a hipStream_t as an integer), which the caller orders against
+the streams that make the inputs and read the outputs; inputs that are freed
+before that stream is done are recorded on it (Tensor.record_stream), as for any
+torch operator on a side stream.
+
 If the libraries have not been built (``python -m fp4_precision_gemms_amd.build``)
 every call raises; there is no fallback.
 """
@@ -132,11 +138,33 @@ def _native():
     return _binding
 
 
-def _stream_of(stream, t: torch.Tensor) -> int:
-    """`stream` as an integer; by default the current stream of t's device."""
+def _as_stream(stream, device) -> torch.cuda.Stream:
+    """A torch stream of `stream`: one already, or a hipStream_t as an integer
+    (or as the `cuda_stream` of another library's object)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    p = int(getattr(stream, "cuda_stream", stream))
+    return torch.cuda.ExternalStream(p, device) if p else torch.cuda.default_stream(device)
+
+
+def _call(function, like, stream, *args):
+    """function(*args, stream) of the native binding, on `stream` or by default
+    on the current stream of like's device.  What the function allocates
+    (outputs, a workspace) comes from the pool of the stream that it runs on:
+    a block of the current stream's pool may still be in use by work queued
+    there, which `stream` does not wait for.  Outputs are recorded on the current
+    stream, whose work may read them after it has waited for `stream`."""
+    if not getattr(like, "is_cuda", False):
+        return function(*args, 0)                  # refuses it
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.device.index) if t.is_cuda else 0
-    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+        return function(*args, torch._C._cuda_getCurrentRawStream(like.device.index))
+    here, there = torch.cuda.current_stream(like.device), _as_stream(stream, like.device)
+    with torch.cuda.stream(there):
+        out = function(*args, there.cuda_stream)
+    if here.cuda_stream != there.cuda_stream:
+        for t in out if isinstance(out, tuple) else (out,):
+            t.record_stream(here)
+    return out
 
 
 def code_shape(R: int, C: int):
@@ -400,7 +428,7 @@ def fp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.
     fp32 [rows].  `out`: optional preallocated (codes, scales, h, rstd); h may
     be x or residual.  `y`: optional bf16 [rows, cols] that receives the norm
     before its quantization, rounded to bf16."""
-    return _native().rmsnorm_quantize(x, weight, residual, eps, fmt, out, y, _stream_of(stream, x))
+    return _call(_native().rmsnorm_quantize, x, stream, x, weight, residual, eps, fmt, out, y)
 
 
 def fp4_rmsnorm_workspace_bytes(rows: int, cols: int) -> int:
@@ -413,11 +441,7 @@ def fp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor
     """(dx bf16 [rows, cols], dw fp32 [cols]) of the norm from dy and the h and
     rstd of the forward pass; `dh`: the gradient that reaches h past the norm
     (see include/fp4.h).  `out`: optional preallocated (dx, dw); dx may be dh."""
-    if workspace is None and stream is not None:
-        # a workspace of this call's own must outlive it on `stream`
-        workspace = torch.empty(fp4_rmsnorm_workspace_bytes(*dy.shape), dtype=torch.uint8, device=dy.device)
-        workspace.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream))
-    return _native().rmsnorm_backward(dy, h, weight, rstd, dh, out, workspace, _stream_of(stream, dy))
+    return _call(_native().rmsnorm_backward, dy, stream, dy, h, weight, rstd, dh, out, workspace)
 
 
 def fp4_gemm_decode(aq: torch.Tensor, as_: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
@@ -425,7 +449,7 @@ def fp4_gemm_decode(aq: torch.Tensor, as_: torch.Tensor, wq: torch.Tensor, ws: t
     """c[M, N] = A W^T for few rows: A MXFP8 (codes [M, K], scales [M, K/32])
     or MXFP4 (codes and scales of mx_shapes(M, K)), W [N, K] MXFP4 (see
     include/fp4.h)."""
-    return _native().gemm_decode(aq, as_, wq, ws, out, out_dtype, _stream_of(stream, aq))
+    return _call(_native().gemm_decode, aq, stream, aq, as_, wq, ws, out, out_dtype)
 
 
 def grouped_shapes(rows: int, cols: int, experts: int, axis: int):
@@ -445,8 +469,8 @@ def fp4_quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, axis: int = AXI
     grouped_shapes (see include/fp4.h)."""
     if axis not in (AXIS_COLS, AXIS_ROWS):
         raise ValueError("axis must be AXIS_COLS or AXIS_ROWS")
-    return _native().quantize_grouped(x, offsets, 1 + axis, had_n, had, sign_seed, rnd, sr_seed, sr_seed, out,
-                                      _stream_of(stream, x))
+    return _call(_native().quantize_grouped, x, stream, x, offsets, 1 + axis, had_n, had, sign_seed, rnd, sr_seed,
+                 sr_seed, out)
 
 
 def fp4_quantize_grouped_dual(x: torch.Tensor, offsets: torch.Tensor, had_n: int = 32, had: int = HAD_NONE,
@@ -454,8 +478,8 @@ def fp4_quantize_grouped_dual(x: torch.Tensor, offsets: torch.Tensor, had_n: int
                               out=None, stream=None):
     """Both quantizations of x from one read: (codes, scales) along rows,
     rotated, and (codes, scales) along cols, not rotated."""
-    return _native().quantize_grouped(x, offsets, 3, had_n, had, sign_seed, rnd, sr_seed_rows, sr_seed_cols, out,
-                                      _stream_of(stream, x))
+    return _call(_native().quantize_grouped, x, stream, x, offsets, 3, had_n, had, sign_seed, rnd, sr_seed_rows,
+                 sr_seed_cols, out)
 
 
 def fp4_gemm_grouped(aq: torch.Tensor, as_: torch.Tensor, offsets: torch.Tensor, wq: torch.Tensor,
@@ -466,7 +490,7 @@ def fp4_gemm_grouped(aq: torch.Tensor, as_: torch.Tensor, offsets: torch.Tensor,
     [experts, ceil(N/32), K/32, 512] and ws [experts, ceil(K/256), N, 8]: the
     experts' weights, each quantized along its contraction.  Rows of no expert
     are left as they were (in a new tensor: not set)."""
-    return _native().gemm_grouped(aq, as_, offsets, wq, ws, rows, out, out_dtype, _stream_of(stream, aq))
+    return _call(_native().gemm_grouped, aq, stream, aq, as_, offsets, wq, ws, rows, out, out_dtype)
 
 
 def fp4_gemm_grouped_wgrad(dytq: torch.Tensor, dyts: torch.Tensor, xtq: torch.Tensor, xts: torch.Tensor,
@@ -475,8 +499,7 @@ def fp4_gemm_grouped_wgrad(dytq: torch.Tensor, dyts: torch.Tensor, xtq: torch.Te
     """dw[experts, N, K] = each expert's dY^T X from dY [rows, N] and X
     [rows, K] quantized along rows by fp4_quantize_grouped with these offsets
     (see include/fp4.h)."""
-    return _native().gemm_grouped_wgrad(dytq, dyts, xtq, xts, offsets, rows, out, out_dtype,
-                                        _stream_of(stream, dytq))
+    return _call(_native().gemm_grouped_wgrad, dytq, stream, dytq, dyts, xtq, xts, offsets, rows, out, out_dtype)
 
 
 from . import linear  # noqa: E402  (the autograd layer built on the calls above)

@@ -31,3 +31,66 @@ def test_decode_refuses_activations_of_one_dimension():
     w = u8(*F.code_shape(64, 96)), u8(*F.scale_shape(64, 96))
     with pytest.raises(ValueError, match="a codes must have two .* or three"):
         F.fp4_gemm_decode(u8(96), u8(3), *w)
+
+
+class FakeStream:
+    def __init__(self, pointer):
+        self.cuda_stream = pointer
+
+
+class FakeTensor:
+    """A tensor of the GPU as far as the host's calls look at it."""
+    is_cuda = True
+    shape = (64, 64)
+    device = torch.device("cuda", 0)
+
+    def __init__(self):
+        self.recorded = []
+
+    def record_stream(self, stream):
+        self.recorded.append(stream.cuda_stream)
+
+
+CALLS = {
+    "rmsnorm_quantize": lambda t, s: F.fp4_rmsnorm_quantize(t, t, stream=s),
+    "rmsnorm_backward": lambda t, s: F.fp4_rmsnorm_backward(t, t, t, t, stream=s),
+    "gemm_decode": lambda t, s: F.fp4_gemm_decode(t, t, t, t, stream=s),
+    "quantize_grouped": lambda t, s: F.fp4_quantize_grouped(t, t, stream=s),
+    "quantize_grouped dual": lambda t, s: F.fp4_quantize_grouped_dual(t, t, stream=s),
+    "gemm_grouped": lambda t, s: F.fp4_gemm_grouped(t, t, t, t, t, 64, stream=s),
+    "gemm_grouped_wgrad": lambda t, s: F.fp4_gemm_grouped_wgrad(t, t, t, t, t, 64, stream=s),
+}
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+@pytest.mark.parametrize("kind", ["object", "integer"])
+def test_a_call_on_a_given_stream_allocates_there(monkeypatch, name, kind):
+    """The binding runs with the given stream as the current one, so that outputs
+    and workspace come from that stream's pool, and gets no workspace of the
+    current stream's; the outputs are recorded on the caller's stream."""
+    import contextlib
+
+    current, seen, made = [FakeStream(0x10)], [], []
+
+    @contextlib.contextmanager
+    def use(stream):
+        current.append(stream)
+        yield
+        current.pop()
+
+    class Binding:
+        def __getattr__(self, function):
+            def call(*args):
+                seen.append((function, current[-1].cuda_stream, args))
+                made.append(FakeTensor())
+                return (made[-1],) if function != "gemm_decode" else made[-1]
+            return call
+
+    monkeypatch.setattr(F, "_native", lambda: Binding())
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current[-1])
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda p, device=None: FakeStream(p))
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: pytest.fail("allocated on the current stream"))
+    CALLS[name](FakeTensor(), FakeStream(0x20) if kind == "object" else 0x20)
+    assert [(f, s) for f, s, _ in seen] == [(name.split()[0], 0x20)]
+    assert seen[0][2][-1] == 0x20 and made[0].recorded == [0x10]
