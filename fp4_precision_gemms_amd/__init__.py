@@ -167,6 +167,19 @@ def _call(function, like, stream, *args):
     return out
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An output or workspace of a call on `stream` that the library makes itself:
+    from the stream's pool, recorded on the current stream (as _call does)."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    here, there = torch.cuda.current_stream(device), _as_stream(stream, device)
+    with torch.cuda.stream(there):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if here.cuda_stream != there.cuda_stream:
+        t.record_stream(here)
+    return t
+
+
 def code_shape(R: int, C: int):
     """Shape of the MXFP4 codes of R rows of C contraction elements in the
     library's 32-row tiled layout: for each group of 32 rows and each
@@ -210,9 +223,9 @@ def fp4_hadamard_quantize(x: torch.Tensor, axis: int = AXIS_COLS, had_n: int = 3
     rows, cols = x.shape
     cshape, sshape = mx_shapes(rows, cols, axis)
     if codes is None:
-        codes = torch.empty(cshape, dtype=torch.uint8, device=x.device)
+        codes = _empty(cshape, torch.uint8, x.device, stream)
     if scales is None:
-        scales = torch.empty(sshape, dtype=torch.uint8, device=x.device)
+        scales = _empty(sshape, torch.uint8, x.device, stream)
     _need(codes, torch.uint8, "codes")
     _need(scales, torch.uint8, "scales")
     if tuple(codes.shape) != cshape or tuple(scales.shape) != sshape:
@@ -237,7 +250,7 @@ def fp4_hadamard_quantize_dual(x: torch.Tensor, had_n_rows: int = 32, had_rows: 
     (cr, sr), (cc, sc) = mx_shapes(rows, cols, AXIS_ROWS), mx_shapes(rows, cols, AXIS_COLS)
     dev = x.device
     if out is None:
-        out = [torch.empty(sh, dtype=torch.uint8, device=dev) for sh in (cr, sr, cc, sc)]
+        out = [_empty(sh, torch.uint8, dev, stream) for sh in (cr, sr, cc, sc)]
     for t, sh in zip(out, (cr, sr, cc, sc)):
         _need(t, torch.uint8, "output")
         if tuple(t.shape) != tuple(sh):
@@ -271,7 +284,7 @@ def fp4_wgrad_quantize(dy: torch.Tensor, x: torch.Tensor, had_n: int = 32, had: 
     _need(dy, torch.bfloat16, "dy")
     _need(x, torch.bfloat16, "x")
     if out is None:
-        out = tuple(torch.empty(sh, dtype=torch.uint8, device=dy.device) for sh in (a, b, c, d))
+        out = tuple(_empty(sh, torch.uint8, dy.device, stream) for sh in (a, b, c, d))
     for t in out:
         _need(t, torch.uint8, "output")
     m = 2 ** 64 - 1
@@ -285,7 +298,7 @@ def _gemm(fn, aq, as_, bq, bs, T, N, K, out_shape, out, stream):
     for t, n in ((aq, "a codes"), (as_, "a scales"), (bq, "b codes"), (bs, "b scales")):
         _need(t, torch.uint8, n)
     if out is None:
-        out = torch.empty(out_shape, dtype=torch.float32, device=aq.device)
+        out = _empty(out_shape, torch.float32, aq.device, stream)
     _need(out, torch.float32, "out")
     if tuple(out.shape) != tuple(out_shape):
         raise ValueError("out must have shape %s" % (out_shape,))
@@ -332,7 +345,7 @@ def fp4_gemm_mx(aq, as_, bq, bs, out=None, out_dtype: int = OUT_F32, accumulate:
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs an existing out")
-        out = torch.empty((M, N), dtype=dt, device=aq.device)
+        out = _empty((M, N), dt, aq.device, stream)
     _need(out, dt, "out")
     if tuple(out.shape) != (M, N):
         raise ValueError("out must have shape %s" % ((M, N),))
@@ -365,9 +378,9 @@ def nvfp4_quantize(x: torch.Tensor, had: int = HAD_SIGNED, sign_seed: int = 0, m
         raise ValueError("amax_in must hold one float")
     _need(x, torch.bfloat16, "x")
     dev = x.device
-    codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev) if codes is None else codes
-    scales = torch.empty((rows, cols // 16), dtype=torch.uint8, device=dev) if scales is None else scales
-    tensor_scale = torch.empty(1, dtype=torch.float32, device=dev) if tensor_scale is None else tensor_scale
+    codes = _empty((rows, cols // 2), torch.uint8, dev, stream) if codes is None else codes
+    scales = _empty((rows, cols // 16), torch.uint8, dev, stream) if scales is None else scales
+    tensor_scale = _empty(1, torch.float32, dev, stream) if tensor_scale is None else tensor_scale
     for t, dt, n in ((codes, torch.uint8, "codes"), (scales, torch.uint8, "scales"),
                      (tensor_scale, torch.float32, "tensor_scale")):
         _need(t, dt, n)
@@ -376,7 +389,7 @@ def nvfp4_quantize(x: torch.Tensor, had: int = HAD_SIGNED, sign_seed: int = 0, m
     if workspace is not None:
         _need(workspace, torch.uint8, "workspace")
     if amax_in is None and workspace is None:
-        workspace = torch.empty(nvfp4_workspace_bytes(rows, cols), dtype=torch.uint8, device=dev)
+        workspace = _empty(nvfp4_workspace_bytes(rows, cols), torch.uint8, dev, stream)
     _check(lib().nvfp4_quantize(x.data_ptr(), rows, cols, had, sign_seed & (2 ** 64 - 1), mode,
                                 sr_seed & (2 ** 64 - 1), _ptr(amax_in), codes.data_ptr(),
                                 scales.data_ptr(), tensor_scale.data_ptr(), _ptr(workspace),

@@ -94,3 +94,49 @@ def test_a_call_on_a_given_stream_allocates_there(monkeypatch, name, kind):
     CALLS[name](FakeTensor(), FakeStream(0x20) if kind == "object" else 0x20)
     assert [(f, s) for f, s, _ in seen] == [(name.split()[0], 0x20)]
     assert seen[0][2][-1] == 0x20 and made[0].recorded == [0x10]
+
+
+def test_outputs_of_the_older_calls_come_from_the_given_stream(monkeypatch):
+    """The quantizers, products and nvfp4_quantize's workspace likewise."""
+    import contextlib
+
+    current, made = [FakeStream(0x10)], []
+
+    class Made(torch.Tensor):
+        def record_stream(self, stream):
+            made.append((current[-1].cuda_stream, stream.cuda_stream))
+
+    @contextlib.contextmanager
+    def use(stream):
+        current.append(stream)
+        yield
+        current.pop()
+
+    def empty(shape, dtype=None, device=None):
+        assert current[-1].cuda_stream == 0x20, "allocated on the current stream"
+        return torch.zeros(shape, dtype=dtype).as_subclass(Made)
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: 64 if name == "nvfp4_workspace_bytes" else 0
+
+    class Bf16(torch.Tensor):
+        device = torch.device("cuda", 0)
+
+    monkeypatch.setattr(F, "lib", lambda: Library())
+    monkeypatch.setattr(F, "_need", lambda *a: None)
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current[-1])
+    monkeypatch.setattr(torch, "empty", empty)
+    x = torch.zeros(64, 64, dtype=torch.bfloat16).as_subclass(Bf16)
+    q = [torch.zeros(s, dtype=torch.uint8).as_subclass(Bf16) for s in (F.code_shape(64, 64), F.scale_shape(64, 64))]
+    s = FakeStream(0x20)
+    monkeypatch.setattr(F, "_as_stream", lambda stream, device: stream)
+    for call, count in ((lambda: F.fp4_hadamard_quantize(x, stream=s), 2),
+                        (lambda: F.fp4_hadamard_quantize_dual(x, stream=s), 4),
+                        (lambda: F.fp4_wgrad_quantize(x, x, stream=s), 4),
+                        (lambda: F.fp4_gemm_fprop(*q, *q, stream=s), 1), (lambda: F.fp4_gemm_mx(*q, *q, stream=s), 1),
+                        (lambda: F.nvfp4_quantize(x, stream=s), 4)):
+        made.clear()
+        call()
+        assert made == [(0x10, 0x10)] * count
