@@ -70,6 +70,8 @@ fp4_status check_grouped_product(const uint8_t* a, const uint8_t* as, fp4_format
     if (!product_ok(rows + 32 * experts, K) || !product_ok(N * experts, K) || !product_ok(rows, N) ||
         (rows / 128 + experts) * ((N + 255) / 256) >= kMaxTiles)
         return FP4_ERR_SHAPE;
+    // a thread of the few-row kernel for each 1/4 of a column
+    if (N >= INT64_C(1) << 30) return FP4_ERR_SHAPE;
     // tiles are counted in 32 bits, also where offsets out of order overlap
     if (experts * (rows / 128 + 1) * ((N + 255) / 256) > INT32_MAX) return FP4_ERR_SHAPE;
     if (!a || !as || !wq || !ws || !c) return FP4_ERR_NULL;

@@ -24,6 +24,15 @@ inline hipError_t launch(void (*k)(P...), dim3 grid, dim3 block, hipStream_t st,
         v);
 }
 
+// A grid of at least n workgroups of `threads` in two dimensions: HIP refuses 2^32
+// threads or more in one (and the refusal stays behind as the next runtime
+// call's error).  The kernel takes workgroup blockIdx.y gridDim.x + blockIdx.x
+// and leaves out those past its work.
+inline dim3 grid_of(int64_t n, unsigned threads) {
+    const int64_t most = UINT32_MAX / threads, y = (n + most - 1) / most;
+    return dim3((unsigned)((n + y - 1) / y), (unsigned)y);
+}
+
 // MXFP4 quantization of bf16 x[rows, cols] along axis 0 (cols) or 1 (rows).
 hipError_t launch_quant_mx(const void* x, int64_t rows, int64_t cols, int axis, int had_n, int had,
                            uint64_t sign_seed, int rnd, uint64_t sr_seed, uint8_t* codes,

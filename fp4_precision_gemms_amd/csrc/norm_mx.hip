@@ -91,8 +91,9 @@ __global__ __launch_bounds__(TPR * RPB) void rmsnorm_quant(
     static_assert(TPR == 64 || RPB == 1, "rows that share a workgroup are a wave each");
     constexpr int kWaves = TPR / 64;
     const int t = threadIdx.x % TPR, nch = cols / 8, q = t & 3;
-    const int64_t row = (int64_t)row_block<32 / RPB>(blockIdx.x, gridDim.x) * RPB + threadIdx.x / TPR;
-    if (RPB > 1 && row >= rows) return;               // a wave of its own: no barrier below
+    const int64_t row =
+        (int64_t)row_block<32 / RPB>(blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y) * RPB + threadIdx.x / TPR;
+    if (row >= rows) return;                           // a wave of its own, or the whole workgroup
     const int64_t base = row * nch;
     uint4 v[V], wv[V];
 #pragma unroll
@@ -191,7 +192,7 @@ __global__ __launch_bounds__(TPR * RPB) void rmsnorm_quant(
 template <int TPR, int RPB, int V>
 hipError_t launch_norm(const void* x, const void* res, const void* w, double eps, int64_t rows, int64_t cols,
                        int e4m3, void* h, float* rstd, void* y, uint8_t* codes, uint8_t* scales, hipStream_t st) {
-    const dim3 grid((unsigned)((rows + RPB - 1) / RPB)), block(TPR * RPB);
+    const dim3 grid = grid_of((rows + RPB - 1) / RPB, TPR * RPB), block(TPR * RPB);
 #define FP4_NORM(RES, E)                                                                                \
     return launch(&rmsnorm_quant<TPR, RPB, V, RES, E>, grid, block, st, (const uint4*)x, (const uint4*)res, \
                   (const uint4*)w, eps, rows, (int)cols, (uint4*)h, rstd, (uint4*)y, codes, scales)

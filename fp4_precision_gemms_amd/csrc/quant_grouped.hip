@@ -44,8 +44,10 @@ __global__ __launch_bounds__(kCols) void quant_grouped(
     // units of the cols output, blocks of the rows output
     const int64_t units = rows / 32 + experts, blocks = 8 * (rows / 256 + experts), nbc = cols / 32;
     const int gx = (cols + kCols - 1) / kCols;
-    const int c0 = (int)(blockIdx.x % gx) * kCols;
-    const int64_t q0 = (int64_t)(blockIdx.x / gx) * (kUnits * kTurns);
+    // (workgroups past the last unit find nothing live)
+    const uint32_t wg = blockIdx.y * gridDim.x + blockIdx.x;
+    const int c0 = (int)(wg % gx) * kCols;
+    const int64_t q0 = (int64_t)(wg / gx) * (kUnits * kTurns);
     // units of one stage belong to one expert
     const int stage_expert = ROWS ? expert_of_unit<256>(offsets, experts, rows, q0 / 8) : -1;
     for (int turn = 0; turn < kTurns; ++turn) {
@@ -167,13 +169,13 @@ hipError_t launch_one(const void* x, const int* offsets, int64_t experts, int64_
     const int64_t gx = (cols + kCols - 1) / kCols;
     if constexpr (ROWS)
         if (rows < 96 * experts && gx * units / 8 >= kFewWorkgroups / 2)
-            return launch(&quant_grouped<HADN, SR, ROWS, COLS, 2, 4>, dim3((unsigned)(gx * (units / 8))), dim3(kCols),
+            return launch(&quant_grouped<HADN, SR, ROWS, COLS, 2, 4>, grid_of(gx * (units / 8), kCols), dim3(kCols),
                           st, (const uint16_t*)x, offsets, (int)experts, rows, (int)cols, rot, sr_rows, sr_cols, cr, sr,
                           cc, sc);
     if (gx * units / 2 < kFewWorkgroups)
-        return launch(&quant_grouped<HADN, SR, ROWS, COLS, 1, 1>, dim3((unsigned)(gx * units)), dim3(kCols), st,
+        return launch(&quant_grouped<HADN, SR, ROWS, COLS, 1, 1>, grid_of(gx * units, kCols), dim3(kCols), st,
                       (const uint16_t*)x, offsets, (int)experts, rows, (int)cols, rot, sr_rows, sr_cols, cr, sr, cc, sc);
-    return launch(&quant_grouped<HADN, SR, ROWS, COLS, 2, 1>, dim3((unsigned)(gx * ((units + 1) / 2))), dim3(kCols), st,
+    return launch(&quant_grouped<HADN, SR, ROWS, COLS, 2, 1>, grid_of(gx * ((units + 1) / 2), kCols), dim3(kCols), st,
                   (const uint16_t*)x, offsets, (int)experts, rows, (int)cols, rot, sr_rows, sr_cols, cr, sr, cc, sc);
 }
 

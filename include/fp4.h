@@ -403,7 +403,7 @@ size_t fp4_rmsnorm_workspace_bytes(int64_t rows, int64_t cols);
  * the weight [N, K] quantized along cols.  It computes what fp4_gemm_mx does
  * (for MXFP4 activations, up to the order of the fp32 sums) for any M, but is
  * made for M up to a few dozen, where the weights' bytes are the time.
- * Requirements: K % 32 == 0 and K < 2^24; M, N < 2^31; fewer than 2^24 tiles
+ * Requirements: K % 32 == 0 and K < 2^24; M < 2^31, N < 2^30; fewer than 2^24 tiles
  * of 128 x 256 outputs; pointers 16-byte aligned.  A scale byte of 0xFF makes
  * its block NaN; every other pair of scales gives the products within the fp32
  * sums' rounding.
@@ -447,7 +447,8 @@ fp4_status fp4_gemm_decode(const uint8_t* a, const uint8_t* as, fp4_format fmt, 
  * output has index row * cols + col (row of x), element i of row col of the
  * rows output index col * 256 G + i.
  * Requirements: cols % 32 == 0, cols < 2^24; 0 < rows < 2^31; 1 <= experts <=
- * 1024; pointers 16-byte aligned (offsets 4).
+ * 1024; ceil(cols / 256) (rows / 32 + 8 experts) < 2^31; pointers 16-byte aligned
+ * (offsets 4).
  */
 fp4_status fp4_quantize_grouped(const void* x_bf16, const int32_t* offsets, int64_t experts,
                                 int64_t rows, int64_t cols, int had_n, fp4_hadamard had,

@@ -140,3 +140,10 @@ def test_outputs_of_the_older_calls_come_from_the_given_stream(monkeypatch):
         made.clear()
         call()
         assert made == [(0x10, 0x10)] * count
+
+
+def test_products_of_more_columns_than_a_launch_holds_are_refused_for_their_shape():
+    a, shape = 0x10000, 2
+    L = F.lib()
+    assert L.fp4_gemm_decode(a, a, 1, a, a, 1, 2 ** 30, 32, a, 1, None) == shape
+    assert L.fp4_gemm_grouped(a, a, 1, a, 1, 1, a, a, 2 ** 30, 32, a, 1, None) == shape
