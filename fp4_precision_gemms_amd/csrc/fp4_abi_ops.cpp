@@ -116,14 +116,19 @@ fp4_status fp4_gemm_grouped(const uint8_t* a, const uint8_t* as, fp4_format fmt,
     if (!offsets) return FP4_ERR_NULL;
     if (!aligned4(offsets)) return FP4_ERR_ALIGN;
     // Up to 32 rows an expert on average the few-row kernel, which reads the
-    // weights once per 64 rows at most (64 experts of 1408 x 1408: 20.4 against
-    // 29.2 us at 32 rows, 23.0 and 19.6 at 48; 40 of 736 x 1120: 7.6 and 8.6 at
-    // 32, 9.6 and 8.8 at 48).  Few experts with a small output also beyond: the
-    // large tiles, too few of them for the CUs, take the time of one (one expert
-    // of 4096 x 4096: 5.3 against 14.3 us at 64 rows, 12.5 and 14.7 at 256, 22.8
-    // and 15.1 at 512; 4 of them 12.8 and 15.1 at 64, 16.2 and 15.2 at 96; but 32
-    // of 768 x 2048: 11.8 and 10.3 at 40).
-    const bool few = rows <= 32 * experts || (experts <= 16 && rows * N <= (INT64_C(1) << 20));
+    // weights once per 64 rows at most (64 experts of 1408 x 1408: 15.5 against
+    // 19.6 us at 32 rows, 19.7 and 19.5 at 40; 128 of 2048 x 2048 54.5 and 53.3,
+    // 81 and 55; 40 of 736 x 1120 5.7 and 8.4, 7.1 and 8.4).  Few experts with a
+    // small output also beyond: the large tiles, too few of them for the CUs, take
+    // the time of one (one expert, K = 4096: 14.5 us; the few-row kernel 12.6 for
+    // 256 rows of 4096 columns, 8.2 for 512 of 1024, 9.7 for 2048 of 256, 7.4 for
+    // 4096 of 64).  Its bound there is the rows, read again for every 16 or 32
+    // columns: with few columns and a long contraction it falls behind at half
+    // that output already (64 columns: K = 4096, 16384 rows 24.0 and 16.0, K =
+    // 14336 70 and 38.6, 4096 rows 20.9 and 35.8; 16 experts of 256 columns, K =
+    // 14336, 256 rows 53.4 and 36.3, 128 rows 29.2 and 36.0).
+    const int64_t outputs = INT64_C(1) << (N < 512 && K > 1024 ? 19 : 20);
+    const bool few = rows <= 32 * experts || (experts <= 16 && rows * N <= outputs);
     if (fmt == FP4_FMT_MXFP4 && !few && fp4dev::row_groups_fit(experts, rows, N, K))
         return from_hip(fp4dev::launch_gemm_row_groups(a, as, offsets, experts, rows, wq, ws, N, K, c,
                                                        out == FP4_OUT_BF16, (hipStream_t)stream));

@@ -33,8 +33,8 @@
 //     (A test of the scales in the loop, with a branch there, took 193 registers
 //     for 128 and up to 9 % of the time; this 1 to 3 %: 96 rows over 64 experts
 //     of 1408 x 2048 17.9 us, 19.3 with the test, 17.8 without either.)
-// More than 16 MT rows (of an expert) are taken one tile after another; the
-// weights then come from the caches.
+// More than 16 MT rows (of an expert) are taken one tile after another by the
+// workgroups of blockIdx.z in turn; the weights then come from the caches.
 #include "fp4_device.hpp"
 #include "fp4_launch.hpp"
 #include "grouped.hpp"
@@ -152,7 +152,8 @@ __global__ __launch_bounds__(64 * W) void gemm_few(
         offb[j] = (uint32_t)((r >> 5) * gstride) + (r & 31) * 16;
     }
 
-    for (int64_t m0 = lo; m0 < hi; m0 += 16 * MT) {
+    const int64_t mstart = lo + (int64_t)blockIdx.z * (16 * MT);
+    for (int64_t m0 = mstart; m0 < hi; m0 += (int64_t)gridDim.z * (16 * MT)) {
         const int mleft = (int)((hi - m0) < 16 * MT ? (hi - m0) : 16 * MT);
         const int64_t p0 = first + (m0 - lo);          // the tile's first row in the A operand
         const __amdgpu_buffer_rsrc_t ra =
@@ -256,7 +257,7 @@ __global__ __launch_bounds__(64 * W) void gemm_few(
             multiply(t, g);
         }
         // join the waves' sums: tile (i, j) is added up by wave (i NT + j) mod W
-        if (m0 != lo) __syncthreads();                 // the previous tile's sums have been read
+        if (m0 != mstart) __syncthreads();             // the previous tile's sums have been read
         bool finite = true;
         if constexpr (A8) {
 #pragma unroll
@@ -326,7 +327,14 @@ __global__ __launch_bounds__(64 * W) void gemm_few(
 template <bool A8, int MT, int NT, int W>
 hipError_t launch_few(const uint8_t* a, const uint8_t* as, const int* offsets, const uint8_t* w, const uint8_t* ws,
                       int64_t rows, int64_t experts, int64_t N, int64_t K, void* c, int out_bf16, hipStream_t st) {
-    const dim3 grid((unsigned)((N + 16 * NT - 1) / (16 * NT)), (unsigned)experts);
+    // Row tiles go to workgroups of their own up to kFewWorkgroups in all: one
+    // after another, 1 expert of 64 columns, K = 1024 and 16384 rows took 323 us,
+    // so 7.4; 1024 columns, K = 4096, 1024 rows 40 and 13.3.  (Up to 256 that is
+    // 12.8, but 64 columns 9.1; up to 2048 14.2 and 6.7.)
+    constexpr int64_t kFewWorkgroups = 512;
+    const int64_t x = (N + 16 * NT - 1) / (16 * NT), tiles = ((rows + experts - 1) / experts + 16 * MT - 1) / (16 * MT);
+    const int64_t fill = kFewWorkgroups / (x * experts), z = fill < 1 ? 1 : fill < tiles ? fill : tiles;
+    const dim3 grid((unsigned)x, (unsigned)experts, (unsigned)z);
     return out_bf16 ? launch(&gemm_few<A8, MT, NT, W, true>, grid, dim3(64 * W), st, a, as, offsets, w, ws, rows,
                              (int)experts, N, K, c)
                     : launch(&gemm_few<A8, MT, NT, W, false>, grid, dim3(64 * W), st, a, as, offsets, w, ws, rows,
