@@ -424,9 +424,19 @@ __global__ __launch_bounds__(kThreads) void gemm_mx_grouped(
     constexpr int kOut = OBF16 ? 2 : 4;
 
     // Staggered start, as in gemm_mx.hip: the tile boundaries of the workgroups
-    // do not all fall at the same moment.
+    // do not all fall at the same moment (8 experts of 4096 x 4096, 1024 uneven
+    // rows 81 us, 92 without; 16 of them, weight gradient, 1024 rows 201 and 227).
+    // The last workgroup starts 7 us late, the time of a short tile, so that row
+    // groups of two rounds or few stages shorten it by their stages (8 experts of
+    // 4096 x 256, 512 rows 18.6 with the whole, 12.3 us with 1/16; 32 of 2048 x
+    // 512, 250 rows 18.7 and 14.4; but 8 of 4096 x 1024, 1000 rows, four rounds,
+    // 35.2 and 42).
     if (ntiles > (int)gridDim.x) {
-        for (int q = 0; q < (int)blockIdx.x; ++q) __builtin_amdgcn_s_sleep(1);
+        int delay = blockIdx.x;
+        if constexpr (GROUP == kRowGroups)
+            if (nk < 16 && (ntiles <= 2 * (int)gridDim.x || (int64_t)ntiles * nk * FM <= 32 * (int)gridDim.x))
+                delay = delay * nk / 16;
+        for (int q = 0; q < delay; ++q) __builtin_amdgcn_s_sleep(1);
     }
     // The first tile's prologue goes out here and every later one during the
     // previous tile's epilogue, which leaves the loop a single prologue site.
