@@ -136,9 +136,9 @@ size_t nvfp4_workspace_bytes(int64_t rows, int64_t cols) {
 }
 
 namespace {
-fp4_status check_nvfp4(const void* x_bf16, int64_t rows, int64_t cols, fp4_hadamard had,
-                       nvfp4_mode mode, const float* amax_in, const uint8_t* codes,
-                       const uint8_t* scales_e4m3, const float* tensor_scale) {
+static fp4_status check_nvfp4(const void* x_bf16, int64_t rows, int64_t cols, fp4_hadamard had,
+                              nvfp4_mode mode, const float* amax_in, const uint8_t* codes,
+                              const uint8_t* scales_e4m3, const float* tensor_scale) {
     if (had != FP4_HAD_NONE && had != FP4_HAD_DET && had != FP4_HAD_SIGNED) return FP4_ERR_ENUM;
     if (mode != NVFP4_RTN && mode != NVFP4_RENORM_SR && mode != NVFP4_ELEMENT_SR) return FP4_ERR_ENUM;
     if (!x_bf16 || !codes || !scales_e4m3 || !tensor_scale) return FP4_ERR_NULL;

@@ -2,7 +2,8 @@
 // (declared in include/fp4.h): argument validation, then dispatch to the HIP
 // launchers, with no HIP call before every argument has been checked.  Shapes
 // come before pointers: an empty batch, whose pointers are NULL, is refused for
-// its shape.
+// its shape.  (Helpers inside extern "C" are static: a C function of an unnamed
+// namespace would be exported.)
 #include "fp4.h"
 
 #include <hip/hip_runtime.h>
@@ -16,7 +17,7 @@ extern "C" {
 
 namespace {
 // rows and cols of a norm: whole 32-element blocks, a row held in registers
-fp4_status check_norm_shape(int64_t rows, int64_t cols) {
+static fp4_status check_norm_shape(int64_t rows, int64_t cols) {
     if (rows <= 0 || cols <= 0 || cols % 32 || cols > 32768 || rows > INT32_MAX) return FP4_ERR_SHAPE;
     return FP4_OK;
 }
@@ -59,9 +60,9 @@ fp4_status fp4_rmsnorm_backward(const void* dy_bf16, const void* h_bf16, const v
 namespace {
 constexpr int64_t kMaxExperts = 1024;
 
-fp4_status check_grouped_product(const uint8_t* a, const uint8_t* as, fp4_format fmt, const uint8_t* wq,
-                                 const uint8_t* ws, int64_t experts, int64_t rows, int64_t N, int64_t K,
-                                 const void* c, fp4_out_dtype out) {
+static fp4_status check_grouped_product(const uint8_t* a, const uint8_t* as, fp4_format fmt, const uint8_t* wq,
+                                        const uint8_t* ws, int64_t experts, int64_t rows, int64_t N, int64_t K,
+                                        const void* c, fp4_out_dtype out) {
     if (fmt != FP4_FMT_MXFP4 && fmt != FP4_FMT_MXFP8) return FP4_ERR_ENUM;
     if (out != FP4_OUT_F32 && out != FP4_OUT_BF16) return FP4_ERR_ENUM;
     if (rows <= 0 || N <= 0 || K <= 0 || K % 32 || K >= kMaxContraction || rows > INT32_MAX || N > INT32_MAX ||
