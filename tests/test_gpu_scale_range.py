@@ -86,3 +86,22 @@ def test_nan_scales_beside_scales_at_the_ends(M, N, K):
     check(got[1:2, keep], ref[1:2, keep], mag[1:2, keep])
     large = np.abs(ref[2:, keep]) > 2.0 ** 130
     assert large.any() and np.isinf(g[2:, keep][large]).all()
+
+
+@pytest.mark.parametrize("fmt", [F.FMT_MXFP8, F.FMT_MXFP4])
+def test_nan_blocks_as_the_quantizers_write_them(fmt):
+    """A NaN activation or weight leaves a block of zero codes under scale byte
+    255: NaN in its row or column, nothing elsewhere."""
+    need_gpu()
+    M, N, K = 6, 96, 320
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x, w = (torch.randn(n, K, device="cuda", generator=g).bfloat16() for n in (M, N))
+    x[4, 77] = float("nan")
+    w[33, 300] = float("-inf")
+    a = F.fp4_rmsnorm_quantize(x, torch.ones(K, device="cuda").bfloat16(), fmt=fmt)[:2]
+    y = F.fp4_gemm_decode(*a, *F.fp4_hadamard_quantize(w))
+    torch.cuda.synchronize()
+    want = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    want[4] = True
+    want[:, 33] = True
+    assert torch.equal(y.isnan(), want)
