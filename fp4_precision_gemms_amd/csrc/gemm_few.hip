@@ -26,13 +26,13 @@
 //     has 4, and the block scale is a power of two that the conversion
 //     applies -- and take four V_MFMA_F32_16X16X32_BF16.  A k-step's elements
 //     are then in another order (the lane's 8 consecutive ones per
-//     instruction), the same for both operands.  A wave whose
-//     sums are not finite, since the upper end of E8M0 takes elements out of
-//     bf16's range (or an input was NaN), multiplies its k-groups again, block
-//     by block without the scales, which then scale each block's sum in fp32.
-//     (A test of the scales in the loop, with a branch there, took 193 registers
-//     for 128 and up to 9 % of the time; this 1 to 3 %: 96 rows over 64 experts
-//     of 1408 x 2048 17.9 us, 19.3 with the test, 17.8 without either.)
+//     instruction), the same for both operands.  A tile
+//     whose sums are not finite, since the upper end of E8M0 takes elements out
+//     of bf16's range (or an input was NaN), is multiplied again, block by block
+//     without the scales, which then scale each block's sum in fp32.  (A test of
+//     the scales in the loop, with a branch there, took 193 registers for 128 and
+//     up to 9 % of the time; this 1 to 2 %, the lift by 2^3: 96 rows over 64
+//     experts of 1408 x 2048 15.1 to 15.4 us.)
 // More than 16 MT rows (of an expert) are taken one tile after another by the
 // workgroups of blockIdx.z in turn; the weights then come from the caches.
 #include "fp4_device.hpp"
@@ -246,6 +246,31 @@ __global__ __launch_bounds__(64 * W) void gemm_few(
                 }
             }
         };
+        // tile q by add_unscaled, a k-group's sum after another
+        auto tile_unscaled = [&](int q) {
+            v4f total = {};
+            if constexpr (A8) {
+                const int m = 16 * (q / NT) + l16, n = 16 * (q % NT) + l16, r = (int)(n0 & 31) + n;
+                const uint32_t offw = (uint32_t)((r >> 5) * gstride) + (r & 31) * 16;
+#pragma unroll 1
+                for (int g = 0; g < groups; ++g) {
+                    const __amdgpu_buffer_rsrc_t rsb = raw_buffer(SB + ((int64_t)g * N + n0) * 8, nleft * 8);
+                    v4f sum = {};
+#pragma unroll 1
+                    for (int b = 8 * g + quad; b < 8 * g + 8; b += 4) {
+                        const bool in = b < nb;
+                        const uint32_t offm = in ? (uint32_t)m * (uint32_t)K + (uint32_t)b * 32 : kOob;
+                        const v4i codes[2] = {load16(ra, offm), load16(ra, offm + 16)};
+                        const int ea = __builtin_amdgcn_raw_buffer_load_b8(
+                            rsa, in ? (uint32_t)m * (uint32_t)nb + (uint32_t)b : kOob, 0, 0);
+                        const int ew = in ? __builtin_amdgcn_raw_buffer_load_b8(rsb, n * 8 + (b & 7), 0, 0) : 0;
+                        add_unscaled(load16(rb, in ? offw + (uint32_t)b * 512 : kOob), ew, codes, ea, sum);
+                    }
+                    total += sum;
+                }
+            }
+            return total;
+        };
         int g = wave;
         if (g < groups) {
             Group<A8, MT, NT> t = load(g);
@@ -258,49 +283,22 @@ __global__ __launch_bounds__(64 * W) void gemm_few(
         }
         // join the waves' sums: tile (i, j) is added up by wave (i NT + j) mod W
         if (m0 != mstart) __syncthreads();             // the previous tile's sums have been read
-        bool finite = true;
-        if constexpr (A8) {
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        finite &= __builtin_fabsf(acc[i][j][r]) < __builtin_inff();
-                        acc[i][j][r] *= 1.0f / (1 << kUp);
-                    }
-        }
-        if (A8 && __any(!finite)) {
-#pragma unroll 1
-            for (int q = 0; q < MT * NT; ++q) {
-                const int m = 16 * (q / NT) + l16, n = 16 * (q % NT) + l16, r = (int)(n0 & 31) + n;
-                const uint32_t offw = (uint32_t)((r >> 5) * gstride) + (r & 31) * 16;
-                v4f sum = {};
-#pragma unroll 1
-                for (int b0 = 8 * wave; b0 < nb; b0 += b0 & 4 ? 8 * W - 4 : 4) {
-                    const __amdgpu_buffer_rsrc_t rsb = raw_buffer(SB + ((int64_t)(b0 >> 3) * N + n0) * 8, nleft * 8);
-                    const int b = b0 + quad;
-                    const bool in = b < nb;
-                    const uint32_t offm = (uint32_t)m * (uint32_t)K + (uint32_t)b * 32;
-                    const v4i codes[2] = {load16(ra, in ? offm : kOob), load16(ra, in ? offm + 16 : kOob)};
-                    const int ea = __builtin_amdgcn_raw_buffer_load_b8(
-                        rsa, in ? (uint32_t)m * (uint32_t)nb + (uint32_t)b : kOob, 0, 0);
-                    const int ew = in ? __builtin_amdgcn_raw_buffer_load_b8(rsb, n * 8 + (b & 7), 0, 0) : 0;
-                    add_unscaled(load16(rb, in ? offw + (uint32_t)b * 512 : kOob), ew, codes, ea, sum);
-                }
-                part[wave][q][lane] = sum;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j) part[wave][i * NT + j][lane] = acc[i][j];
-        }
+            for (int j = 0; j < NT; ++j) part[wave][i * NT + j][lane] = acc[i][j];
         __syncthreads();
         for (int q = wave; q < MT * NT; q += W) {
             v4f s = part[0][q][lane];
 #pragma unroll
             for (int w = 1; w < W; ++w) s += part[w][q][lane];
+            if constexpr (A8) {
+                bool finite = true;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) finite &= __builtin_fabsf(s[r]) < __builtin_inff();
+                s *= 1.0f / (1 << kUp);
+                if (__builtin_expect(__any(!finite), 0)) s = tile_unscaled(q);
+            }
             const int m = 16 * (q / NT) + l16, n = 16 * (q % NT) + 4 * quad;
             if (m >= mleft || n >= nleft) continue;
             const int64_t at = (m0 + m) * N + n0 + n;
