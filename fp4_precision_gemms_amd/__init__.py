@@ -435,9 +435,9 @@ def fp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.
                          stream=None):
     """h = x + residual and its root-mean-square norm times `weight`, quantized
     along cols: (codes, scales, h, rstd) of bf16 x[rows, cols] (see
-    include/fp4.h).  fmt FMT_MXFP8: codes uint8 [rows, cols] (E4M3), scales
-    uint8 [rows, cols/32]; FMT_MXFP4: codes and scales in the shapes of
-    mx_shapes(rows, cols, AXIS_COLS).  h is x itself without a residual, rstd
+    include/fp4.h).  fmt FMT_MXFP8: codes (E4M3) and scales in the shapes of
+    mx8_shapes(rows, cols); FMT_MXFP4: of mx_shapes(rows, cols, AXIS_COLS), all
+    uint8.  h is x itself without a residual, rstd
     fp32 [rows].  `out`: optional preallocated (codes, scales, h, rstd); h may
     be x or residual.  `y`: optional bf16 [rows, cols] that receives the norm
     before its quantization, rounded to bf16."""
@@ -459,8 +459,8 @@ def fp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor
 
 def fp4_gemm_decode(aq: torch.Tensor, as_: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
                     out: torch.Tensor | None = None, out_dtype: int = OUT_BF16, stream=None):
-    """c[M, N] = A W^T for few rows: A MXFP8 (codes [M, K], scales [M, K/32])
-    or MXFP4 (codes and scales of mx_shapes(M, K)), W [N, K] MXFP4 (see
+    """c[M, N] = A W^T for few rows: A MXFP8 (codes and scales of mx8_shapes(M,
+    K)) or MXFP4 (of mx_shapes(M, K, AXIS_COLS)), W [N, K] MXFP4 (see
     include/fp4.h)."""
     return _call(_native().gemm_decode, aq, stream, aq, as_, wq, ws, out, out_dtype)
 

@@ -365,6 +365,9 @@ hipError_t launch_rmsnorm_quant(const void* x, const void* res, const void* w, d
 // Workgroups of the backward pass: one per CU keeps the parts of dw, and the
 // kernel that adds them up, small (8192 x 8192: 256 parts 97 + 5 us, 1024 parts
 // 103 + 10); narrow rows, whose workgroups are a few waves, take more of them.
+// Beyond 16384 columns a lane holds four chunks in 128 registers and spills 64 to
+// 79 of them, which then bounds the kernel: 2048 x 32768 220 us (1.8 TB/s), with
+// dh 295; 2048 x 16384 37 and 50 (5.4 TB/s).
 int64_t rmsnorm_back_parts(int64_t rows, int64_t cols) {
     const int64_t most = cols <= 1024 ? 1024 : cols <= 2048 ? 512 : 256;
     return rows < most ? rows : most;

@@ -22,6 +22,11 @@ sequences library calls; all arithmetic runs in libfp4.so.
 MXFP4NormLinear puts the norm that feeds such a layer in front of it (residual
 added, output quantized without a pass of its own), MXFP4GroupedLinear is the
 layer of a mixture of experts: rows sorted by expert, one weight each.
+
+Captured into a HIP graph, a layer's forward and backward pass go into the same
+capture, after a warm-up on the capturing stream and with no eager graph of its
+parameters alive (torch's gradient accumulation would wait for the stream of
+that one).
 """
 from __future__ import annotations
 
@@ -147,7 +152,9 @@ class MXFP4NormLinear(torch.nn.Module):
 def quantize_experts(w: torch.Tensor):
     """Both operands of each of the experts' weights w [E, N, K] (bf16, N and K
     multiples of 32), as fp4_gemm_grouped takes them: (wtq, wts) for Dgrad,
-    (wq, ws) for the forward product."""
+    (wq, ws) for the forward product.  One launch an expert, 13 us each on the
+    host: 40 experts of 736 x 1120 526 us, 8 of 14336 x 4096 310 (bound by their
+    bytes)."""
     E, N, K = w.shape
     shapes = (code_shape(K, N), scale_shape(K, N), code_shape(N, K), scale_shape(N, K))
     out = tuple(torch.empty((E, *s), dtype=torch.uint8, device=w.device) for s in shapes)

@@ -147,3 +147,10 @@ def test_products_of_more_columns_than_a_launch_holds_are_refused_for_their_shap
     L = F.lib()
     assert L.fp4_gemm_decode(a, a, 1, a, a, 1, 2 ** 30, 32, a, 1, None) == shape
     assert L.fp4_gemm_grouped(a, a, 1, a, 1, 1, a, a, 2 ** 30, 32, a, 1, None) == shape
+
+
+def test_shapes_of_an_mxfp8_operand():
+    assert F.mx8_shapes(7, 96) == ((7, 96), (7, 3))
+    codes, scales = (u8(*s) for s in F.mx8_shapes(7, 96))
+    with pytest.raises(ValueError, match="GPU"):       # its shapes are taken
+        F.fp4_gemm_decode(codes, scales, u8(*F.code_shape(64, 96)), u8(*F.scale_shape(64, 96)))
