@@ -71,7 +71,7 @@ static fp4_status check_grouped_product(const uint8_t* a, const uint8_t* as, fp4
     if (!product_ok(rows + 32 * experts, K) || !product_ok(N * experts, K) || !product_ok(rows, N) ||
         (rows / 128 + experts) * ((N + 255) / 256) >= kMaxTiles)
         return FP4_ERR_SHAPE;
-    // a thread of the few-row kernel for each 1/4 of a column
+    // the few-row kernel has 4 threads a column at least, a launch 2^32 - 1
     if (N >= INT64_C(1) << 30) return FP4_ERR_SHAPE;
     // tiles are counted in 32 bits, also where offsets out of order overlap
     if (experts * (rows / 128 + 1) * ((N + 255) / 256) > INT32_MAX) return FP4_ERR_SHAPE;

@@ -32,7 +32,8 @@
 //     without the scales, which then scale each block's sum in fp32.  (A test of
 //     the scales in the loop, with a branch there, took 193 registers for 128 and
 //     up to 9 % of the time; this 1 to 2 %, the lift by 2^3: 96 rows over 64
-//     experts of 1408 x 2048 15.1 to 15.4 us.)
+//     experts of 1408 x 2048 15.1 to 15.4 us.  The second time over a tile is slow,
+//     24 x 4096 x 14336 with a NaN in one row 145 us for 20.5.)
 // More than 16 MT rows (of an expert) are taken one tile after another by the
 // workgroups of blockIdx.z in turn; the weights then come from the caches.
 #include "fp4_device.hpp"
@@ -257,7 +258,8 @@ __global__ __launch_bounds__(64 * W) void gemm_few(
                     const __amdgpu_buffer_rsrc_t rsb = raw_buffer(SB + ((int64_t)g * N + n0) * 8, nleft * 8);
                     v4f sum = {};
 #pragma unroll 1
-                    for (int b = 8 * g + quad; b < 8 * g + 8; b += 4) {
+                    for (int s = 0; s < 2; ++s) {
+                        const int b = 8 * g + 4 * s + quad;
                         const bool in = b < nb;
                         const uint32_t offm = in ? (uint32_t)m * (uint32_t)K + (uint32_t)b * 32 : kOob;
                         const v4i codes[2] = {load16(ra, offm), load16(ra, offm + 16)};

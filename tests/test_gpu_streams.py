@@ -81,3 +81,36 @@ def test_stream_zero_is_the_default_stream():
     got = F.fp4_rmsnorm_backward(x, x, w, torch.ones(64, device="cuda"), stream=0)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_a_given_stream_inside_a_captured_graph():
+    """The norm on the capturing stream, its gradient and a product on a stream
+    that forks from it, replayed with other inputs and eager work between."""
+    need_gpu()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, dy = (torch.randn(T, K, device="cuda", generator=g).bfloat16() for _ in range(2))
+    w = torch.randn(K, device="cuda", generator=g).bfloat16()
+    wq, ws = F.fp4_hadamard_quantize(torch.randn(N, K, device="cuda", generator=g).bfloat16())
+    side = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        q, s, h, rstd = F.fp4_rmsnorm_quantize(x, w, x, stream=here)
+        side.wait_stream(here)
+        y = F.fp4_gemm_decode(q, s, wq, ws, stream=side)
+        back = F.fp4_rmsnorm_backward(dy, h, w, rstd, stream=side.cuda_stream)
+        here.wait_stream(side)
+        return (h, y + 1) + back
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        caught = step()
+    for i in range(4):
+        x.mul_(1.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(caught, step()):
+            assert torch.equal(a, b), i
+        torch.cuda.synchronize()
