@@ -3,8 +3,8 @@ for AMD Instinct MI355X (gfx950).
 
 The functions below carry the names of the C entry points (include/fp4.h)
 and only marshal arguments: shapes and pointers of torch tensors in, status
-codes out (through ctypes; the norm, grouped and few-row operators, whose
-calls are short, through the CPython functions of csrc/torch_binding.cpp).  Every step of the computation runs in the HIP kernels of the
+codes out (through ctypes; the operators from the norm on, whose calls are
+short, through the CPython functions of csrc/torch_binding*.cpp).  Every step of the computation runs in the HIP kernels of the
 library.  torch supplies device memory and the current HIP stream.
 
 A call runs on the current stream of its tensors' device, or on `stream` (a
@@ -28,6 +28,8 @@ HAD_NONE, HAD_DET, HAD_SIGNED = 0, 1, 2
 RTN, SR = 0, 1
 OUT_F32, OUT_BF16 = 0, 1
 FMT_MXFP4, FMT_MXFP8 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+ACT_SILU, ACT_GELU = 0, 1
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp4.so")
@@ -87,6 +89,24 @@ def lib() -> ctypes.CDLL:
     L.fp4_gemm_grouped.restype = i32
     L.fp4_gemm_grouped_wgrad.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, i32, vp]
     L.fp4_gemm_grouped_wgrad.restype = i32
+    L.fp4_moe_route.argtypes = [vp, i32, i64, i64, i64, i32, i32, vp, vp, vp]
+    L.fp4_moe_route.restype = i32
+    L.fp4_moe_route_backward.argtypes = [vp, vp, i32, vp, i64, i64, i64, i32, i32, vp, vp]
+    L.fp4_moe_route_backward.restype = i32
+    L.fp4_moe_sort.argtypes = [vp, i64, i64, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    L.fp4_moe_sort.restype = i32
+    L.fp4_moe_sort_workspace_bytes.argtypes = [i64, i64]
+    L.fp4_moe_sort_workspace_bytes.restype = ctypes.c_size_t
+    L.fp4_moe_gather.argtypes = [vp, vp, vp, i64, i64, i64, i64, vp, vp, vp]
+    L.fp4_moe_gather.restype = i32
+    L.fp4_moe_combine.argtypes = [vp, vp, vp, i64, i64, i64, i64, vp, vp]
+    L.fp4_moe_combine.restype = i32
+    L.fp4_moe_combine_backward.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, vp, vp, vp]
+    L.fp4_moe_combine_backward.restype = i32
+    L.fp4_glu.argtypes = [vp, vp, vp, vp, i64, i32, i64, i64, vp, i32, vp, vp, vp, vp, vp]
+    L.fp4_glu.restype = i32
+    L.fp4_glu_backward.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i64, i64, vp, vp, vp]
+    L.fp4_glu_backward.restype = i32
     L.fp4_status_string.argtypes = [i32]
     L.fp4_status_string.restype = ctypes.c_char_p
     _lib = L
@@ -513,6 +533,94 @@ def fp4_gemm_grouped_wgrad(dytq: torch.Tensor, dyts: torch.Tensor, xtq: torch.Te
     [rows, K] quantized along rows by fp4_quantize_grouped with these offsets
     (see include/fp4.h)."""
     return _call(_native().gemm_grouped_wgrad, dytq, stream, dytq, dyts, xtq, xts, offsets, rows, out, out_dtype)
+
+
+def fp4_moe_route(logits: torch.Tensor, k: int, score: int = SCORE_SOFTMAX, normalize: bool = True, out=None,
+                  stream=None):
+    """(ids int32 [T, k], weights fp32 [T, k]): the k experts of the largest
+    logits [T, E] (fp32 or bf16) of each token, largest first, equal ones by
+    their index, and their scores, over their sum if `normalize` (see
+    include/fp4.h).  Logits of -infinity or NaN are no choice (id -1, weight 0
+    where nothing else is left).  `out`: optional preallocated (ids, weights)."""
+    return _call(_native().moe_route, logits, stream, logits, k, score, normalize, out)
+
+
+def fp4_moe_route_backward(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor,
+                           score: int = SCORE_SOFTMAX, normalize: bool = True, out: torch.Tensor | None = None,
+                           stream=None):
+    """dlogits [T, E] in the type of the logits, from the gradient of
+    fp4_moe_route's weights for its ids (see include/fp4.h)."""
+    return _call(_native().moe_route_backward, logits, stream, dweights, logits, ids, score, normalize, out)
+
+
+def fp4_moe_sort_workspace_bytes(slots: int, experts: int) -> int:
+    return int(lib().fp4_moe_sort_workspace_bytes(slots, experts))
+
+
+def fp4_moe_sort(ids: torch.Tensor, experts: int, out=None, workspace: torch.Tensor | None = None, stream=None):
+    """Slots sorted by expert from ids int32 [T, k]: (offsets [experts + 1] as the
+    grouped operators take them, order [T k] the slot t k + j of each row, position
+    [T, k] the row of each slot), int32.  A slot whose id is outside of [0,
+    experts) has position -1, and its place in order is behind the last expert's rows.
+    `out`: optional preallocated (offsets, order, position)."""
+    return _call(_native().moe_sort, ids, stream, ids, experts, out, workspace)
+
+
+def fp4_moe_gather(x: torch.Tensor, position: torch.Tensor, scales: torch.Tensor | None = None, out=None, stream=None):
+    """Tokens to their experts' rows: out[position[t, j]] = x[t] for x bf16
+    [T, cols], or MXFP8 codes uint8 [T, cols] with `scales` [T, cols / 32], giving
+    (codes, scales).  Rows of no slot are left as they were (in a new tensor of
+    T k rows: not set).  `out`: optional tensor, or pair, of any number of rows;
+    positions beyond them are no slot's.  The gradient is fp4_moe_combine without
+    weights."""
+    return _call(_native().moe_gather, x, stream, x, position, scales, out)
+
+
+def fp4_moe_combine(y: torch.Tensor, position: torch.Tensor, weights: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, stream=None):
+    """out[t] = sum over j of weights[t, j] y[position[t, j]]: bf16 [T, cols] of
+    the experts' rows y bf16 [rows, cols]; weights fp32 [T, k], all 1 if None (the
+    gradient is then fp4_moe_gather)."""
+    return _call(_native().moe_combine, y, stream, y, position, weights, out)
+
+
+def fp4_moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, position: torch.Tensor, weights: torch.Tensor,
+                             out=None, stream=None):
+    """(dy bf16 [rows, cols], dweights fp32 [T, k]) of fp4_moe_combine with
+    weights from dout bf16 [T, cols].  Rows of no slot are left as they were (in
+    a new dy: not set).  `out`: optional preallocated (dy, dweights); dy may be y."""
+    return _call(_native().moe_combine_backward, y, stream, dout, y, position, weights, out)
+
+
+def fp4_glu(x: torch.Tensor, act: int = ACT_SILU, weights: torch.Tensor | None = None,
+            order: torch.Tensor | None = None, offsets: torch.Tensor | None = None, checkpoint: bool = False, out=None,
+            stream=None):
+    """The gated activation y[r, c] = w_r act(x[r, c]) x[r, cols + c] of x bf16
+    [rows, 2 cols], gate and up side by side (see include/fp4.h): y bf16
+    [rows, cols], with `checkpoint` (y, xq, xs), x in MXFP8 (mx8_shapes(rows, 2
+    cols)) for fp4_glu_backward.  weights (fp32, one a row in any shape) and order
+    (int32, fp4_moe_sort's): w_r = weights[order[r]], or weights[r] without an order.
+    offsets (fp4_moe_sort's): rows of no expert are left as they were (in a new
+    tensor: not set).  `out`: optional preallocated y, or (y, xq, xs)."""
+    return _call(_native().glu, x, stream, x, act, weights, order, offsets, checkpoint, out)
+
+
+def fp4_glu_quantize(x: torch.Tensor, act: int = ACT_SILU, weights: torch.Tensor | None = None,
+                     order: torch.Tensor | None = None, offsets: torch.Tensor | None = None, fmt: int = FMT_MXFP8,
+                     out=None, stream=None):
+    """fp4_glu with its output quantized along cols: (codes, scales) in `fmt`, as
+    fp4_rmsnorm_quantize gives them, for fp4_gemm_decode and fp4_gemm_grouped."""
+    return _call(_native().glu_quantize, x, stream, x, act, weights, order, offsets, fmt, out)
+
+
+def fp4_glu_backward(dy: torch.Tensor, xq: torch.Tensor, xs: torch.Tensor, act: int = ACT_SILU,
+                     weights: torch.Tensor | None = None, order: torch.Tensor | None = None,
+                     offsets: torch.Tensor | None = None, out=None, stream=None):
+    """dx bf16 [rows, 2 cols] of fp4_glu from dy bf16 [rows, cols] and its
+    checkpoint, and with weights (dx, dweights fp32 in the shape of weights).  Rows
+    of no expert leave dx as it was (in a new tensor: not set) and give 0 in
+    dweights.  `out`: optional preallocated dx, or (dx, dweights)."""
+    return _call(_native().glu_backward, dy, stream, dy, xq, xs, act, weights, order, offsets, out)
 
 
 from . import linear  # noqa: E402  (the autograd layer built on the calls above)

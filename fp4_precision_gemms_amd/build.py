@@ -1,6 +1,6 @@
 """Builds libfp4.so (the HIP kernels and the C ABI) in-tree for gfx950, and
 beside it libfp4calib.so, the MFMA-rate measurement aid (include/fp4_calib.h),
-and _torch_binding.so, the CPython functions of csrc/torch_binding.cpp.
+and _torch_binding.so, the CPython functions of csrc/torch_binding*.cpp.
 
     python -m fp4_precision_gemms_amd.build
 
@@ -28,8 +28,10 @@ LIB_PATH = os.path.join(HERE, "libfp4.so")
 CALIB_LIB_PATH = os.path.join(HERE, "libfp4calib.so")
 BINDING_PATH = os.path.join(HERE, "_torch_binding.so")
 
-SOURCES = ["fp4_abi.cpp", "fp4_abi_ops.cpp", "quant_mx.hip", "gemm_mx.hip", "nvfp4.hip", "norm_mx.hip", "gemm_few.hip",
-           "gemm_grouped.hip", "gemm_depth.hip", "quant_grouped.hip"]
+SOURCES = ["fp4_abi.cpp", "fp4_abi_ops.cpp", "fp4_abi_moe.cpp", "quant_mx.hip", "gemm_mx.hip", "nvfp4.hip", "norm_mx.hip",
+           "gemm_few.hip", "gemm_grouped.hip", "gemm_depth.hip", "quant_grouped.hip", "moe_route.hip", "moe_sort.hip",
+           "moe_rows.hip", "glu_mx.hip"]
+BINDING_SOURCES = ["torch_binding.cpp", "torch_binding_moe.cpp"]
 CALIB_SOURCES = ["calib_mfma.hip"]
 ARCH = "gfx950"
 
@@ -65,27 +67,27 @@ def _link(objs: list[str], path: str) -> None:
     os.replace(tmp, path)
 
 
-def _compile_binding() -> str:
+def _compile_binding(src: str) -> str:
     import torch
 
-    obj = os.path.join(BUILD_DIR, "torch_binding.o")
+    obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE, "-isystem", inc,
            "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"],
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
-           "-c", os.path.join(CSRC, "torch_binding.cpp"), "-o", obj]
+           "-c", os.path.join(CSRC, src), "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("compile failed: %s\n%s%s" % (" ".join(cmd), res.stdout, res.stderr))
     return obj
 
 
-def _link_binding(obj: str) -> None:
+def _link_binding(objs: list[str]) -> None:
     import torch
 
     tmp = BINDING_PATH + ".tmp%d" % os.getpid()
-    cmd = [os.environ.get("CXX", "g++"), "-shared", "-fPIC", obj, "-o", tmp,
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-fPIC", *objs, "-o", tmp,
            "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python",
            "-L", HERE, "-l:" + os.path.basename(LIB_PATH), "-Wl,-rpath,$ORIGIN"]
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -100,11 +102,11 @@ def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = SOURCES + CALIB_SOURCES
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 1)) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = [ex.submit(_compile_binding, s) for s in BINDING_SOURCES]
         objs = dict(zip(srcs, ex.map(_compile, srcs)))
     _link([objs[s] for s in SOURCES], LIB_PATH)
     _link([objs[s] for s in CALIB_SOURCES], CALIB_LIB_PATH)
-    _link_binding(binding.result())
+    _link_binding([b.result() for b in binding])
     if verbose:
         print("built", LIB_PATH, CALIB_LIB_PATH, "and", BINDING_PATH)
     return LIB_PATH

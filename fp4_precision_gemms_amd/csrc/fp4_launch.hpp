@@ -109,6 +109,40 @@ hipError_t launch_quant_grouped(const void* x, const int* offsets, int64_t exper
                                 uint8_t* codes_r, uint8_t* scales_r, uint8_t* codes_c, uint8_t* scales_c,
                                 hipStream_t st);
 
+// The k best experts of each token and their weights; the weights' gradient.
+hipError_t launch_moe_route(const void* logits, int bf16, int64_t tokens, int64_t experts, int64_t k, int sigmoid,
+                            int normalize, int* ids, float* weights, hipStream_t st);
+hipError_t launch_moe_route_back(const float* dweights, const void* logits, int bf16, const int* ids, int64_t tokens,
+                                 int64_t experts, int64_t k, int sigmoid, int normalize, void* dlogits, hipStream_t st);
+
+// Slots sorted by expert; counts: int32 [moe_sort_workgroups(slots), experts + 1],
+// not used (may be null) where that is one workgroup.
+int64_t moe_sort_workgroups(int64_t slots);
+hipError_t launch_moe_sort(const int* ids, int64_t slots, int64_t experts, int* offsets, int* order, int* position,
+                           int* counts, hipStream_t st);
+
+// Tokens' rows (of row_bytes bytes, a multiple of 16, and scale_bytes bytes of
+// scales, may be null) to the rows of their slots; rows combined by token; the
+// gradients of that.
+hipError_t launch_moe_gather(const void* x, int64_t row_bytes, const uint8_t* scales, int64_t scale_bytes,
+                             const int* position, int64_t tokens, int64_t k, int64_t rows, void* out,
+                             uint8_t* out_scales, hipStream_t st);
+hipError_t launch_moe_combine(const void* y, const int* position, const float* weights, int64_t tokens, int64_t k,
+                              int64_t rows, int64_t cols, void* out, hipStream_t st);
+hipError_t launch_moe_combine_back(const void* dout, const void* y, const int* position, const float* weights,
+                                   int64_t tokens, int64_t k, int64_t rows, int64_t cols, void* dy, float* dweights,
+                                   hipStream_t st);
+
+// Gated activation (fmt: 0 no codes, 1 MXFP8, 2 MXFP4; y and the checkpoint xq, xs
+// may be null) and its gradient from the checkpoint; weights, order and offsets
+// may be null.
+hipError_t launch_glu(const void* x, const float* weights, const int* order, const int* offsets, int64_t experts,
+                      int gelu, int64_t rows, int64_t cols, void* y, int fmt, uint8_t* codes, uint8_t* scales,
+                      uint8_t* xq, uint8_t* xs, hipStream_t st);
+hipError_t launch_glu_back(const void* dy, const uint8_t* xq, const uint8_t* xs, const float* weights, const int* order,
+                           const int* offsets, int64_t experts, int gelu, int64_t rows, int64_t cols, void* dx,
+                           float* dweights, hipStream_t st);
+
 uint32_t host_sign_word(int had, uint64_t seed);
 
 }  // namespace fp4dev

@@ -1,0 +1,217 @@
+// moe_rows.hip -- tokens to their experts' rows and back.
+//
+// position[t, j]: the row of token t's j-th choice, anything outside [0, rows) for
+// none.
+//     gather            row[position[t, j]] = x[t]
+//     combine           out[t] = sum_j w[t, j] y[position[t, j]]      (w = 1 if not given)
+//     combine's back    dy[position[t, j]] = w[t, j] dout[t],  dw[t, j] = <dout[t], y[position[t, j]]>
+// (the gather's gradient is the combination without weights, the gradient of that
+// the gather).  All of them walk over the tokens, so that a token's row is read or
+// written once, whatever k, and rows of no slot are not touched.  Bound by HBM:
+// each row is moved in 16-byte pieces, 64 lanes 1 KB.  Sums in binary32, over j
+// in their order, rounded to bf16 once.
+#include "fp4_launch.hpp"
+#include "mx_device.hpp"
+#include "wave.hpp"
+
+namespace fp4dev {
+namespace {
+
+constexpr int kThreads = 256;
+
+// The row of a token's j-th choice, -1 for none.
+__device__ __forceinline__ int64_t row_of(const int* position, int64_t slot, int64_t rows) {
+    const int p = wave_uniform(position[slot]);
+    return p >= 0 && p < rows ? p : -1;
+}
+
+struct Place {
+    int64_t token;
+    int c0;                                            // first 16-byte piece of this wave's lanes
+};
+
+// TPR threads share a token, V pieces each: the workgroup's tokens and the part
+// of their rows of nch pieces that this wave has.
+template <int TPR, int V>
+__device__ __forceinline__ Place place(int nch) {
+    constexpr int kTokens = kThreads / TPR;
+    const uint32_t b = blockIdx.y * gridDim.x + blockIdx.x;
+    const uint32_t parts = (nch + TPR * V - 1) / (TPR * V);
+    const uint32_t group = parts == 1 ? b : b / parts, part = b - group * parts;
+    return {(int64_t)group * kTokens + wave_uniform(threadIdx.x / TPR), (int)(part * TPR * V + threadIdx.x % TPR)};
+}
+
+template <int TPR, int V>
+__global__ __launch_bounds__(kThreads) void moe_gather(const uint4* __restrict__ x, int nch,
+                                                       const uint8_t* __restrict__ scales, int sb,
+                                                       const int* __restrict__ position, int64_t tokens, int k,
+                                                       int64_t rows, uint4* __restrict__ out,
+                                                       uint8_t* __restrict__ out_scales) {
+    const Place at = place<TPR, V>(nch);
+    if (at.token >= tokens) return;
+    uint4 v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (at.c0 + i * TPR < nch) v[i] = x[at.token * nch + at.c0 + i * TPR];
+    for (int j = 0; j < k; ++j) {
+        const int64_t r = row_of(position, at.token * k + j, rows);
+        if (r < 0) continue;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (at.c0 + i * TPR < nch) out[r * nch + at.c0 + i * TPR] = v[i];
+        // a row's scale bytes: by the lanes of its first part
+        if (scales && at.c0 < TPR)
+            for (int c = at.c0; c < sb; c += TPR) out_scales[r * sb + c] = scales[at.token * sb + c];
+    }
+}
+
+template <int TPR, int V, bool W>
+__global__ __launch_bounds__(kThreads) void moe_combine(const uint4* __restrict__ y, int nch,
+                                                        const int* __restrict__ position,
+                                                        const float* __restrict__ weights, int64_t tokens, int k,
+                                                        int64_t rows, uint4* __restrict__ out) {
+    const Place at = place<TPR, V>(nch);
+    if (at.token >= tokens) return;
+    float acc[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[i][e] = 0.0f;
+    constexpr int kAhead = 4;                          // rows on their way at a time
+    for (int j0 = 0; j0 < k; j0 += kAhead) {
+        uint4 v[kAhead][V];
+        int64_t r[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            r[j] = j0 + j < k ? row_of(position, at.token * k + j0 + j, rows) : -1;
+            if (r[j] < 0) continue;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (at.c0 + i * TPR < nch) v[j][i] = y[r[j] * nch + at.c0 + i * TPR];
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (r[j] < 0) continue;
+            const float w = W ? weights[at.token * k + j0 + j] : 1.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (at.c0 + i * TPR >= nch) continue;
+                float a[8];
+                unpack8(v[j][i], a);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[i][e] = W ? __builtin_fmaf(w, a[e], acc[i][e]) : acc[i][e] + a[e];
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (at.c0 + i * TPR < nch) out[at.token * nch + at.c0 + i * TPR] = pack8(acc[i]);
+}
+
+// A workgroup (TPR = 256) or a wave (64) takes a token.  dy may be y: a lane has
+// read a piece before it writes it, and no other reads it.
+template <int TPR>
+__global__ __launch_bounds__(kThreads) void moe_combine_back(const uint4* __restrict__ dout, const uint4* y, int nch,
+                                                             const int* __restrict__ position,
+                                                             const float* __restrict__ weights, int64_t tokens, int k,
+                                                             int64_t rows, uint4* dy, float* __restrict__ dweights) {
+    constexpr int kTokens = kThreads / TPR, kAhead = 4;
+    __shared__ float part[2][kAhead][kThreads / 64];
+    const int64_t t = (int64_t)(blockIdx.y * gridDim.x + blockIdx.x) * kTokens + wave_uniform(threadIdx.x / TPR);
+    if (t >= tokens) return;                           // a wave of its own, or the whole workgroup
+    const int lane = threadIdx.x % TPR, wave = wave_uniform(threadIdx.x >> 6);
+    int turn = 0;
+    for (int j0 = 0; j0 < k; j0 += kAhead, turn ^= 1) {
+        int64_t r[kAhead];
+        float w[kAhead], dot[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const bool in = j0 + j < k;
+            r[j] = in ? row_of(position, t * k + j0 + j, rows) : -1;
+            w[j] = in ? weights[t * k + j0 + j] : 0.0f;
+            dot[j] = 0.0f;
+        }
+        for (int c = lane; c < nch; c += TPR) {
+            const uint4 d = dout[t * nch + c];
+            uint4 v[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (r[j] >= 0) v[j] = y[r[j] * nch + c];
+            float g[8];
+            unpack8(d, g);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                if (r[j] < 0) continue;
+                float a[8];
+                unpack8(v[j], a);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    dot[j] = __builtin_fmaf(g[e], a[e], dot[j]);
+                    a[e] = w[j] * g[e];
+                }
+                dy[r[j] * nch + c] = pack8(a);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            dot[j] = wave_sum(dot[j]);
+            if (TPR > 64 && (threadIdx.x & 63) == 0) part[turn][j][wave] = dot[j];
+        }
+        // two buffers: the next turn's parts do not overwrite these before the
+        // barrier that every reader of these has passed
+        if constexpr (TPR > 64) __syncthreads();
+        if (lane < kAhead && j0 + lane < k) {
+            float s = 0.0f;
+            if constexpr (TPR > 64) {
+#pragma unroll
+                for (int i = 0; i < TPR / 64; ++i) s += part[turn][lane][i];
+            } else {
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) s = lane == j ? dot[j] : s;
+            }
+            dweights[t * k + j0 + lane] = s;
+        }
+    }
+}
+
+// Threads of a row: a wave up to 2 KB, else a workgroup.
+constexpr int kWaveRow = 128;
+
+dim3 grid_for(int64_t tokens, int64_t nch, int tpr, int v) {
+    const int64_t per = kThreads / tpr, parts = (nch + tpr * v - 1) / (tpr * v);
+    return grid_of((tokens + per - 1) / per * parts, kThreads);
+}
+
+}  // namespace
+
+hipError_t launch_moe_gather(const void* x, int64_t row_bytes, const uint8_t* scales, int64_t scale_bytes,
+                             const int* position, int64_t tokens, int64_t k, int64_t rows, void* out,
+                             uint8_t* out_scales, hipStream_t st) {
+    const int64_t nch = row_bytes / 16;
+    const bool narrow = nch <= kWaveRow;
+    return launch(narrow ? &moe_gather<64, 2> : &moe_gather<256, 2>, grid_for(tokens, nch, narrow ? 64 : 256, 2),
+                  dim3(kThreads), st, (const uint4*)x, (int)nch, scales, (int)scale_bytes, position, tokens, (int)k, rows,
+                  (uint4*)out, out_scales);
+}
+
+hipError_t launch_moe_combine(const void* y, const int* position, const float* weights, int64_t tokens, int64_t k,
+                              int64_t rows, int64_t cols, void* out, hipStream_t st) {
+    const int64_t nch = cols / 8;
+    const bool narrow = nch <= kWaveRow;
+    auto* const run = narrow ? (weights ? &moe_combine<64, 2, true> : &moe_combine<64, 2, false>)
+                             : (weights ? &moe_combine<256, 2, true> : &moe_combine<256, 2, false>);
+    return launch(run, grid_for(tokens, nch, narrow ? 64 : 256, 2), dim3(kThreads), st, (const uint4*)y, (int)nch,
+                  position, weights, tokens, (int)k, rows, (uint4*)out);
+}
+
+hipError_t launch_moe_combine_back(const void* dout, const void* y, const int* position, const float* weights,
+                                   int64_t tokens, int64_t k, int64_t rows, int64_t cols, void* dy, float* dweights,
+                                   hipStream_t st) {
+    const int64_t nch = cols / 8;
+    const bool narrow = nch <= kWaveRow;
+    return launch(narrow ? &moe_combine_back<64> : &moe_combine_back<256>,
+                  grid_of(narrow ? (tokens + 3) / 4 : tokens, kThreads), dim3(kThreads), st, (const uint4*)dout,
+                  (const uint4*)y, (int)nch, position, weights, tokens, (int)k, rows, (uint4*)dy, dweights);
+}
+
+}  // namespace fp4dev

@@ -39,34 +39,6 @@ __device__ __forceinline__ T wave_sum(T v) {
     return v;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& w, float* a) {
-    a[0] = bf16_lo(w.x); a[1] = bf16_hi(w.x); a[2] = bf16_lo(w.y); a[3] = bf16_hi(w.y);
-    a[4] = bf16_lo(w.z); a[5] = bf16_hi(w.z); a[6] = bf16_lo(w.w); a[7] = bf16_hi(w.w);
-}
-
-__device__ __forceinline__ uint4 pack8(const float* a) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = bf16_pair(a[2 * i], a[2 * i + 1]);
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Codes of 8 values under scale byte `byte` (not 255) as E4M3: the hardware
-// conversion rounds to nearest even but turns what lies beyond 464 into NaN,
-// so the scaled value is clamped to +-448 first.
-__device__ __forceinline__ uint2 encode8_e4m3(const float* y, uint32_t byte) {
-    const float inv = inv_scale_from_e8m0(byte);
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __builtin_amdgcn_fmed3f(y[i] * inv, -448.0f, 448.0f);
-    int lo = 0, hi = 0;
-    lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], lo, false);
-    lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
-    hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], hi, false);
-    hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], hi, true);
-    return make_uint2((uint32_t)lo, (uint32_t)hi);
-}
-
 // The row block of workgroup b of n.  Workgroups go round-robin over the 8
 // XCDs, each with an L2 of its own; here B consecutive row blocks (32 rows) run
 // on one XCD, so that the 16-byte code pieces and 8-byte scale groups of

@@ -9,153 +9,11 @@
 // package name and document them) and the stream as an integer.  Wrong types
 // raise TypeError, wrong shapes or devices ValueError, a nonzero status the
 // package's Fp4Error.
-#include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/python_variable.h>
-#include <torch/csrc/utils/object_ptr.h>
+#include "torch_binding.hpp"
 
-#include <ATen/ATen.h>
-#include <ATen/hip/EmptyTensor.h>
-#include <c10/core/DeviceGuard.h>
-
-#include <cstdarg>
-#include <string>
-#include <tuple>
-#include <utility>
-#include <vector>
-
-#include "fp4.h"
+using namespace fp4py;
 
 namespace {
-
-PyObject* fp4_error = nullptr;      // the package's Fp4Error
-
-using Shape = std::vector<int64_t>;
-
-// Raises `cls` with a printf-like message.
-[[noreturn]] void fail(PyObject* cls, const char* format, ...) {
-    va_list args;
-    va_start(args, format);
-    PyErr_FormatV(cls, format, args);
-    va_end(args);
-    throw python_error();
-}
-
-std::string text(at::IntArrayRef s) {
-    std::string t = "(";
-    for (size_t i = 0; i < s.size(); ++i) t += (i ? ", " : "") + std::to_string(s[i]);
-    return t + (s.size() == 1 ? ",)" : ")");
-}
-
-const char* type_text(at::ScalarType t) {
-    switch (t) {
-        case at::kBFloat16: return "torch.bfloat16";
-        case at::kByte: return "torch.uint8";
-        case at::kInt: return "torch.int32";
-        default: return "torch.float32";
-    }
-}
-
-const at::Tensor& tensor(PyObject* o, const char* name) {
-    if (!THPVariable_Check(o)) fail(PyExc_TypeError, "%s must be a tensor, got %s", name, Py_TYPE(o)->tp_name);
-    return THPVariable_Unpack(o);
-}
-
-// A contiguous tensor of that type and shape on `like`'s device (a GPU).
-const at::Tensor& need(const at::Tensor& t, at::ScalarType type, at::IntArrayRef shape, const at::Tensor& like,
-                       const char* name) {
-    if (t.sizes() != shape)
-        fail(PyExc_ValueError, "%s must have shape %s, got %s", name, text(shape).c_str(), text(t.sizes()).c_str());
-    if (t.scalar_type() != type)
-        fail(PyExc_TypeError, "%s must be %s, got %s", name, type_text(type), c10::toString(t.scalar_type()));
-    if (!t.is_cuda() || t.device() != like.device())
-        fail(PyExc_ValueError, "%s must be a GPU tensor on %s, got one on %s", name, like.device().str().c_str(),
-                                t.device().str().c_str());
-    if (!t.is_contiguous()) fail(PyExc_ValueError, "%s must be contiguous", name);
-    return t;
-}
-
-const at::Tensor& need(PyObject* o, at::ScalarType type, at::IntArrayRef shape, const at::Tensor& like,
-                       const char* name) {
-    return need(tensor(o, name), type, shape, like, name);
-}
-
-const at::Tensor& matrix(PyObject* o, at::ScalarType type, const char* name) {
-    const at::Tensor& t = tensor(o, name);
-    if (t.dim() != 2) fail(PyExc_ValueError, "%s must have two dimensions, got shape %s", name, text(t.sizes()).c_str());
-    return need(t, type, t.sizes(), t, name);
-}
-
-// A new tensor on `like`'s device, which is the current one: torch's caching
-// allocator without the dispatch of at::empty (a norm's call with its four
-// outputs 6.4 against 7.1 us).
-at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
-    return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
-}
-
-template <typename T = void>
-T* ptr(const at::Tensor& t) { return static_cast<T*>(t.data_ptr()); }
-
-int64_t integer(PyObject* o) {
-    const long long v = PyLong_AsLongLong(o);
-    if (v == -1 && PyErr_Occurred()) throw python_error();
-    return v;
-}
-// seeds: the low 64 bits of any Python integer
-uint64_t seed(PyObject* o) {
-    const unsigned long long v = PyLong_AsUnsignedLongLongMask(o);
-    if (PyErr_Occurred()) throw python_error();
-    return v;
-}
-void* stream(PyObject* o) { return reinterpret_cast<void*>(static_cast<uintptr_t>(seed(o))); }
-
-void check(fp4_status s) {
-    if (s == FP4_OK) return;
-    PyObject* e = PyObject_CallFunction(fp4_error, "is", (int)s, fp4_status_string(s));
-    if (e) {
-        PyErr_SetObject(fp4_error, e);
-        Py_DECREF(e);
-    }
-    throw python_error();
-}
-
-void arguments(Py_ssize_t got, Py_ssize_t want) {
-    if (got != want) fail(PyExc_TypeError, "%d arguments expected, got %d", (int)want, (int)got);
-}
-
-PyObject* wrap(const at::Tensor& t) { return THPVariable_Wrap(t); }
-
-template <typename... T>
-PyObject* tuple(const T&... t) {
-    PyObject* r = PyTuple_New(sizeof...(T));
-    if (!r) throw python_error();
-    Py_ssize_t i = 0;
-    ((PyTuple_SET_ITEM(r, i++, wrap(t))), ...);
-    return r;
-}
-
-// The items of an `out` argument: any sequence or iterator of tensors.
-std::vector<at::Tensor> items(PyObject* o, Py_ssize_t n) {
-    const THPObjectPtr f(PySequence_Fast(o, "out must be a sequence of tensors"));
-    if (!f) throw python_error();
-    if (PySequence_Fast_GET_SIZE(f.get()) != n)
-        fail(PyExc_ValueError, "out must hold %d tensors, got %d", (int)n, (int)PySequence_Fast_GET_SIZE(f.get()));
-    std::vector<at::Tensor> v;
-    for (Py_ssize_t i = 0; i < n; ++i) v.push_back(tensor(PySequence_Fast_GET_ITEM(f.get(), i), "output"));
-    return v;
-}
-
-int64_t groups32(int64_t n) { return (n + 31) / 32; }
-Shape code_shape(int64_t R, int64_t C) { return {groups32(R), C / 32, 512}; }
-Shape scale_shape(int64_t R, int64_t C) { return {(C / 32 + 7) / 8, R, 8}; }
-
-at::ScalarType out_type(int64_t out) {
-    if (out != FP4_OUT_F32 && out != FP4_OUT_BF16) check(FP4_ERR_ENUM);
-    return out == FP4_OUT_BF16 ? at::kBFloat16 : at::kFloat;
-}
-
-at::Tensor output(PyObject* o, at::IntArrayRef shape, int64_t out, const at::Tensor& like) {
-    return o == Py_None ? empty(shape, out_type(out), like) : need(o, out_type(out), shape, like, "out");
-}
 
 // (x, weight, residual, eps, fmt, out, y, stream)
 PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -275,14 +133,6 @@ PyObject* gemm_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// the number of experts of row offsets (int32 [experts + 1])
-int64_t experts_of(const at::Tensor& offsets, const at::Tensor& like) {
-    if (offsets.dim() != 1 || offsets.size(0) < 2)
-        fail(PyExc_ValueError, "offsets must be int32 [experts + 1], got shape %s", text(offsets.sizes()).c_str());
-    need(offsets, at::kInt, offsets.sizes(), like, "offsets");
-    return offsets.size(0) - 1;
-}
-
 Shape grouped_codes(int64_t rows, int64_t cols, int64_t E, bool along_rows) {
     return along_rows ? Shape{cols / 32, 8 * FP4_GROUPED_STAGES(rows, E), 512}
                       : Shape{FP4_GROUPED_UNITS(rows, E), cols / 32, 512};
@@ -378,6 +228,9 @@ PyObject* set_error(PyObject*, PyObject* cls) {
 #define FP4_METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FP4_METHOD(rmsnorm_quantize), FP4_METHOD(rmsnorm_backward), FP4_METHOD(gemm_decode),
                          FP4_METHOD(quantize_grouped), FP4_METHOD(gemm_grouped), FP4_METHOD(gemm_grouped_wgrad),
+                         FP4_METHOD(moe_route), FP4_METHOD(moe_route_backward), FP4_METHOD(moe_sort),
+                         FP4_METHOD(moe_gather), FP4_METHOD(moe_combine), FP4_METHOD(moe_combine_backward),
+                         FP4_METHOD(glu), FP4_METHOD(glu_quantize), FP4_METHOD(glu_backward),
                          {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_torch_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

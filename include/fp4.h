@@ -28,8 +28,8 @@
  *   - Pointers are device pointers (hipMalloc / torch CUDA tensors) owned by
  *     the caller, 16-byte aligned, tensors contiguous row-major.  The library
  *     allocates nothing in these calls and keeps no state between calls,
- *     except the device workspace the caller passes to nvfp4_quantize and
- *     fp4_rmsnorm_backward.
+ *     except the device workspace the caller passes to nvfp4_quantize,
+ *     fp4_rmsnorm_backward and fp4_moe_sort.
  *   - `stream` is a hipStream_t (NULL = the null stream).  Every call only
  *     enqueues work on it and returns; results are ready when the stream is.
  *   - Arguments are validated before any HIP call.  The status code is the
@@ -489,6 +489,144 @@ fp4_status fp4_gemm_grouped_wgrad(const uint8_t* dytq, const uint8_t* dyts, cons
                                   const uint8_t* xts, const int32_t* offsets, int64_t experts,
                                   int64_t rows, int64_t N, int64_t K, void* dw, fp4_out_dtype out,
                                   void* stream);
+
+/*
+ * A mixture of experts around the grouped products.  `tokens` T tokens choose k
+ * of E = `experts` experts each; slot t k + j is token t's j-th choice, and S =
+ * T k < 2^31 slots give S rows sorted by expert.
+ */
+
+/* Scores of the experts, both increasing in the logit l: */
+typedef enum {
+    FP4_SCORE_SOFTMAX = 0,   /* exp(l) over its sum over all experts             */
+    FP4_SCORE_SIGMOID = 1    /* 1 / (1 + exp(-l))                                */
+} fp4_score;
+
+/*
+ * fp4_moe_route -- the router's choice: each token's k experts of the largest
+ * logits [T, E] (row-major fp32 or bf16, `dtype`), largest first, equal ones by
+ * their index, as ids[T, k], and their weights[T, k] (fp32): the scores, with
+ * `normalize` 1 over the sum of the chosen ones' (by way of their logarithms:
+ * also where every score of a token is below binary32).  A logit that is
+ * -infinity or NaN is no choice; where nothing else is left the id is -1 and the
+ * weight 0.  An infinite largest logit counts as the limit: equal logits share.
+ * Requirements: 1 <= E <= 1024, 1 <= k <= min(E, 64); normalize 0 or 1 (else
+ * FP4_ERR_ENUM); pointers aligned to their elements.
+ */
+fp4_status fp4_moe_route(const void* logits, fp4_out_dtype dtype, int64_t tokens, int64_t experts, int64_t k,
+                         fp4_score score, int normalize, int32_t* ids, float* weights, void* stream);
+
+/*
+ * fp4_moe_route_backward -- the gradient dlogits[T, E] (in `dtype`, overwritten)
+ * of the weights of fp4_moe_route for fixed ids, from their gradient
+ * dweights[T, k].  Zero for every logit that is no choice, and for those not
+ * chosen unless the score is the softmax without `normalize`; slots whose id is
+ * outside of [0, E) are not looked at.  The valid ids of a token are distinct,
+ * as the router gives them (else the values are unspecified).
+ * Requirements as for fp4_moe_route.
+ */
+fp4_status fp4_moe_route_backward(const float* dweights, const void* logits, fp4_out_dtype dtype, const int32_t* ids,
+                                  int64_t tokens, int64_t experts, int64_t k, fp4_score score, int normalize,
+                                  void* dlogits, void* stream);
+
+/*
+ * fp4_moe_sort -- slots sorted by expert, in their order within one: from
+ * ids[slots], offsets[E + 1] as the grouped operators take them, order[slots]
+ * the slot of each row, position[slots] the row of each slot.  A slot whose id is
+ * outside of [0, E) has position -1, and its place in `order` is behind the last
+ * expert's rows.  workspace: fp4_moe_sort_workspace_bytes() bytes (0: may be
+ * NULL), whose contents need not be kept between calls; calls that overlap need
+ * one each.
+ * Requirements: 0 < slots < 2^31, 1 <= E <= 1024; pointers 4-byte aligned
+ * (workspace 16).
+ */
+fp4_status fp4_moe_sort(const int32_t* ids, int64_t slots, int64_t experts, int32_t* offsets, int32_t* order,
+                        int32_t* position, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes fp4_moe_sort needs. */
+size_t fp4_moe_sort_workspace_bytes(int64_t slots, int64_t experts);
+
+/*
+ * fp4_moe_gather -- tokens to their experts' rows: out[position[t, j]] = x[t] for
+ * every slot whose position is in [0, rows); other rows of out are left as they
+ * were.  x[T, cols] is bf16 (scales NULL), or MXFP8 codes with scales[T, cols /
+ * 32], which go to out_scales.  The gradient of x is fp4_moe_combine of out's
+ * without weights.  out must not overlap x.
+ * Requirements: cols % 32 == 0, cols < 2^24; T, k, rows > 0, T k < 2^31, rows <
+ * 2^31; pointers 16-byte aligned (position 4, scales any).
+ */
+fp4_status fp4_moe_gather(const void* x, const uint8_t* scales, const int32_t* position, int64_t tokens, int64_t k,
+                          int64_t rows, int64_t cols, void* out, uint8_t* out_scales, void* stream);
+
+/*
+ * fp4_moe_combine -- experts' rows back to the tokens: out[t] = sum over j of
+ * weights[t, j] y[position[t, j]], y bf16 [rows, cols], summed in binary32 in the
+ * order of j and rounded once to bf16 [T, cols].  weights NULL: all 1.  Slots
+ * whose position is outside of [0, rows) add nothing (their weight is not looked
+ * at).  out must not overlap y.
+ * Requirements as for fp4_moe_gather; weights 4-byte aligned.
+ */
+fp4_status fp4_moe_combine(const void* y_bf16, const int32_t* position, const float* weights, int64_t tokens, int64_t k,
+                           int64_t rows, int64_t cols, void* out_bf16, void* stream);
+
+/*
+ * fp4_moe_combine_backward -- the gradients of fp4_moe_combine with weights, from
+ * dout bf16 [T, cols]: dy[position[t, j]] = bf16(weights[t, j] dout[t]), other
+ * rows of dy left as they were, and dweights[t, j] = sum over the columns of
+ * dout[t] y[position[t, j]] (fp32, summed in an order that depends on the sizes
+ * only), 0 for a slot without a row.  The rows of a call's slots are distinct.
+ * dy may be y (in place).  (Without weights the gradient is fp4_moe_gather of
+ * dout.)  Requirements as for fp4_moe_combine.
+ */
+fp4_status fp4_moe_combine_backward(const void* dout_bf16, const void* y_bf16, const int32_t* position,
+                                    const float* weights, int64_t tokens, int64_t k, int64_t rows, int64_t cols,
+                                    void* dy_bf16, float* dweights, void* stream);
+
+/* Activations of a gate: act(g) = g sigma(s(g)), sigma(v) = 1 / (1 + exp(-v)). */
+typedef enum {
+    FP4_ACT_SILU = 0,        /* s(g) = g                                         */
+    FP4_ACT_GELU = 1         /* s(g) = 2 sqrt(2/pi) (g + 0.044715 g^3): the tanh
+                                form of GELU                                     */
+} fp4_act;
+
+/*
+ * fp4_glu -- the gated activation between two products: from x bf16 [rows, 2
+ * cols], gate and up side by side, y[r, c] = w_r act(x[r, c]) x[r, cols + c],
+ * computed in binary32 and rounded once, to bf16 [rows, cols] (y_bf16, NULL if not
+ * wanted) and / or to an operand of `rows` rows of `cols` elements in `fmt`
+ * (codes and scales as fp4_rmsnorm_quantize writes them, both NULL if not
+ * wanted).  xq [rows, 2 cols], xs [rows, 2 cols / 32]: the checkpoint for the
+ * backward pass, x in MXFP8 (both NULL if not wanted).
+ * weights (fp32 [rows], NULL: all 1) and order (int32 [rows], NULL: row r's weight
+ * is weights[r]): row r's weight is weights[order[r]], 0 where order[r] is outside
+ * of [0, rows).  offsets (int32 [experts + 1], NULL: every row counts): rows before
+ * offsets[0] or from offsets[experts] on are not read and nothing is written for
+ * them.
+ * Weighting here and not in fp4_moe_combine gives the same output of a layer whose
+ * second product has no bias, and its gradient needs no rows of that product.
+ * Requirements: cols % 32 == 0, cols < 2^24, 0 < rows < 2^31, rows ceil(cols /
+ * 1024) < 2^32; 1 <= experts <= 1024 with offsets; at least one output; pointers
+ * 16-byte aligned (weights, order, offsets 4).
+ */
+fp4_status fp4_glu(const void* x_bf16, const float* weights, const int32_t* order, const int32_t* offsets,
+                   int64_t experts, fp4_act act, int64_t rows, int64_t cols, void* y_bf16, fp4_format fmt,
+                   uint8_t* codes, uint8_t* scales, uint8_t* xq, uint8_t* xs, void* stream);
+
+/*
+ * fp4_glu_backward -- the gradients of fp4_glu at the checkpoint's values v = (g,
+ * u), from dy bf16 [rows, cols]: dx bf16 [rows, 2 cols] = (dy w_r u act'(g), dy w_r
+ * act(g)) in binary32, rounded once (the checkpoint's and the output's
+ * quantization are passed straight through), and with weights dweights (fp32
+ * [rows], as weights): dweights[order[r]] = sum over the columns of dy act(g) u, in
+ * an order that depends on the sizes only.  Rows of no expert leave their row of
+ * dx as it was and give 0 in dweights; the entries of `order` are distinct.  A
+ * checkpoint block of scale 255 (one that held a NaN or an infinity) gives NaN.
+ * dweights is required with weights and ignored without.
+ * Requirements as for fp4_glu.
+ */
+fp4_status fp4_glu_backward(const void* dy_bf16, const uint8_t* xq, const uint8_t* xs, const float* weights,
+                            const int32_t* order, const int32_t* offsets, int64_t experts, fp4_act act, int64_t rows,
+                            int64_t cols, void* dx_bf16, float* dweights, void* stream);
 
 /* Static, NUL-terminated name of a status code. */
 const char* fp4_status_string(fp4_status status);
