@@ -623,4 +623,4 @@ def fp4_glu_backward(dy: torch.Tensor, xq: torch.Tensor, xs: torch.Tensor, act: 
     return _call(_native().glu_backward, dy, stream, dy, xq, xs, act, weights, order, offsets, out)
 
 
-from . import linear  # noqa: E402  (the autograd layer built on the calls above)
+from . import linear, moe  # noqa: E402  (the autograd layers built on the calls above)
