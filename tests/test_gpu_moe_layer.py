@@ -328,7 +328,7 @@ def test_refusals():
                          (lambda: F.fp4_moe_route(logits, 2, 7), 4), (lambda: F.fp4_moe_route(logits[:0], 2), 2),
                          (lambda: F.fp4_moe_sort(ids, 0), 2), (lambda: F.fp4_moe_sort(ids, 1025), 2),
                          (lambda: F.fp4_moe_sort(ids[:0], 4), 2),
-                         (lambda: F.fp4_moe_sort(torch.zeros(5000, 1, dtype=torch.int32, device="cuda"), 4,
+                         (lambda: F.fp4_moe_sort(torch.zeros(100000, 1, dtype=torch.int32, device="cuda"), 4,
                                                  workspace=torch.zeros(16, dtype=torch.uint8, device="cuda")), 6),
                          (lambda: F.fp4_moe_gather(x[:0], ids[:0]), 2), (lambda: F.fp4_moe_combine(x, ids[:, :0]), 2),
                          (lambda: F.fp4_moe_gather(x[:, :40].contiguous(), ids), 2),

@@ -42,14 +42,14 @@ def test_route_errors(L):
 
 
 def test_sort_errors(L):
-    def call(ids=A, n=5000, E=64, off=A, order=A, pos=A, ws=A, b=1 << 20):
+    def call(ids=A, n=100000, E=64, off=A, order=A, pos=A, ws=A, b=1 << 20):
         return L.fp4_moe_sort(ids, n, E, off, order, pos, ws, b, None)
 
     for bad in (dict(n=0), dict(n=-4), dict(n=2 ** 31), dict(E=0), dict(E=1025), dict(E=-2 ** 40)):
         assert call(**bad) == ERR_SHAPE, bad
     for name in ("ids", "off", "order", "pos"):
         assert call(**{name: None}) == ERR_NULL and call(**{name: ODD}) == ERR_ALIGN, name
-    need = F.fp4_moe_sort_workspace_bytes(5000, 64)
+    need = F.fp4_moe_sort_workspace_bytes(100000, 64)
     assert need > 0 and call(b=need - 1) == ERR_WORKSPACE and call(ws=None) == ERR_WORKSPACE and call(ws=MIS) == ERR_ALIGN
     assert F.fp4_moe_sort_workspace_bytes(64, 1024) == 0 and F.fp4_moe_sort_workspace_bytes(0, 64) == 0
     assert F.fp4_moe_sort_workspace_bytes(2 ** 31 - 1, 1024) <= 256 * 1025 * 4
