@@ -17,6 +17,7 @@
 //
 // Bound by HBM: 4 bytes read an element of y and 2 written, 2.06 more for the
 // checkpoint; backward 4.06 read and 4 written.
+#include "exp_device.hpp"
 #include "fp4_launch.hpp"
 #include "mx_device.hpp"
 #include "wave.hpp"
@@ -40,17 +41,6 @@ __device__ __forceinline__ int64_t weight_at(const int* order, int64_t row, int6
     if (!order) return row;
     const int s = wave_uniform(order[row]);
     return s >= 0 && s < rows ? s : -1;
-}
-
-// exp(-a), a >= 0: 2^t by the hardware's exp2 with what the product a log2(e)
-// rounds off put back (without it the error grows with a, to 2^-18).  Zero in
-// binary32 long before a = 200, where an infinite a ends too; a NaN stays one.
-__device__ __forceinline__ float exp_minus(float a) {
-    constexpr float kLog2e = 1.44269504f, kRest = 1.92596303e-8f;   // log2(e) in two parts
-    a = a > 200.0f ? 200.0f : a;
-    const float t = a * kLog2e;
-    const float rest = __builtin_fmaf(a, kLog2e, -t) + a * kRest;
-    return __builtin_amdgcn_exp2f(-t) * __builtin_fmaf(rest, -0.693147181f, 1.0f);
 }
 
 template <bool GELU>

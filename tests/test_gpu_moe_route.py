@@ -146,3 +146,20 @@ def test_preallocated_outputs_and_unaligned_slices():
         for t in range(9):
             F.fp4_moe_route_backward(g[t:t + 1], l[t:t + 1], want[0][t:t + 1], out=part[t:t + 1])
         assert torch.equal(whole, part)
+
+
+def test_rows_off_the_vector_loads_alignment():
+    """The same values at an address that whole rows of four cannot be loaded from."""
+    need_gpu()
+    for dtype in (torch.float32, torch.bfloat16):
+        for E, k in ((40, 4), (200, 8), (1024, 20)):
+            l = torch.randn(9, E, device="cuda").to(dtype)
+            off = torch.empty(9 * E + 1, dtype=dtype, device="cuda")[1:].view(9, E)
+            off.copy_(l)
+            g = torch.randn(9, k, device="cuda")
+            out = torch.empty(9 * E + 1, dtype=dtype, device="cuda")[1:].view(9, E)
+            for score, normalize in KINDS:
+                a, b = (F.fp4_moe_route(t, k, score, normalize) for t in (l, off))
+                assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+                want = F.fp4_moe_route_backward(g, l, a[0], score, normalize)
+                assert torch.equal(want, F.fp4_moe_route_backward(g, off, a[0], score, normalize, out=out))
