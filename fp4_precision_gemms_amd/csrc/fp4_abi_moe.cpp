@@ -47,8 +47,8 @@ static fp4_status check_glu(int64_t rows, int64_t cols, fp4_act act, const int32
     if (act != FP4_ACT_SILU && act != FP4_ACT_GELU) return FP4_ERR_ENUM;
     if (rows <= 0 || rows > INT32_MAX || cols <= 0 || cols % 32 || cols >= kMaxContraction) return FP4_ERR_SHAPE;
     if (offsets && (experts <= 0 || experts > kMaxExperts)) return FP4_ERR_SHAPE;
-    // waves are counted in 32 bits, of 1024 columns at most
-    if (rows > (UINT32_MAX - 3) / ((cols + 1023) / 1024)) return FP4_ERR_SHAPE;
+    // waves are counted in 32 bits, of 512 columns at most
+    if (rows > (UINT32_MAX - 3) / ((cols + 511) / 512)) return FP4_ERR_SHAPE;
     return FP4_OK;
 }
 }  // namespace

@@ -54,6 +54,32 @@ __device__ __forceinline__ uint32_t encode8_hw(const float* y, uint32_t byte) {
     return w;
 }
 
+// Loads and stores of 16 and 8 bytes, non-temporal with NT.
+typedef uint32_t word4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t word2_t __attribute__((ext_vector_type(2)));
+template <bool NT>
+__device__ __forceinline__ uint4 load16(const uint4* p) {
+    if constexpr (!NT) return *p;
+    const word4_t v = __builtin_nontemporal_load(reinterpret_cast<const word4_t*>(p));
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+template <bool NT>
+__device__ __forceinline__ uint2 load8(const uint2* p) {
+    if constexpr (!NT) return *p;
+    const word2_t v = __builtin_nontemporal_load(reinterpret_cast<const word2_t*>(p));
+    return make_uint2(v.x, v.y);
+}
+template <bool NT>
+__device__ __forceinline__ void store16(uint4* p, uint4 v) {
+    if constexpr (!NT) *p = v;
+    else __builtin_nontemporal_store(word4_t{v.x, v.y, v.z, v.w}, reinterpret_cast<word4_t*>(p));
+}
+template <bool NT>
+__device__ __forceinline__ void store8(void* p, uint2 v) {
+    if constexpr (!NT) *static_cast<uint2*>(p) = v;
+    else __builtin_nontemporal_store(word2_t{v.x, v.y}, static_cast<word2_t*>(p));
+}
+
 // Eight bf16 values of 16 bytes, and back (rounded to nearest even).
 __device__ __forceinline__ void unpack8(const uint4& w, float* a) {
     a[0] = bf16_lo(w.x); a[1] = bf16_hi(w.x); a[2] = bf16_lo(w.y); a[3] = bf16_hi(w.y);

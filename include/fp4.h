@@ -605,7 +605,7 @@ typedef enum {
  * Weighting here and not in fp4_moe_combine gives the same output of a layer whose
  * second product has no bias, and its gradient needs no rows of that product.
  * Requirements: cols % 32 == 0, cols < 2^24, 0 < rows < 2^31, rows ceil(cols /
- * 1024) < 2^32; 1 <= experts <= 1024 with offsets; at least one output; pointers
+ * 512) < 2^32 - 3; 1 <= experts <= 1024 with offsets; at least one output; pointers
  * 16-byte aligned (weights, order, offsets 4).
  */
 fp4_status fp4_glu(const void* x_bf16, const float* weights, const int32_t* order, const int32_t* offsets,
