@@ -19,6 +19,15 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// The rows' reads are non-temporal (FAR) where they, or with the gradient's writes
+// both, are larger than the 256 MB last-level cache: combining 49152 rows of 4096
+// columns 93 to 80 us, behind a product 205 to 179 with it; the gradients of 16384 rows
+// of 4096 columns 68 to 55, of 49152 of 2048 88 to 69. Within that size they lose:
+// gradients of 4096 rows of 2048 columns 7.9 to 9.1.  (Non-temporal writes: 49152
+// gathered rows of 4096 columns 91 to 80, but 16384 32 to 38, and no gain with the
+// quantizer that reads them: 209 and 209, 69 and 76.)
+constexpr int64_t kFarBytes = INT64_C(1) << 28;
+
 // A token's rows and weights, 64 choices at a time, one a lane: their loads are
 // on their way together, and none of them waits for a store (loads and stores
 // return in order: with each position loaded where it is used, 128 tokens to 6
@@ -91,7 +100,7 @@ __global__ __launch_bounds__(kThreads) void moe_gather(const uint4* __restrict__
     }
 }
 
-template <int TPR, int V, bool W>
+template <int TPR, int V, bool W, bool FAR>
 __global__ __launch_bounds__(kThreads) void moe_combine(const uint4* __restrict__ y, int nch,
                                                         const int* __restrict__ position,
                                                         const float* __restrict__ weights, int64_t tokens, int k,
@@ -115,7 +124,7 @@ __global__ __launch_bounds__(kThreads) void moe_combine(const uint4* __restrict_
             if (r[j] < 0) continue;
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (at.c0 + i * TPR < nch) v[j][i] = y[r[j] * nch + at.c0 + i * TPR];
+                if (at.c0 + i * TPR < nch) v[j][i] = load16<FAR>(y + r[j] * nch + at.c0 + i * TPR);
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
@@ -138,7 +147,7 @@ __global__ __launch_bounds__(kThreads) void moe_combine(const uint4* __restrict_
 
 // A workgroup (TPR = 256) or a wave (64) takes a token.  dy may be y: a lane has
 // read a piece before it writes it, and no other reads it.
-template <int TPR>
+template <int TPR, bool FAR>
 __global__ __launch_bounds__(kThreads) void moe_combine_back(const uint4* __restrict__ dout, const uint4* y, int nch,
                                                              const int* __restrict__ position,
                                                              const float* __restrict__ weights, int64_t tokens, int k,
@@ -165,7 +174,7 @@ __global__ __launch_bounds__(kThreads) void moe_combine_back(const uint4* __rest
             uint4 v[kAhead];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j)
-                if (r[j] >= 0) v[j] = y[r[j] * nch + c];
+                if (r[j] >= 0) v[j] = load16<FAR>(y + r[j] * nch + c);
             float g[8];
             unpack8(d, g);
 #pragma unroll
@@ -226,9 +235,12 @@ hipError_t launch_moe_gather(const void* x, int64_t row_bytes, const uint8_t* sc
 hipError_t launch_moe_combine(const void* y, const int* position, const float* weights, int64_t tokens, int64_t k,
                               int64_t rows, int64_t cols, void* out, hipStream_t st) {
     const int64_t nch = cols / 8;
-    const bool narrow = nch <= kWaveRow;
-    auto* const run = narrow ? (weights ? &moe_combine<64, 2, true> : &moe_combine<64, 2, false>)
-                             : (weights ? &moe_combine<256, 2, true> : &moe_combine<256, 2, false>);
+    const bool narrow = nch <= kWaveRow, far = 2 * rows * cols >= kFarBytes;
+    auto* run = narrow ? (weights ? &moe_combine<64, 2, true, false> : &moe_combine<64, 2, false, false>)
+                       : (weights ? &moe_combine<256, 2, true, false> : &moe_combine<256, 2, false, false>);
+    if (far)
+        run = narrow ? (weights ? &moe_combine<64, 2, true, true> : &moe_combine<64, 2, false, true>)
+                     : (weights ? &moe_combine<256, 2, true, true> : &moe_combine<256, 2, false, true>);
     return launch(run, grid_for(tokens, nch, narrow ? 64 : 256, 2), dim3(kThreads), st, (const uint4*)y, (int)nch,
                   position, weights, tokens, (int)k, rows, (uint4*)out);
 }
@@ -237,9 +249,10 @@ hipError_t launch_moe_combine_back(const void* dout, const void* y, const int* p
                                    int64_t tokens, int64_t k, int64_t rows, int64_t cols, void* dy, float* dweights,
                                    hipStream_t st) {
     const int64_t nch = cols / 8;
-    const bool narrow = nch <= kWaveRow;
-    return launch(narrow ? &moe_combine_back<64> : &moe_combine_back<256>,
-                  grid_of(narrow ? (tokens + 3) / 4 : tokens, kThreads), dim3(kThreads), st, (const uint4*)dout,
+    const bool narrow = nch <= kWaveRow, far = 4 * rows * cols >= kFarBytes;
+    auto* const run = narrow ? (far ? &moe_combine_back<64, true> : &moe_combine_back<64, false>)
+                             : (far ? &moe_combine_back<256, true> : &moe_combine_back<256, false>);
+    return launch(run, grid_of(narrow ? (tokens + 3) / 4 : tokens, kThreads), dim3(kThreads), st, (const uint4*)dout,
                   (const uint4*)y, (int)nch, position, weights, tokens, (int)k, rows, (uint4*)dy, dweights);
 }
 
