@@ -141,11 +141,14 @@ __device__ __forceinline__ void decode8_e4m3(uint2 q, uint32_t byte, float* a) {
 }
 
 // TPR threads share a row: a wave, or the workgroup.
+constexpr int back_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
+
 template <bool GELU, int TPR, bool FAR>
-__global__ __launch_bounds__(kThreads) void glu_back(const uint4* __restrict__ dy, const uint2* __restrict__ xq,
+__global__ __launch_bounds__(back_threads(TPR)) void glu_back(const uint4* __restrict__ dy, const uint2* __restrict__ xq,
                                                      const uint8_t* __restrict__ xs, const float* __restrict__ weights,
                                                      const int* __restrict__ order, Live live, int64_t rows, int cols,
                                                      uint4* __restrict__ dx, float* __restrict__ dweights) {
+    constexpr int kThreads = back_threads(TPR);
     __shared__ float part[kThreads / 64];
     const int nch = cols / 8, nb = cols / 32;
     const int64_t row =
@@ -209,7 +212,7 @@ hipError_t launch_back(bool gelu, const void* dy, const uint8_t* xq, const uint8
     const bool far = 4 * rows * cols >= kFarBytes;
     auto* const run = far ? (gelu ? &glu_back<true, TPR, true> : &glu_back<false, TPR, true>)
                           : (gelu ? &glu_back<true, TPR, false> : &glu_back<false, TPR, false>);
-    constexpr int kRows = kThreads / TPR;
+    constexpr int kThreads = back_threads(TPR), kRows = kThreads / TPR;
     return launch(run, grid_of((rows + kRows - 1) / kRows, kThreads), dim3(kThreads), st, (const uint4*)dy,
                   (const uint2*)xq, xs, weights, order, live, rows, (int)cols, (uint4*)dx, dweights);
 }
@@ -226,7 +229,13 @@ hipError_t launch_glu(const void* x, const float* weights, const int* order, con
 hipError_t launch_glu_back(const void* dy, const uint8_t* xq, const uint8_t* xs, const float* weights, const int* order,
                            const int* offsets, int64_t experts, int gelu, int64_t rows, int64_t cols, void* dx,
                            float* dweights, hipStream_t st) {
-    auto* const run = cols <= 1024 ? &launch_back<64> : &launch_back<256>;
+    // 1024 threads for a row of 8192 columns or more (16384 x 14336 344 us with 256,
+    // 321 with 512, 299 with 1024; 96 x 14336 8.2, 6.7 and 6.0; but 16384 x 4096 87, 86
+    // and 103); a wave where it is one or two pieces of it, and where 256 threads would
+    // idle for the most part, if there are rows enough (12000 x 1408 27.1 and 24.9 us).
+    auto* const run = cols >= 8192                                       ? &launch_back<1024>
+                      : cols <= 1024 || (cols < 2048 && rows >= 1024) ? &launch_back<64>
+                                                                         : &launch_back<256>;
     return run(gelu != 0, dy, xq, xs, weights, order, Live{offsets, (int)experts}, rows, cols, dx, dweights, st);
 }
 
