@@ -41,15 +41,17 @@ __global__ __launch_bounds__(kThreads) void sort_count(const int* __restrict__ i
     for (int e = threadIdx.x; e <= E; e += kThreads) counts[(int64_t)blockIdx.x * (E + 1) + e] = count[e];
 }
 
-// The rows of a workgroup's `run` slots, tiles of kThreads I of them; counts null
-// for the only workgroup, whose slots are one tile.  bits: of the largest key.
-template <int I>
+// The rows of a workgroup's `run` slots, tiles of kThreads I of them; ONE: of the
+// only workgroup, whose slots are one tile (counts is not looked at) and whose order
+// goes through LDS, so that it leaves in whole lines.  bits: of the largest key.
+template <int I, bool ONE>
 __global__ __launch_bounds__(kThreads) void sort_place(const int* __restrict__ ids, int64_t slots, int E, int bits,
                                                        int64_t run, const int* __restrict__ counts,
                                                        int* __restrict__ offsets, int* __restrict__ order,
                                                        int* __restrict__ position) {
     constexpr int kTile = kThreads * I;
-    static_assert(kTile <= 65535, "a tile's counts in 16 bits");
+    static_assert(kTile <= 65535, "a tile's counts, and its slots, in 16 bits");
+    __shared__ uint16_t by_row[ONE ? kTile : 1];
     __shared__ __attribute__((aligned(4))) uint16_t count[kWaves][kKeys + 1];   // of a wave's slots; of the waves before
     __shared__ int next_row[kKeys];                    // of a key's slots that come next
     __shared__ int before_part[kKeys], all_part[kKeys], totals[kWaves];
@@ -63,7 +65,7 @@ __global__ __launch_bounds__(kThreads) void sort_place(const int* __restrict__ i
     // a key's slots of all workgroups and of those before this one: where the keys
     // are fewer than the threads, `groups` threads share a key's workgroups
     const int groups = bits < 10 ? kThreads >> bits : 1;
-    if (counts) {
+    if constexpr (!ONE) {
         for (int k = tid; k < kThreads || k <= E; k += kThreads) {
             const int e = groups > 1 ? k & ((1 << bits) - 1) : k;
             int before = 0, all = 0;
@@ -124,7 +126,7 @@ __global__ __launch_bounds__(kThreads) void sort_place(const int* __restrict__ i
         }
         if (tile == first) {
             int all[2] = {n[0], n[1]}, before[2] = {0, 0};
-            if (counts) {
+            if constexpr (!ONE) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     all[k] = 0;
@@ -160,8 +162,14 @@ __global__ __launch_bounds__(kThreads) void sort_place(const int* __restrict__ i
             const int64_t i = tile + in_tile + 64 * c;
             if (i >= end) continue;
             const int row = next_row[id[c]] + mine[id[c]] + rank[c];
-            order[row] = (int)i;
+            if constexpr (ONE) by_row[row] = (uint16_t)i;
+            else order[row] = (int)i;
             position[i] = id[c] < E ? row : -1;
+        }
+        if constexpr (ONE) {
+            __syncthreads();
+            for (int row = tid; row < (int)end; row += kThreads) order[row] = by_row[row];
+            return;
         }
         if (tile + kTile < end) {
             __syncthreads();
@@ -172,14 +180,18 @@ __global__ __launch_bounds__(kThreads) void sort_place(const int* __restrict__ i
     }
 }
 
-// One launch up to this many slots.
-constexpr int64_t kOneWorkgroup = 8192;
-constexpr int kTileItems = 2;                          // a thread's slots of a tile, with several workgroups
+// One launch up to this many slots (4096 of 64 experts 5.0 us, 6.1 with two; 6000 of
+// 256 8.3 and 7.3).
+constexpr int64_t kOneWorkgroup = 4096;
+// A thread's slots of a tile, with several workgroups: 16384 slots of 8 experts 6.7 us
+// with one and 7.4 with two, 49152 of 64 7.9 and 8.1, 131072 of 256 11.7 and 10.2, of
+// 1024 19.7 and 14.7.
+int64_t tile_items(int64_t slots) { return slots <= 65536 ? 1 : 2; }
 
-template <int I>
+template <int I, bool ONE>
 hipError_t launch_place(const int* ids, int64_t slots, int64_t experts, int64_t workgroups, int64_t run,
                         const int* counts, int* offsets, int* order, int* position, hipStream_t st) {
-    return launch(&sort_place<I>, dim3((unsigned)workgroups), dim3(kThreads), st, ids, slots, (int)experts,
+    return launch(&sort_place<I, ONE>, dim3((unsigned)workgroups), dim3(kThreads), st, ids, slots, (int)experts,
                   32 - __builtin_clz((unsigned)experts), run, counts, offsets, order, position);
 }
 
@@ -187,7 +199,7 @@ hipError_t launch_place(const int* ids, int64_t slots, int64_t experts, int64_t 
 
 int64_t moe_sort_workgroups(int64_t slots) {
     if (slots <= kOneWorkgroup) return 1;
-    const int64_t n = (slots + kThreads * kTileItems - 1) / (kThreads * kTileItems);
+    const int64_t tile = kThreads * tile_items(slots), n = (slots + tile - 1) / tile;
     return n < 256 ? n : 256;
 }
 
@@ -195,18 +207,17 @@ hipError_t launch_moe_sort(const int* ids, int64_t slots, int64_t experts, int* 
                            int* counts, hipStream_t st) {
     const int64_t n = moe_sort_workgroups(slots);
     if (n == 1) {
-        auto* const place = slots <= kThreads       ? &launch_place<1>
-                            : slots <= 2 * kThreads ? &launch_place<2>
-                            : slots <= 4 * kThreads ? &launch_place<4>
-                                                    : &launch_place<8>;
+        auto* const place = slots <= kThreads       ? &launch_place<1, true>
+                            : slots <= 2 * kThreads ? &launch_place<2, true>
+                                                    : &launch_place<4, true>;
         return place(ids, slots, experts, 1, slots, nullptr, offsets, order, position, st);
     }
-    constexpr int64_t kTile = kThreads * kTileItems;
-    const int64_t run = ((slots + n - 1) / n + kTile - 1) / kTile * kTile;
+    const int64_t tile = kThreads * tile_items(slots), run = ((slots + n - 1) / n + tile - 1) / tile * tile;
     const hipError_t e =
         launch(&sort_count, dim3((unsigned)n), dim3(kThreads), st, ids, slots, (int)experts, run, counts);
     if (e != hipSuccess) return e;
-    return launch_place<kTileItems>(ids, slots, experts, n, run, counts, offsets, order, position, st);
+    auto* const place = tile == kThreads ? &launch_place<1, false> : &launch_place<2, false>;
+    return place(ids, slots, experts, n, run, counts, offsets, order, position, st);
 }
 
 }  // namespace fp4dev
