@@ -103,6 +103,8 @@ def lib() -> ctypes.CDLL:
     L.fp4_moe_combine.restype = i32
     L.fp4_moe_combine_backward.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, vp, vp, vp]
     L.fp4_moe_combine_backward.restype = i32
+    L.fp4_quantize_experts.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, vp]
+    L.fp4_quantize_experts.restype = i32
     L.fp4_glu.argtypes = [vp, vp, vp, vp, i64, i32, i64, i64, vp, i32, vp, vp, vp, vp, vp]
     L.fp4_glu.restype = i32
     L.fp4_glu_backward.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i64, i64, vp, vp, vp]
@@ -533,6 +535,29 @@ def fp4_gemm_grouped_wgrad(dytq: torch.Tensor, dyts: torch.Tensor, xtq: torch.Te
     [rows, K] quantized along rows by fp4_quantize_grouped with these offsets
     (see include/fp4.h)."""
     return _call(_native().gemm_grouped_wgrad, dytq, stream, dytq, dyts, xtq, xts, offsets, rows, out, out_dtype)
+
+
+def fp4_quantize_experts(w: torch.Tensor, out=None, stream=None):
+    """The weights w bf16 [E, N, K] of a mixture of experts (N and K multiples of
+    32) quantized both ways, as fp4_gemm_grouped takes them: (wtq, wts) of W^T for
+    Dgrad, (wq, ws) for the forward product, each [E, ...] (see include/fp4.h).
+    `out`: optional preallocated (wtq, wts, wq, ws)."""
+    if w.dim() != 3:
+        raise ValueError("w must be [experts, N, K], got shape %s" % (tuple(w.shape),))
+    _need(w, torch.bfloat16, "w")
+    E, N, K = w.shape
+    shapes = [(E, *s) for s in (code_shape(K, N), scale_shape(K, N), code_shape(N, K), scale_shape(N, K))]
+    out = [_empty(s, torch.uint8, w.device, stream) for s in shapes] if out is None else list(out)
+    if len(out) != 4:
+        raise ValueError("out must be (wtq, wts, wq, ws)")
+    for t, s in zip(out, shapes):
+        _need(t, torch.uint8, "output")
+        if tuple(t.shape) != s or t.device != w.device:
+            raise ValueError("output of shape %s on %s expected, got %s on %s" % (s, w.device, tuple(t.shape), t.device))
+    with torch.cuda.device(w.device):
+        _check(lib().fp4_quantize_experts(w.data_ptr(), E, N, K, *(t.data_ptr() for t in out),
+                                          _stream_ptr(stream, w.device)))
+    return tuple(out)
 
 
 def fp4_moe_route(logits: torch.Tensor, k: int, score: int = SCORE_SOFTMAX, normalize: bool = True, out=None,

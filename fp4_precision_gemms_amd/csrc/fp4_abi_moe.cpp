@@ -1,6 +1,6 @@
 // fp4_abi_moe.cpp -- the C ABI's entry points around the experts' products
 // (declared in include/fp4.h): router, sorted slots, rows gathered and combined,
-// gated activation.  Argument validation, then dispatch to the HIP launchers, with
+// gated activation, the experts' weights.  Argument validation, then dispatch to the HIP launchers, with
 // no HIP call before every argument has been checked, shapes before pointers.
 #include "fp4.h"
 
@@ -145,6 +145,27 @@ fp4_status fp4_glu_backward(const void* dy_bf16, const uint8_t* xq, const uint8_
         return FP4_ERR_ALIGN;
     return from_hip(fp4dev::launch_glu_back(dy_bf16, xq, xs, weights, order, offsets, experts, act == FP4_ACT_GELU, rows,
                                             cols, dx_bf16, dweights, (hipStream_t)stream));
+}
+
+fp4_status fp4_quantize_experts(const void* w_bf16, int64_t experts, int64_t N, int64_t K, uint8_t* wtq, uint8_t* wts,
+                                uint8_t* wq, uint8_t* ws, void* stream) {
+    if (experts <= 0 || experts > kMaxExperts || N <= 0 || K <= 0 || N % 32 || K % 32 || N >= (INT64_C(1) << 22) ||
+        K >= kMaxContraction || !product_ok(N, K) || !product_ok(N * K, experts))
+        return FP4_ERR_SHAPE;
+    if (!w_bf16 || !wtq || !wts || !wq || !ws) return FP4_ERR_NULL;
+    if (!aligned16(w_bf16) || !aligned16(wtq) || !aligned16(wts) || !aligned16(wq) || !aligned16(ws))
+        return FP4_ERR_ALIGN;
+    if (N * K * 2 < (INT64_C(1) << 31))
+        return from_hip(fp4dev::launch_quant_mx_stack(w_bf16, experts, N, K, wtq, wts, wq, ws, (hipStream_t)stream));
+    // beyond the stack's 32-bit offsets within a matrix: one after another
+    for (int64_t e = 0; e < experts; ++e) {
+        const hipError_t s = fp4dev::launch_quant_mx_dual(
+            (const char*)w_bf16 + e * N * K * 2, N, K, 32, FP4_HAD_NONE, 0, FP4_RTN, 0, wtq + e * FP4_CODE_BYTES(K, N),
+            wts + e * FP4_SCALE_BYTES(K, N), 32, FP4_HAD_NONE, 0, FP4_RTN, 0, wq + e * FP4_CODE_BYTES(N, K),
+            ws + e * FP4_SCALE_BYTES(N, K), (hipStream_t)stream);
+        if (s != hipSuccess) return FP4_ERR_LAUNCH;
+    }
+    return FP4_OK;
 }
 
 }  // extern "C"

@@ -47,6 +47,12 @@ hipError_t launch_quant_mx_dual(const void* x, int64_t rows, int64_t cols, int h
                                 int rnd_c, uint64_t sr_seed_c, uint8_t* codes_c, uint8_t* scales_c,
                                 hipStream_t st);
 
+// Both outputs, without rotation and to nearest, of each matrix of a stack [count,
+// rows, cols], the operands of one matrix after those of another.  Needs rows % 32 ==
+// 0, cols % 32 == 0 and rows cols 2 < 2^31.
+hipError_t launch_quant_mx_stack(const void* x, int64_t count, int64_t rows, int64_t cols, uint8_t* codes_r,
+                                 uint8_t* scales_r, uint8_t* codes_c, uint8_t* scales_c, hipStream_t st);
+
 // The two Wgrad operands a [rows, n1] and b [rows, n2] quantized along rows
 // with one rotation (own SR seeds), in one launch when it fits.
 hipError_t launch_quant_mx_pair(const void* a, int64_t rows, int64_t n1, const void* b, int64_t n2,

@@ -32,9 +32,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (AXIS_ROWS, FMT_MXFP4, HAD_DET, HAD_NONE, OUT_BF16, RTN, code_shape, fp4_gemm_grouped,
+from . import (AXIS_ROWS, FMT_MXFP4, HAD_DET, HAD_NONE, OUT_BF16, RTN, fp4_gemm_grouped,
                fp4_gemm_grouped_wgrad, fp4_gemm_mx, fp4_hadamard_quantize, fp4_hadamard_quantize_dual,
-               fp4_quantize_grouped_dual, fp4_rmsnorm_backward, fp4_rmsnorm_quantize, scale_shape)
+               fp4_quantize_experts, fp4_quantize_grouped_dual, fp4_rmsnorm_backward, fp4_rmsnorm_quantize)
 
 _SR_COLS = 0x9E3779B97F4A7C15      # tells the SR stream of the Dgrad operand from the Wgrad one's
 
@@ -152,15 +152,8 @@ class MXFP4NormLinear(torch.nn.Module):
 def quantize_experts(w: torch.Tensor):
     """Both operands of each of the experts' weights w [E, N, K] (bf16, N and K
     multiples of 32), as fp4_gemm_grouped takes them: (wtq, wts) for Dgrad,
-    (wq, ws) for the forward product.  One launch an expert, 13 us each on the
-    host: 40 experts of 736 x 1120 526 us, 8 of 14336 x 4096 310 (bound by their
-    bytes)."""
-    E, N, K = w.shape
-    shapes = (code_shape(K, N), scale_shape(K, N), code_shape(N, K), scale_shape(N, K))
-    out = tuple(torch.empty((E, *s), dtype=torch.uint8, device=w.device) for s in shapes)
-    for e in range(E):
-        fp4_hadamard_quantize_dual(w[e], out=[t[e] for t in out])
-    return out
+    (wq, ws) for the forward product."""
+    return fp4_quantize_experts(w.contiguous())
 
 
 class MXFP4GroupedLinearFunction(torch.autograd.Function):

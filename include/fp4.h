@@ -582,6 +582,20 @@ fp4_status fp4_moe_combine_backward(const void* dout_bf16, const void* y_bf16, c
                                     const float* weights, int64_t tokens, int64_t k, int64_t rows, int64_t cols,
                                     void* dy_bf16, float* dweights, void* stream);
 
+/*
+ * fp4_quantize_experts -- the weights w bf16 [experts, N, K] of a mixture of
+ * experts quantized both ways, as fp4_gemm_grouped takes them: for each expert what
+ *   fp4_hadamard_quantize_dual(w[e], N, K, rows: none, nearest, -> wtq[e], wts[e],
+ *                              cols: none, nearest, -> wq[e], ws[e])
+ * writes, the operands of one expert after another's (wtq / wts: W^T for Dgrad, K
+ * rows of N elements; wq / ws: W for the forward product, N rows of K), in one
+ * launch where an expert's weight is below 2 GiB.
+ * Requirements: N % 32 == 0, K % 32 == 0, N < 2^22, K < 2^24; 1 <= experts <=
+ * 1024; pointers 16-byte aligned.
+ */
+fp4_status fp4_quantize_experts(const void* w_bf16, int64_t experts, int64_t N, int64_t K, uint8_t* wtq, uint8_t* wts,
+                                uint8_t* wq, uint8_t* ws, void* stream);
+
 /* Activations of a gate: act(g) = g sigma(s(g)), sigma(v) = 1 / (1 + exp(-v)). */
 typedef enum {
     FP4_ACT_SILU = 0,        /* s(g) = g                                         */

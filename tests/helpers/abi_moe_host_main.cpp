@@ -61,6 +61,15 @@ hipError_t launch_glu_back(const void*, const uint8_t*, const uint8_t*, const fl
                            int64_t experts, int gelu, int64_t rows, int64_t cols, void*, float*, hipStream_t) {
     return record("glu back", experts, rows, cols, 0, gelu, 0, weights);
 }
+hipError_t launch_quant_mx_stack(const void*, int64_t count, int64_t rows, int64_t cols, uint8_t*, uint8_t*, uint8_t*,
+                                 uint8_t*, hipStream_t) {
+    return record("stack", count, rows, cols, 0, 0, 0, nullptr);
+}
+hipError_t launch_quant_mx_dual(const void* x, int64_t rows, int64_t cols, int, int had_r, uint64_t, int rnd_r, uint64_t,
+                                uint8_t* codes_r, uint8_t*, int, int, uint64_t, int, uint64_t, uint8_t*,
+                                uint8_t* scales_c, hipStream_t) {
+    return record("dual", rows, cols, codes_r - (uint8_t*)nullptr, scales_c - (uint8_t*)nullptr, had_r, rnd_r, x);
+}
 }  // namespace fp4dev
 
 namespace {
@@ -160,7 +169,26 @@ int main() {
         REFUSED(fp4_glu_backward(x, q, q, f, i, i, 8, FP4_ACT_SILU, 3, n, x, f, nullptr), FP4_ERR_SHAPE);
     }
 
+    REACHES(fp4_quantize_experts(x, 64, 2816, 2048, q, q, q, q, nullptr), "stack");
+    CHECK(g_a == 64 && g_b == 2816 && g_c == 2048);
+    for (int64_t n : bad) {
+        REFUSED(fp4_quantize_experts(x, n, 64, 64, q, q, q, q, nullptr), FP4_ERR_SHAPE);
+        REFUSED(fp4_quantize_experts(x, 4, n, 64, q, q, q, q, nullptr), FP4_ERR_SHAPE);
+        REFUSED(fp4_quantize_experts(x, 4, 64, n, q, q, q, q, nullptr), FP4_ERR_SHAPE);
+    }
+    // an expert of 2 GiB: one launch each, at its own operands
+    {
+        const int before = g_count;
+        const int64_t N = 1 << 15, K = 1 << 15;
+        CHECK(fp4_quantize_experts(x, 3, N, K, q, q, q, q, nullptr) == FP4_OK);
+        CHECK(g_count == before + 3 && g_fn == "dual" && g_a == N && g_b == K);
+        CHECK(g_p == P<char>(0x10000) + 2 * N * K * 2);
+        CHECK(g_c == 0x30000 + 2 * FP4_CODE_BYTES(K, N));
+        CHECK(g_d == 0x30000 + 2 * FP4_SCALE_BYTES(N, K));
+    }
+
     g_status = hipErrorInvalidValue;
+    CHECK(fp4_quantize_experts(x, 3, 1 << 15, 1 << 15, q, q, q, q, nullptr) == FP4_ERR_LAUNCH);
     CHECK(fp4_moe_sort(i, 5, 8, i, i, i, nullptr, 0, nullptr) == FP4_ERR_LAUNCH);
     CHECK(fp4_moe_gather(x, nullptr, i, 5, 2, 11, 96, x, nullptr, nullptr) == FP4_ERR_LAUNCH);
     CHECK(fp4_glu_backward(x, q, q, f, i, i, 8, FP4_ACT_GELU, 3, 64, x, f, nullptr) == FP4_ERR_LAUNCH);

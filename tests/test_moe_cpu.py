@@ -106,6 +106,21 @@ def test_glu_errors(L):
     assert back(dw=ODD) == ERR_ALIGN
 
 
+def test_quantize_experts_errors(L):
+    def call(w=A, E=4, N=64, K=96, wtq=A, wts=A, wq=A, ws=A):
+        return L.fp4_quantize_experts(w, E, N, K, wtq, wts, wq, ws, None)
+
+    for bad in (dict(E=0), dict(E=1025), dict(N=0), dict(N=48), dict(K=16), dict(K=-32), dict(N=2 ** 22),
+                dict(E=1024, K=2 ** 40)):
+        assert call(**bad) == ERR_SHAPE, bad
+    for n in ("w", "wtq", "wts", "wq", "ws"):
+        assert call(**{n: None}) == ERR_NULL and call(**{n: MIS}) == ERR_ALIGN, n
+    with pytest.raises(ValueError, match="experts, N, K"):
+        F.fp4_quantize_experts(torch.zeros(64, 64, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="GPU"):
+        F.fp4_quantize_experts(torch.zeros(2, 64, 64, dtype=torch.bfloat16))
+
+
 def test_binding_refuses(L):
     f32, bf, i32, u8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
     z = lambda *s, dtype=bf: torch.zeros(*s, dtype=dtype)  # noqa: E731
