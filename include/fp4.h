@@ -551,7 +551,8 @@ size_t fp4_moe_sort_workspace_bytes(int64_t slots, int64_t experts);
  * every slot whose position is in [0, rows); other rows of out are left as they
  * were.  x[T, cols] is bf16 (scales NULL), or MXFP8 codes with scales[T, cols /
  * 32], which go to out_scales.  The gradient of x is fp4_moe_combine of out's
- * without weights.  out must not overlap x.
+ * without weights.  The rows of a call's slots are distinct (else one of their
+ * tokens' is left, or parts of several).  out must not overlap x.
  * Requirements: cols % 32 == 0, cols < 2^24; T, k, rows > 0, T k < 2^31, rows <
  * 2^31; pointers 16-byte aligned (position 4, scales any).
  */
@@ -618,6 +619,7 @@ typedef enum {
  * them.
  * Weighting here and not in fp4_moe_combine gives the same output of a layer whose
  * second product has no bias, and its gradient needs no rows of that product.
+ * No output may overlap x.
  * Requirements: cols % 32 == 0, cols < 2^24, 0 < rows < 2^31, rows ceil(cols /
  * 512) < 2^32 - 3; 1 <= experts <= 1024 with offsets; at least one output; pointers
  * 16-byte aligned (weights, order, offsets 4).
@@ -635,7 +637,8 @@ fp4_status fp4_glu(const void* x_bf16, const float* weights, const int32_t* orde
  * an order that depends on the sizes only.  Rows of no expert leave their row of
  * dx as it was and give 0 in dweights; the entries of `order` are distinct.  A
  * checkpoint block of scale 255 (one that held a NaN or an infinity) gives NaN.
- * dweights is required with weights and ignored without.
+ * dweights is required with weights and ignored without.  dx must not overlap an
+ * input.
  * Requirements as for fp4_glu.
  */
 fp4_status fp4_glu_backward(const void* dy_bf16, const uint8_t* xq, const uint8_t* xs, const float* weights,

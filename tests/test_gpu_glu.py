@@ -12,7 +12,7 @@ from _util import need_gpu, say, ungroup_scales, untile_codes
 
 pytestmark = pytest.mark.gpu
 
-SHAPES = [(1, 32), (1, 1408), (3, 96), (33, 736), (70, 1024), (5, 1056), (17, 2080), (2, 14336)]
+SHAPES = [(1, 32), (1, 1408), (3, 96), (33, 736), (70, 1024), (5, 1056), (17, 2080), (2, 14336), (1030, 1056)]
 ACTS = [F.ACT_SILU, F.ACT_GELU]
 HALF = 2.0 ** -8       # half a step of bf16
 

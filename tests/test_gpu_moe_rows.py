@@ -155,6 +155,56 @@ def test_combine_and_its_gradient(T, k, E, cols, weighted):
     assert torch.isnan(y2[free]).all()
 
 
+@pytest.mark.parametrize("k,cols", [(70, 96), (64, 32), (130, 1056)])
+def test_more_choices_than_lanes(k, cols):
+    """Positions and weights come 64 at a time."""
+    need_gpu()
+    T = 5
+    rng, _, position = case(T, k, 16, cols)
+    say("many choices", k, cols)
+    live = position >= 0
+    p = gpu(position, torch.int32)
+    x = torch.from_numpy(rng.integers(-4, 5, (T, cols)).astype(np.float32)).bfloat16()
+    rows = torch.zeros(T * k, cols).bfloat16()
+    got = F.fp4_moe_gather(x.cuda(), p, out=rows.cuda()).cpu()
+    rows[position[live]] = x[np.nonzero(live)[0]]
+    assert torch.equal(got, rows)
+    # small whole numbers: every sum is exact in binary32
+    y = torch.from_numpy(rng.integers(-2, 3, (T * k, cols)).astype(np.float32)).bfloat16()
+    w = torch.from_numpy(rng.integers(-2, 3, (T, k)).astype(np.float32))
+    terms = y.double().numpy()[np.maximum(position, 0)] * w.double().numpy()[..., None] * live[..., None]
+    out = F.fp4_moe_combine(y.cuda(), p, w.cuda()).cpu()
+    assert torch.equal(out, torch.from_numpy(terms.sum(1)).bfloat16())
+    dy, dw = F.fp4_moe_combine_backward(x.cuda(), y.cuda(), p, w.cuda(), out=(torch.zeros_like(rows).cuda(), w.cuda()))
+    want = torch.zeros_like(rows)
+    want[position[live]] = (w[live][:, None] * x.float()[np.nonzero(live)[0]]).bfloat16()
+    assert torch.equal(dy.cpu(), want)
+    pairs = (y.double().numpy()[np.maximum(position, 0)] * x.double().numpy()[:, None] * live[..., None]).sum(2)
+    assert np.array_equal(dw.double().cpu().numpy(), pairs)
+
+
+@pytest.mark.parametrize("cols,rows", [(1024, 140000), (2080, 70000)])
+def test_rows_beyond_the_last_level_cache(cols, rows):
+    """Non-temporal reads: the same values as from a small copy of the rows."""
+    need_gpu()
+    say("far rows", cols, rows)
+    T, k = 20, 3
+    big = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    at = torch.randperm(rows, device="cuda")[:T * k].sort().values
+    small = torch.randn(T * k, cols, device="cuda").bfloat16()
+    big[at] = small
+    p = torch.randperm(T * k, device="cuda").int().view(T, k)
+    p[3, 1] = -1
+    far = torch.where(p < 0, -1, at[p.clamp(min=0).long()]).int()
+    w, d = torch.randn(T, k, device="cuda"), torch.randn(T, cols, device="cuda").bfloat16()
+    for weights in (None, w):
+        assert torch.equal(F.fp4_moe_combine(big, far, weights), F.fp4_moe_combine(small, p, weights))
+    dy, dw = F.fp4_moe_combine_backward(d, small, p, w, out=(torch.zeros_like(small), torch.empty_like(w)))
+    dbig, dwf = F.fp4_moe_combine_backward(d, big, far, w, out=(torch.zeros_like(big), torch.empty_like(w)))
+    assert torch.equal(dwf, dw) and torch.equal(dbig[at], dy)
+    assert int(torch.count_nonzero(dbig.any(1))) == int(torch.count_nonzero(dy.any(1)))
+
+
 def test_combine_of_infinite_values():
     need_gpu()
     inf = float("inf")
