@@ -16,7 +16,8 @@
 // overflows and 1 - sigma is no difference of near values.
 //
 // Bound by HBM: 4 bytes read an element of y and 2 written, 2.06 more for the
-// checkpoint; backward 4.06 read and 4 written.
+// checkpoint; backward 4.06 read and 4 written.  16384 x 14336: 302 us (6.3 TB/s)
+// forward with the checkpoint, 300 (6.3) backward.
 #include "exp_device.hpp"
 #include "fp4_launch.hpp"
 #include "mx_device.hpp"

@@ -9,7 +9,8 @@
 // the gather).  All of them walk over the tokens, so that a token's row is read or
 // written once, whatever k, and rows of no slot are not touched.  Bound by HBM:
 // each row is moved in 16-byte pieces, 64 lanes 1 KB.  Sums in binary32, over j
-// in their order, rounded to bf16 once.
+// in their order, rounded to bf16 once.  16384 rows of 4096 columns of 8192 tokens:
+// gathered in 32 us (6.3 TB/s), combined in 33 (6.1), gradients 52 (6.4).
 #include "fp4_launch.hpp"
 #include "mx_device.hpp"
 #include "wave.hpp"
@@ -29,9 +30,8 @@ constexpr int kThreads = 256;
 constexpr int64_t kFarBytes = INT64_C(1) << 28;
 
 // A token's rows and weights, 64 choices at a time, one a lane: their loads are
-// on their way together, and none of them waits for a store (loads and stores
-// return in order: with each position loaded where it is used, 128 tokens to 6
-// rows of 4 KB took 12.3 us).
+// on their way together, and none of them comes behind a store, which it would wait
+// for (they return in order).
 struct Choices {
     int position;                                      // -1 for none
     float weight;
@@ -73,6 +73,8 @@ __global__ __launch_bounds__(kThreads) void moe_gather(const uint4* __restrict__
                                                        uint8_t* __restrict__ out_scales) {
     const Place at = place<TPR, V>(nch);
     if (at.token >= tokens) return;
+    // zero past the row's end: left unset there, the array went to LDS, and every
+    // store waited for the one before (128 tokens to 6 rows of 4 KB 11.7 us, now 3.0)
     uint4 v[V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
