@@ -522,7 +522,8 @@ fp4_status fp4_moe_route(const void* logits, fp4_out_dtype dtype, int64_t tokens
  * dweights[T, k].  Zero for every logit that is no choice, and for those not
  * chosen unless the score is the softmax without `normalize`; slots whose id is
  * outside of [0, E) are not looked at.  The valid ids of a token are distinct,
- * as the router gives them (else the values are unspecified).
+ * as the router gives them (else the values are unspecified).  dlogits must not
+ * overlap an input.
  * Requirements as for fp4_moe_route.
  */
 fp4_status fp4_moe_route_backward(const float* dweights, const void* logits, fp4_out_dtype dtype, const int32_t* ids,
@@ -635,7 +636,8 @@ fp4_status fp4_glu(const void* x_bf16, const float* weights, const int32_t* orde
  * quantization are passed straight through), and with weights dweights (fp32
  * [rows], as weights): dweights[order[r]] = sum over the columns of dy act(g) u, in
  * an order that depends on the sizes only.  Rows of no expert leave their row of
- * dx as it was and give 0 in dweights; the entries of `order` are distinct.  A
+ * dx as it was and give 0 in dweights; the entries of `order` are distinct, and
+ * what none of them names in dweights is left as it was.  A
  * checkpoint block of scale 255 (one that held a NaN or an infinity) gives NaN.
  * dweights is required with weights and ignored without.  dx must not overlap an
  * input.

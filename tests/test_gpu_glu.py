@@ -205,6 +205,32 @@ def test_extreme_gates():
         assert torch.isnan(dx[2, :32]).all() and torch.isnan(dx[3, 32:cols]).all() and torch.isfinite(dx[3, :32]).all()
 
 
+@pytest.mark.parametrize("fmt", [F.FMT_MXFP8, F.FMT_MXFP4])
+def test_every_output_of_one_call(fmt):
+    """The C entry point writes whichever outputs it is given."""
+    need_gpu()
+    rng, x = inputs(37, 1056, 4)
+    x = x.cuda()
+    y, xq, xs = F.fp4_glu(x, F.ACT_GELU, checkpoint=True)
+    codes, scales = F.fp4_glu_quantize(x, F.ACT_GELU, fmt=fmt, out=None)
+    out = [torch.zeros_like(t) for t in (y, codes, scales, xq, xs)]
+    status = F.lib().fp4_glu(x.data_ptr(), None, None, None, 0, F.ACT_GELU, 37, 1056, out[0].data_ptr(), fmt,
+                             *(t.data_ptr() for t in out[1:]), torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert status == 0 and torch.equal(out[0], y) and torch.equal(out[3], xq) and torch.equal(out[4], xs)
+    values = R.mxfp8_values if fmt == F.FMT_MXFP8 else R.mxfp4_values
+    def rows(c, s):
+        c, s = c.cpu().numpy(), s.cpu().numpy()
+        return (c, s) if fmt == F.FMT_MXFP8 else (untile_codes(c, 37), ungroup_scales(s, 33))
+    assert np.array_equal(values(*rows(out[1], out[2])), values(*rows(codes, scales)))
+    # the checkpoint alone
+    only = [torch.zeros_like(t) for t in (xq, xs)]
+    status = F.lib().fp4_glu(x.data_ptr(), None, None, None, 0, F.ACT_GELU, 37, 1056, None, fmt, None, None,
+                             only[0].data_ptr(), only[1].data_ptr(), torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert status == 0 and torch.equal(only[0], xq) and torch.equal(only[1], xs)
+
+
 def test_orders_out_of_range():
     """A row whose order names no row has weight 0 and no entry in dweights."""
     need_gpu()

@@ -113,6 +113,9 @@ def test_infinite_logits_share():
         assert ids.tolist() == [[1, 3, 0], [0, 2, 1]]
         if score == F.SCORE_SOFTMAX:
             assert w.tolist() == [[0.5, 0.5, 0.0], [1.0, 0.0, 0.0]]
+            # of all experts, beside a token of ordinary logits in the same wave
+            both = torch.cat((l, torch.tensor([[0.0, 0.0, -inf, float("nan")]])))
+            assert F.fp4_moe_route(both.cuda(), 3, score, False)[1].tolist() == w.tolist() + [[0.5, 0.5, 0.0]]
         d = F.fp4_moe_route_backward(torch.ones(2, 3, device="cuda"), l.cuda(), ids, score, True)
         assert torch.isfinite(d).all()
 
