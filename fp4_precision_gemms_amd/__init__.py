@@ -176,10 +176,10 @@ def _call(function, like, stream, *args):
     a block of the current stream's pool may still be in use by work queued
     there, which `stream` does not wait for.  Outputs are recorded on the current
     stream, whose work may read them after it has waited for `stream`."""
+    if stream is None:
+        return function(*args, None)               # which takes the current one
     if not getattr(like, "is_cuda", False):
         return function(*args, 0)                  # refuses it
-    if stream is None:
-        return function(*args, torch._C._cuda_getCurrentRawStream(like.device.index))
     here, there = torch.cuda.current_stream(like.device), _as_stream(stream, like.device)
     with torch.cuda.stream(there):
         out = function(*args, there.cuda_stream)

@@ -43,6 +43,11 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found (ROCm is required to build libfp4.so)")
 
 
+def rocm_path() -> str:
+    """Where ROCm's headers are: ROCM_PATH, or above the hipcc in use."""
+    return os.environ.get("ROCM_PATH") or os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
+
+
 def compile_flags() -> list[str]:
     return ["-x", "hip", f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
             "-ffp-contract=off", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -75,6 +80,7 @@ def _compile_binding(src: str) -> str:
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE, "-isystem", inc,
            "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(rocm_path(), "include"), "-D__HIP_PLATFORM_AMD__",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
            "-c", os.path.join(CSRC, src), "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -88,7 +94,8 @@ def _link_binding(objs: list[str]) -> None:
 
     tmp = BINDING_PATH + ".tmp%d" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-shared", "-fPIC", *objs, "-o", tmp,
-           "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python",
+           "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip",
+           "-ltorch_python",
            "-L", HERE, "-l:" + os.path.basename(LIB_PATH), "-Wl,-rpath,$ORIGIN"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:

@@ -6,7 +6,8 @@
 // for the stream, 4 us the launch itself), here 6.4.
 //
 // Every function takes its arguments by position (the Python functions of the
-// package name and document them) and the stream as an integer.  Wrong types
+// package name and document them) and the stream as an integer, or None for the
+// current one.  Wrong types
 // raise TypeError, wrong shapes or devices ValueError, a nonzero status the
 // package's Fp4Error.
 #include "torch_binding.hpp"
@@ -46,7 +47,7 @@ PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const bool same = !added && ptr(h) == ptr(x);
     check(fp4_rmsnorm_quantize(ptr(x), added ? ptr(THPVariable_Unpack(a[2])) : nullptr, ptr(w), eps, rows, cols,
                                (fp4_format)fmt, same ? nullptr : ptr(h), ptr<float>(rstd), y, ptr<uint8_t>(codes),
-                               ptr<uint8_t>(scales), stream(a[7])));
+                               ptr<uint8_t>(scales), stream(a[7], x)));
     return tuple(codes, scales, h, rstd);
     END_HANDLE_TH_ERRORS
 }
@@ -78,7 +79,7 @@ PyObject* rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         need(ws, at::kByte, ws.sizes(), dy, "workspace");
     }
     check(fp4_rmsnorm_backward(ptr(dy), ptr(h), ptr(w), ptr<float>(rstd), dh, rows, cols, ptr(dx), ptr<float>(dw),
-                               ptr(ws), (size_t)ws.numel(), stream(a[7])));
+                               ptr(ws), (size_t)ws.numel(), stream(a[7], dy)));
     return tuple(dx, dw);
     END_HANDLE_TH_ERRORS
 }
@@ -128,7 +129,7 @@ PyObject* gemm_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t od = integer(a[5]);
     const at::Tensor c = output(a[4], {M, N}, od, aq);
     check(fp4_gemm_decode(ptr<uint8_t>(aq), ptr<uint8_t>(as), fmt, ptr<uint8_t>(wq), ptr<uint8_t>(ws), M, N, K,
-                          ptr(c), (fp4_out_dtype)od, stream(a[6])));
+                          ptr(c), (fp4_out_dtype)od, stream(a[6], aq)));
     return wrap(c);
     END_HANDLE_TH_ERRORS
 }
@@ -166,7 +167,7 @@ PyObject* quantize_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
     for (int i = 0; i < m; ++i) p[axes == 1 ? i + 2 : i] = ptr<uint8_t>(out[i]);
     check(fp4_quantize_grouped(ptr(x), ptr<int32_t>(off), E, rows, cols, (int)integer(a[3]),
                                (fp4_hadamard)integer(a[4]), seed(a[5]), (fp4_rounding)integer(a[6]), seed(a[7]),
-                               seed(a[8]), p[0], p[1], p[2], p[3], stream(a[10])));
+                               seed(a[8]), p[0], p[1], p[2], p[3], stream(a[10], x)));
     return axes == 3 ? tuple(out[0], out[1], out[2], out[3]) : tuple(out[0], out[1]);
     END_HANDLE_TH_ERRORS
 }
@@ -191,7 +192,7 @@ PyObject* gemm_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t od = integer(a[7]);
     const at::Tensor c = output(a[6], {rows, N}, od, aq);
     check(fp4_gemm_grouped(ptr<uint8_t>(aq), ptr<uint8_t>(as), fmt, ptr<int32_t>(off), E, rows, ptr<uint8_t>(wq),
-                           ptr<uint8_t>(ws), N, K, ptr(c), (fp4_out_dtype)od, stream(a[8])));
+                           ptr<uint8_t>(ws), N, K, ptr(c), (fp4_out_dtype)od, stream(a[8], aq)));
     return wrap(c);
     END_HANDLE_TH_ERRORS
 }
@@ -213,7 +214,7 @@ PyObject* gemm_grouped_wgrad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t od = integer(a[7]);
     const at::Tensor c = output(a[6], {E, N, K}, od, dq);
     check(fp4_gemm_grouped_wgrad(ptr<uint8_t>(dq), ptr<uint8_t>(ds), ptr<uint8_t>(xq), ptr<uint8_t>(xs),
-                                 ptr<int32_t>(off), E, rows, N, K, ptr(c), (fp4_out_dtype)od, stream(a[8])));
+                                 ptr<int32_t>(off), E, rows, N, K, ptr(c), (fp4_out_dtype)od, stream(a[8], dq)));
     return wrap(c);
     END_HANDLE_TH_ERRORS
 }

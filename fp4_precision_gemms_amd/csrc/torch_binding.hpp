@@ -9,6 +9,7 @@
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/hip/HIPStream.h>
 
 #include <cstdarg>
 #include <string>
@@ -85,6 +86,32 @@ inline at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Te
     return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
 
+// New tensors in one allocation, each at a multiple of 512 bytes: outputs that live
+// and die together, or are small.  An allocation costs 0.5 us of a call's 4 to 5, a
+// tensor in one 0.1.
+inline std::vector<at::Tensor> empty_together(const at::Tensor& like,
+                                              std::initializer_list<std::pair<Shape, at::ScalarType>> parts) {
+    auto bytes = [](const std::pair<Shape, at::ScalarType>& p) {
+        int64_t n = (int64_t)c10::elementSize(p.second);
+        for (const int64_t s : p.first) n *= s;
+        return n;
+    };
+    int64_t total = 0;
+    for (const auto& p : parts) total += (bytes(p) + 511) / 512 * 512;
+    const c10::Storage storage = empty({total}, at::kByte, like).storage();
+    std::vector<at::Tensor> out;
+    int64_t at = 0;
+    for (const auto& p : parts) {
+        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(storage), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                                c10::scalarTypeToTypeMeta(p.second));
+        t.unsafeGetTensorImpl()->set_storage_offset(at / (int64_t)c10::elementSize(p.second));
+        t.unsafeGetTensorImpl()->set_sizes_contiguous(p.first);
+        out.push_back(std::move(t));
+        at += (bytes(p) + 511) / 512 * 512;
+    }
+    return out;
+}
+
 template <typename T = void>
 T* ptr(const at::Tensor& t) { return static_cast<T*>(t.data_ptr()); }
 
@@ -99,7 +126,11 @@ inline uint64_t seed(PyObject* o) {
     if (PyErr_Occurred()) throw python_error();
     return v;
 }
-inline void* stream(PyObject* o) { return reinterpret_cast<void*>(static_cast<uintptr_t>(seed(o))); }
+// a stream's handle as an integer; None: the current stream of like's device
+inline void* stream(PyObject* o, const at::Tensor& like) {
+    if (o == Py_None) return c10::hip::getCurrentHIPStream(like.device().index()).stream();
+    return reinterpret_cast<void*>(static_cast<uintptr_t>(seed(o)));
+}
 
 inline void check(fp4_status s) {
     if (s == FP4_OK) return;

@@ -81,15 +81,16 @@ FP4_FUNCTION(moe_route) {
     const c10::DeviceGuard guard(l.device());
     at::Tensor ids, weights;
     if (a[4] == Py_None) {
-        ids = empty({T, k}, at::kInt, l);
-        weights = empty({T, k}, at::kFloat, l);
+        const auto o = empty_together(l, {{{T, k}, at::kInt}, {{T, k}, at::kFloat}});
+        ids = o[0];
+        weights = o[1];
     } else {
         const auto o = items(a[4], 2);
         ids = need(o[0], at::kInt, {T, k}, l, "ids");
         weights = need(o[1], at::kFloat, {T, k}, l, "weights");
     }
     check(fp4_moe_route(ptr(l), dtype_of(l), T, E, k, (fp4_score)integer(a[2]), truth(a[3]), ptr<int32_t>(ids),
-                        ptr<float>(weights), stream(a[5])));
+                        ptr<float>(weights), stream(a[5], l)));
     return tuple(ids, weights);
     END_HANDLE_TH_ERRORS
 }
@@ -106,7 +107,7 @@ FP4_FUNCTION(moe_route_backward) {
     const c10::DeviceGuard guard(l.device());
     const at::Tensor d = a[5] == Py_None ? empty({T, E}, l.scalar_type(), l) : need(a[5], l.scalar_type(), {T, E}, l, "out");
     check(fp4_moe_route_backward(ptr<float>(dw), ptr(l), dtype_of(l), ptr<int32_t>(ids), T, E, k,
-                                 (fp4_score)integer(a[3]), truth(a[4]), ptr(d), stream(a[6])));
+                                 (fp4_score)integer(a[3]), truth(a[4]), ptr(d), stream(a[6], l)));
     return wrap(d);
     END_HANDLE_TH_ERRORS
 }
@@ -121,9 +122,10 @@ FP4_FUNCTION(moe_sort) {
     const c10::DeviceGuard guard(ids.device());
     at::Tensor offsets, order, position, ws;
     if (a[2] == Py_None) {
-        offsets = empty({E + 1}, at::kInt, ids);
-        order = empty({slots}, at::kInt, ids);
-        position = empty(ids.sizes(), at::kInt, ids);
+        const auto o = empty_together(ids, {{{E + 1}, at::kInt}, {{slots}, at::kInt}, {ids.sizes().vec(), at::kInt}});
+        offsets = o[0];
+        order = o[1];
+        position = o[2];
     } else {
         const auto o = items(a[2], 3);
         offsets = need(o[0], at::kInt, {E + 1}, ids, "offsets");
@@ -138,7 +140,7 @@ FP4_FUNCTION(moe_sort) {
         ws = empty({bytes}, at::kByte, ids);
     }
     check(fp4_moe_sort(ptr<int32_t>(ids), slots, E, ptr<int32_t>(offsets), ptr<int32_t>(order), ptr<int32_t>(position),
-                       ws.defined() ? ptr(ws) : nullptr, ws.defined() ? (size_t)ws.numel() : 0, stream(a[4])));
+                       ws.defined() ? ptr(ws) : nullptr, ws.defined() ? (size_t)ws.numel() : 0, stream(a[4], ids)));
     return tuple(offsets, order, position);
     END_HANDLE_TH_ERRORS
 }
@@ -163,8 +165,13 @@ FP4_FUNCTION(moe_gather) {
         return need(t, type, {t.size(0), width}, x, name);
     };
     if (a[3] == Py_None) {
-        out = empty({rows, cols}, type, x);
-        if (eight) os = empty({rows, cols / 32}, type, x);
+        if (eight) {
+            const auto o = empty_together(x, {{{rows, cols}, type}, {{rows, cols / 32}, type}});
+            out = o[0];
+            os = o[1];
+        } else {
+            out = empty({rows, cols}, type, x);
+        }
     } else if (eight) {
         const auto o = items(a[3], 2);
         out = given(o[0], cols, "out");
@@ -175,7 +182,7 @@ FP4_FUNCTION(moe_gather) {
         rows = out.size(0);
     }
     check(fp4_moe_gather(ptr(x), s ? ptr<uint8_t>(*s) : nullptr, ptr<int32_t>(p), T, k, rows, cols, ptr(out),
-                         eight ? ptr<uint8_t>(os) : nullptr, stream(a[4])));
+                         eight ? ptr<uint8_t>(os) : nullptr, stream(a[4], x)));
     return eight ? tuple(out, os) : wrap(out);
     END_HANDLE_TH_ERRORS
 }
@@ -190,7 +197,7 @@ FP4_FUNCTION(moe_combine) {
     const float* w = a[2] == Py_None ? nullptr : ptr<float>(need(a[2], at::kFloat, {T, k}, y, "weights"));
     const c10::DeviceGuard guard(y.device());
     const at::Tensor out = a[3] == Py_None ? empty({T, cols}, at::kBFloat16, y) : need(a[3], at::kBFloat16, {T, cols}, y, "out");
-    check(fp4_moe_combine(ptr(y), ptr<int32_t>(p), w, T, k, rows, cols, ptr(out), stream(a[4])));
+    check(fp4_moe_combine(ptr(y), ptr<int32_t>(p), w, T, k, rows, cols, ptr(out), stream(a[4], y)));
     return wrap(out);
     END_HANDLE_TH_ERRORS
 }
@@ -215,7 +222,7 @@ FP4_FUNCTION(moe_combine_backward) {
         dw = need(o[1], at::kFloat, {T, k}, y, "dweights");
     }
     check(fp4_moe_combine_backward(ptr(d), ptr(y), ptr<int32_t>(p), ptr<float>(w), T, k, rows, cols, ptr(dy),
-                                   ptr<float>(dw), stream(a[5])));
+                                   ptr<float>(dw), stream(a[5], y)));
     return tuple(dy, dw);
     END_HANDLE_TH_ERRORS
 }
@@ -243,7 +250,7 @@ FP4_FUNCTION(glu) {
         y = need(a[6], at::kBFloat16, ys, x, "out");
     }
     check(fp4_glu(ptr(x), r.w(), r.o(), r.off(), r.experts, (fp4_act)integer(a[1]), rows, cols, ptr(y), FP4_FMT_MXFP8,
-                  nullptr, nullptr, kept ? ptr<uint8_t>(xq) : nullptr, kept ? ptr<uint8_t>(xs) : nullptr, stream(a[7])));
+                  nullptr, nullptr, kept ? ptr<uint8_t>(xq) : nullptr, kept ? ptr<uint8_t>(xs) : nullptr, stream(a[7], x)));
     return kept ? tuple(y, xq, xs) : wrap(y);
     END_HANDLE_TH_ERRORS
 }
@@ -260,15 +267,16 @@ FP4_FUNCTION(glu_quantize) {
     const c10::DeviceGuard guard(x.device());
     at::Tensor codes, scales;
     if (a[6] == Py_None) {
-        codes = empty(cs, at::kByte, x);
-        scales = empty(ss, at::kByte, x);
+        const auto o = empty_together(x, {{cs, at::kByte}, {ss, at::kByte}});
+        codes = o[0];
+        scales = o[1];
     } else {
         const auto o = items(a[6], 2);
         codes = need(o[0], at::kByte, cs, x, "codes");
         scales = need(o[1], at::kByte, ss, x, "scales");
     }
     check(fp4_glu(ptr(x), r.w(), r.o(), r.off(), r.experts, (fp4_act)integer(a[1]), rows, cols, nullptr, (fp4_format)fmt,
-                  ptr<uint8_t>(codes), ptr<uint8_t>(scales), nullptr, nullptr, stream(a[7])));
+                  ptr<uint8_t>(codes), ptr<uint8_t>(scales), nullptr, nullptr, stream(a[7], x)));
     return tuple(codes, scales);
     END_HANDLE_TH_ERRORS
 }
@@ -296,7 +304,7 @@ FP4_FUNCTION(glu_backward) {
     }
     check(fp4_glu_backward(ptr(dy), ptr<uint8_t>(xq), ptr<uint8_t>(xs), r.w(), r.o(), r.off(), r.experts,
                            (fp4_act)integer(a[3]), rows, cols, ptr(dx), r.weights ? ptr<float>(dw) : nullptr,
-                           stream(a[8])));
+                           stream(a[8], dy)));
     return r.weights ? tuple(dx, dw) : wrap(dx);
     END_HANDLE_TH_ERRORS
 }
