@@ -13,6 +13,9 @@ the streams that make the inputs and read the outputs; inputs that are freed
 before that stream is done are recorded on it (Tensor.record_stream), as for any
 torch operator on a side stream.
 
+Where a call makes its outputs itself, small ones of one call, and codes with their
+scales, may share an allocation, which lives as long as any of them.
+
 If the libraries have not been built (``python -m fp4_precision_gemms_amd.build``)
 every call raises; there is no fallback.
 """

@@ -290,7 +290,8 @@ __global__ __launch_bounds__(64) void moe_route_back(const float* __restrict__ d
                                                      const void* __restrict__ logits, const int* __restrict__ ids,
                                                      int64_t tokens, int E, bool whole, int k, bool sigmoid,
                                                      bool normalize, void* __restrict__ dlogits) {
-    __shared__ __attribute__((aligned(16))) float row[64 * V];                      // by token and expert: its gradient, or that of its weight
+    // by token and expert: its gradient, or that of its weight
+    __shared__ __attribute__((aligned(16))) float row[64 * V];
     const int64_t mine = token_of<LANES>(), t = mine < tokens ? mine : tokens - 1;
     const int lane = threadIdx.x & (LANES - 1);
     float* const at = row + threadIdx.x / LANES * (LANES * V);

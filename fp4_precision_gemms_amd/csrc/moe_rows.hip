@@ -79,7 +79,7 @@ __global__ __launch_bounds__(kThreads) void moe_gather(const uint4* __restrict__
 #pragma unroll
     for (int i = 0; i < V; ++i)
         v[i] = at.c0 + i * TPR < nch ? x[at.token * nch + at.c0 + i * TPR] : make_uint4(0, 0, 0, 0);
-    // a row's scale bytes, the first TPR of them: by the lanes of its first part
+    // a row's scale bytes, TPR at a time: by the lanes of its first part
     const bool scaled = scales && at.c0 < TPR;
     const uint8_t s0 = scaled && at.c0 < sb ? scales[at.token * sb + at.c0] : 0;
     for (int j0 = 0; j0 < k; j0 += 64) {
@@ -93,11 +93,15 @@ __global__ __launch_bounds__(kThreads) void moe_gather(const uint4* __restrict__
                 if (at.c0 + i * TPR < nch) out[r * nch + at.c0 + i * TPR] = v[i];
             if (scaled && at.c0 < sb) out_scales[r * sb + at.c0] = s0;
         }
-        if (!scaled || sb <= TPR) continue;
-        for (int c = at.c0 + TPR; c < sb; c += TPR) {
-            const uint8_t s = scales[at.token * sb + c];
-            for (int j = 0; j < 64 && j0 + j < k; ++j)
-                if (to.row(j) >= 0) out_scales[to.row(j) * sb + c] = s;
+        // (the same loops in every lane: each asks others for a row)
+        for (int first = TPR; scales && first < sb; first += TPR) {
+            const int c = at.c0 + first;
+            const bool in = scaled && c < sb;
+            const uint8_t s = in ? scales[at.token * sb + c] : 0;
+            for (int j = 0; j < 64 && j0 + j < k; ++j) {
+                const int64_t r = to.row(j);
+                if (r >= 0 && in) out_scales[r * sb + c] = s;
+            }
         }
     }
 }

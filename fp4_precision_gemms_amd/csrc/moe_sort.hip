@@ -27,6 +27,8 @@ constexpr int kWaves = 16, kThreads = 64 * kWaves;
 constexpr int kKeys = kMaxExperts + 1;
 static_assert(kMaxExperts <= kThreads, "a thread an expert");
 
+typedef uint32_t count_pair_t __attribute__((may_alias));       // two 16-bit counts
+
 __device__ __forceinline__ int key_of(int id, int E) { return id >= 0 && id < E ? id : E; }
 
 // Counts of each workgroup's `run` slots: counts[workgroup][E + 1].
@@ -87,7 +89,7 @@ __global__ __launch_bounds__(kThreads) void sort_place(const int* __restrict__ i
             for (int c = 0; c < I; ++c) id[c] = tile + in_tile + 64 * c < end ? ids[tile + in_tile + 64 * c] : -1;
             __syncthreads();                           // count and next_row have been read
         }
-        for (int e = lane; 2 * e <= E; e += 64) reinterpret_cast<uint32_t*>(mine)[e] = 0;
+        for (int e = lane; 2 * e <= E; e += 64) reinterpret_cast<count_pair_t*>(mine)[e] = 0;
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         // the rank of each slot among its wave's of the same key
 #pragma unroll

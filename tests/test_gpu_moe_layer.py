@@ -279,6 +279,26 @@ def test_every_call_on_a_given_stream(kind):
     assert all(pool_of(t) != s.cuda_stream for t in want)
 
 
+def test_outputs_of_one_allocation_are_apart():
+    """Writing all of one output leaves the others as they were, whatever the sizes."""
+    need_gpu()
+    for T, k, E in ((1, 1, 1), (3, 3, 127), (129, 2, 128), (700, 5, 1000)):
+        logits = torch.randn(T, E, device="cuda")
+        x8 = torch.randint(0, 100, (T, 96), device="cuda", dtype=torch.uint8)
+        s8 = torch.randint(0, 100, (T, 3), device="cuda", dtype=torch.uint8)
+        h = torch.randn(T, 192, device="cuda").bfloat16()
+        for call in (lambda: F.fp4_moe_route(logits, k), lambda: F.fp4_moe_sort(F.fp4_moe_route(logits, k)[0], E),
+                     lambda: F.fp4_moe_gather(x8, torch.arange(T, device="cuda").int()[:, None], s8),
+                     lambda: F.fp4_glu_quantize(h), lambda: F.fp4_glu_quantize(h, fmt=F.FMT_MXFP4, out=None)):
+            n = len(call())
+            for i in range(n):
+                got = call()
+                kept = [t.clone() for t in got]
+                got[i].fill_(77)
+                assert all(torch.equal(a, b) for j, (a, b) in enumerate(zip(got, kept)) if j != i)
+                assert (got[i] == 77).all() and all(t.is_contiguous() and t._version == (j == i) for j, t in enumerate(got))
+
+
 def test_two_sorts_at_once():
     """Calls on two streams, each with a workspace of its own."""
     need_gpu()

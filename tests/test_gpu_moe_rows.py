@@ -54,7 +54,7 @@ def test_sort_of_many_slots(E):
         assert np.array_equal(a.cpu().numpy(), b)
 
 
-COLS = [32, 96, 1024, 1056, 2080, 4096, 4128, 8224]
+COLS = [32, 96, 1024, 1056, 2080, 4096, 4128, 8224, 24608]
 SHAPES = [(1, 1, 4), (5, 6, 64), (67, 3, 5), (40, 9, 16)]
 
 
