@@ -208,32 +208,22 @@ __device__ __forceinline__ void load_logits(const void* logits, int64_t t, int E
 }
 
 // The scores of a lane's logits over the largest one, 0 for what is no choice, and
-// their sum over the token's lanes.
+// their sum over the token's lanes: the forward pass divides by it and the backward
+// pass by the same bits.  The exponential is the corrected one: equal logits err the
+// same way, so that hundreds of them would leave the plain one's error, which grows
+// with the argument, whole in the sum.
 template <int LANES, int V>
 __device__ __forceinline__ float scores(const float* l, float top, float* s) {
-    float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const float v = score_over(l[i], top);
-        s[i] = l[i] > -INFINITY ? v : 0.0f;            // not for a NaN
-        sum += s[i];
-    }
-    return token_sum<LANES>(sum);
-}
-
-// The sum of them alone.  A term's rounding counts by what it adds, so the plain
-// exponential does here: its relative error a 2^-24 at exp(-a) is at most 0.37 2^-24
-// of the largest term, 1 (16384 x 256: 9.1 to 8.2 us).
-template <int LANES, int V>
-__device__ __forceinline__ float sum_scores(const float* l, float top) {
-    if (__any(top == INFINITY)) {                      // the largest is no number to subtract
-        float s[V];
-        return scores<LANES, V>(l, top, s);
+    for (int i = 0; i < V; ++i)                        // of a NaN and 200 the minimum is 200
+        s[i] = exp_minus_to_200(fminf(top - l[i], 200.0f));
+    if (__any(top == INFINITY)) {                      // no number to subtract; other tokens' stay as they are
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = l[i] == INFINITY ? 1.0f : s[i];
     }
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i)                        // a NaN is no choice: the larger of it and -infinity
-        sum += __builtin_amdgcn_exp2f((fmaxf(l[i], -INFINITY) - top) * 1.44269504f);
+    for (int i = 0; i < V; ++i) sum += s[i];
     return token_sum<LANES>(sum);
 }
 
@@ -261,7 +251,10 @@ __global__ __launch_bounds__(64) void moe_route(const void* __restrict__ logits,
     P m = largest<LANES>(p[0]), chosen = P::none();
     const float top = m.logit();
     float total = 1.0f;
-    if (!sigmoid && !normalize) total = sum_scores<LANES, V>(l, top);
+    if (!sigmoid && !normalize) {
+        float s[V];
+        total = scores<LANES, V>(l, top, s);
+    }
     for (int j = 0;;) {
         if (lane == j) chosen = m;
         if (++j == k) break;
