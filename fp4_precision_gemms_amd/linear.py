@@ -32,9 +32,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (AXIS_ROWS, FMT_MXFP4, HAD_DET, HAD_NONE, OUT_BF16, RTN, fp4_gemm_grouped,
+from . import (AXIS_ROWS, FMT_MXFP4, HAD_DET, HAD_NONE, OUT_BF16, RTN, code_shape, fp4_gemm_grouped,
                fp4_gemm_grouped_wgrad, fp4_gemm_mx, fp4_hadamard_quantize, fp4_hadamard_quantize_dual,
-               fp4_quantize_experts, fp4_quantize_grouped_dual, fp4_rmsnorm_backward, fp4_rmsnorm_quantize)
+               fp4_quantize_experts, fp4_quantize_grouped_dual, fp4_rmsnorm_backward, fp4_rmsnorm_quantize, scale_shape)
 
 _SR_COLS = 0x9E3779B97F4A7C15      # tells the SR stream of the Dgrad operand from the Wgrad one's
 
@@ -152,8 +152,21 @@ class MXFP4NormLinear(torch.nn.Module):
 def quantize_experts(w: torch.Tensor):
     """Both operands of each of the experts' weights w [E, N, K] (bf16, N and K
     multiples of 32), as fp4_gemm_grouped takes them: (wtq, wts) for Dgrad,
-    (wq, ws) for the forward product."""
-    return fp4_quantize_experts(w.contiguous())
+    (wq, ws) for the forward product.  Any number of experts of any size: what
+    one fp4_quantize_experts does not take goes in several calls."""
+    w = w.contiguous()
+    E, N, K = w.shape
+    whole = N < 2 ** 22 and K < 2 ** 24
+    if whole and 1 <= E <= 1024:
+        return fp4_quantize_experts(w)
+    shapes = (code_shape(K, N), scale_shape(K, N), code_shape(N, K), scale_shape(N, K))
+    out = tuple(torch.empty((E, *s), dtype=torch.uint8, device=w.device) for s in shapes)
+    for e in range(0, E, 1024 if whole else 1):
+        if whole:
+            fp4_quantize_experts(w[e:e + 1024], out=[t[e:e + 1024] for t in out])
+        else:
+            fp4_hadamard_quantize_dual(w[e], out=[t[e] for t in out])
+    return out
 
 
 class MXFP4GroupedLinearFunction(torch.autograd.Function):
