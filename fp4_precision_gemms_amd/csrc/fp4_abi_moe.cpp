@@ -38,6 +38,8 @@ static fp4_status check_rows(int64_t tokens, int64_t k, int64_t rows, int64_t co
     if (tokens <= 0 || k <= 0 || tokens > INT32_MAX / k || rows <= 0 || rows > INT32_MAX || cols <= 0 || cols % 32 ||
         cols >= kMaxContraction)
         return FP4_ERR_SHAPE;
+    // a token's choices are counted in 32 bits, 64 at a time
+    if (k > INT32_MAX - 64) return FP4_ERR_SHAPE;
     // workgroups are counted in 32 bits, of 512 pieces of 16 bytes at most
     if (tokens > UINT32_MAX / ((cols + 4095) / 4096)) return FP4_ERR_SHAPE;
     return FP4_OK;

@@ -554,8 +554,9 @@ size_t fp4_moe_sort_workspace_bytes(int64_t slots, int64_t experts);
  * 32], which go to out_scales.  The gradient of x is fp4_moe_combine of out's
  * without weights.  The rows of a call's slots are distinct (else one of their
  * tokens' is left, or parts of several).  out must not overlap x.
- * Requirements: cols % 32 == 0, cols < 2^24; T, k, rows > 0, T k < 2^31, rows <
- * 2^31; pointers 16-byte aligned (position 4, scales any).
+ * Requirements: cols % 32 == 0, cols < 2^24; T, k, rows > 0, T k < 2^31, k < 2^31 -
+ * 64, rows < 2^31, T ceil(cols / 4096) < 2^32; pointers 16-byte aligned (position
+ * 4, scales any).
  */
 fp4_status fp4_moe_gather(const void* x, const uint8_t* scales, const int32_t* position, int64_t tokens, int64_t k,
                           int64_t rows, int64_t cols, void* out, uint8_t* out_scales, void* stream);
