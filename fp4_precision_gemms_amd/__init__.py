@@ -246,6 +246,8 @@ def fp4_hadamard_quantize(x: torch.Tensor, axis: int = AXIS_COLS, had_n: int = 3
     """MXFP4 codes and E8M0 scales of bf16 x[rows, cols] (see include/fp4.h)."""
     _need(x, torch.bfloat16, "x")
     rows, cols = x.shape
+    if axis not in (AXIS_COLS, AXIS_ROWS):         # ctypes would pass its low bits, the shapes go by all of it
+        _check(4)
     cshape, sshape = mx_shapes(rows, cols, axis)
     if codes is None:
         codes = _empty(cshape, torch.uint8, x.device, stream)

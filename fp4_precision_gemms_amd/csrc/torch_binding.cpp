@@ -21,7 +21,8 @@ PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     arguments(n, 8);
     const at::Tensor& x = matrix(a[0], at::kBFloat16, "x");
-    const int64_t rows = x.size(0), cols = x.size(1), fmt = integer(a[4]);
+    const int64_t rows = x.size(0), cols = x.size(1);
+    const int fmt = option<int>(a[4]);
     const at::Tensor& w = need(a[1], at::kBFloat16, {cols}, x, "weight");
     const bool added = a[2] != Py_None;
     if (added) need(a[2], at::kBFloat16, x.sizes(), x, "residual");
@@ -165,8 +166,8 @@ PyObject* quantize_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     uint8_t* p[4] = {};                                // rows codes, rows scales, cols codes, cols scales
     for (int i = 0; i < m; ++i) p[axes == 1 ? i + 2 : i] = ptr<uint8_t>(out[i]);
-    check(fp4_quantize_grouped(ptr(x), ptr<int32_t>(off), E, rows, cols, (int)integer(a[3]),
-                               (fp4_hadamard)integer(a[4]), seed(a[5]), (fp4_rounding)integer(a[6]), seed(a[7]),
+    check(fp4_quantize_grouped(ptr(x), ptr<int32_t>(off), E, rows, cols, option<int>(a[3]),
+                               option<fp4_hadamard>(a[4]), seed(a[5]), option<fp4_rounding>(a[6]), seed(a[7]),
                                seed(a[8]), p[0], p[1], p[2], p[3], stream(a[10], x)));
     return axes == 3 ? tuple(out[0], out[1], out[2], out[3]) : tuple(out[0], out[1]);
     END_HANDLE_TH_ERRORS

@@ -115,10 +115,27 @@ inline std::vector<at::Tensor> empty_together(const at::Tensor& like,
 template <typename T = void>
 T* ptr(const at::Tensor& t) { return static_cast<T*>(t.data_ptr()); }
 
+inline void check(fp4_status s) {
+    if (s == FP4_OK) return;
+    PyObject* e = PyObject_CallFunction(fp4_error, "is", (int)s, fp4_status_string(s));
+    if (e) {
+        PyErr_SetObject(fp4_error, e);
+        Py_DECREF(e);
+    }
+    throw python_error();
+}
+
 inline int64_t integer(PyObject* o) {
     const long long v = PyLong_AsLongLong(o);
     if (v == -1 && PyErr_Occurred()) throw python_error();
     return v;
+}
+// an enumeration's value, or a size of a few bits; what is no int is none of them
+template <typename E>
+E option(PyObject* o) {
+    const int64_t v = integer(o);
+    if (v != (int)v) check(FP4_ERR_ENUM);
+    return static_cast<E>(v);
 }
 // seeds: the low 64 bits of any Python integer
 inline uint64_t seed(PyObject* o) {
@@ -130,16 +147,6 @@ inline uint64_t seed(PyObject* o) {
 inline void* stream(PyObject* o, const at::Tensor& like) {
     if (o == Py_None) return c10::hip::getCurrentHIPStream(like.device().index()).stream();
     return reinterpret_cast<void*>(static_cast<uintptr_t>(seed(o)));
-}
-
-inline void check(fp4_status s) {
-    if (s == FP4_OK) return;
-    PyObject* e = PyObject_CallFunction(fp4_error, "is", (int)s, fp4_status_string(s));
-    if (e) {
-        PyErr_SetObject(fp4_error, e);
-        Py_DECREF(e);
-    }
-    throw python_error();
 }
 
 inline void arguments(Py_ssize_t got, Py_ssize_t want) {

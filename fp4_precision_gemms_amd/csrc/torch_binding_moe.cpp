@@ -89,7 +89,7 @@ FP4_FUNCTION(moe_route) {
         ids = need(o[0], at::kInt, {T, k}, l, "ids");
         weights = need(o[1], at::kFloat, {T, k}, l, "weights");
     }
-    check(fp4_moe_route(ptr(l), dtype_of(l), T, E, k, (fp4_score)integer(a[2]), truth(a[3]), ptr<int32_t>(ids),
+    check(fp4_moe_route(ptr(l), dtype_of(l), T, E, k, option<fp4_score>(a[2]), truth(a[3]), ptr<int32_t>(ids),
                         ptr<float>(weights), stream(a[5], l)));
     return tuple(ids, weights);
     END_HANDLE_TH_ERRORS
@@ -107,7 +107,7 @@ FP4_FUNCTION(moe_route_backward) {
     const c10::DeviceGuard guard(l.device());
     const at::Tensor d = a[5] == Py_None ? empty({T, E}, l.scalar_type(), l) : need(a[5], l.scalar_type(), {T, E}, l, "out");
     check(fp4_moe_route_backward(ptr<float>(dw), ptr(l), dtype_of(l), ptr<int32_t>(ids), T, E, k,
-                                 (fp4_score)integer(a[3]), truth(a[4]), ptr(d), stream(a[6], l)));
+                                 option<fp4_score>(a[3]), truth(a[4]), ptr(d), stream(a[6], l)));
     return wrap(d);
     END_HANDLE_TH_ERRORS
 }
@@ -249,7 +249,7 @@ FP4_FUNCTION(glu) {
     } else {
         y = need(a[6], at::kBFloat16, ys, x, "out");
     }
-    check(fp4_glu(ptr(x), r.w(), r.o(), r.off(), r.experts, (fp4_act)integer(a[1]), rows, cols, ptr(y), FP4_FMT_MXFP8,
+    check(fp4_glu(ptr(x), r.w(), r.o(), r.off(), r.experts, option<fp4_act>(a[1]), rows, cols, ptr(y), FP4_FMT_MXFP8,
                   nullptr, nullptr, kept ? ptr<uint8_t>(xq) : nullptr, kept ? ptr<uint8_t>(xs) : nullptr, stream(a[7], x)));
     return kept ? tuple(y, xq, xs) : wrap(y);
     END_HANDLE_TH_ERRORS
@@ -260,7 +260,8 @@ FP4_FUNCTION(glu_quantize) {
     HANDLE_TH_ERRORS
     arguments(n, 8);
     const at::Tensor& x = gate_and_up(a[0]);
-    const int64_t rows = x.size(0), cols = x.size(1) / 2, fmt = integer(a[5]);
+    const int64_t rows = x.size(0), cols = x.size(1) / 2;
+    const int fmt = option<int>(a[5]);
     const RowArgs r = row_args(a[2], a[3], a[4], rows, x);
     const Shape cs = fmt == FP4_FMT_MXFP8 ? Shape{rows, cols} : code_shape(rows, cols);
     const Shape ss = fmt == FP4_FMT_MXFP8 ? Shape{rows, cols / 32} : scale_shape(rows, cols);
@@ -275,7 +276,7 @@ FP4_FUNCTION(glu_quantize) {
         codes = need(o[0], at::kByte, cs, x, "codes");
         scales = need(o[1], at::kByte, ss, x, "scales");
     }
-    check(fp4_glu(ptr(x), r.w(), r.o(), r.off(), r.experts, (fp4_act)integer(a[1]), rows, cols, nullptr, (fp4_format)fmt,
+    check(fp4_glu(ptr(x), r.w(), r.o(), r.off(), r.experts, option<fp4_act>(a[1]), rows, cols, nullptr, (fp4_format)fmt,
                   ptr<uint8_t>(codes), ptr<uint8_t>(scales), nullptr, nullptr, stream(a[7], x)));
     return tuple(codes, scales);
     END_HANDLE_TH_ERRORS
@@ -303,7 +304,7 @@ FP4_FUNCTION(glu_backward) {
         dx = need(a[7], at::kBFloat16, {rows, 2 * cols}, dy, "out");
     }
     check(fp4_glu_backward(ptr(dy), ptr<uint8_t>(xq), ptr<uint8_t>(xs), r.w(), r.o(), r.off(), r.experts,
-                           (fp4_act)integer(a[3]), rows, cols, ptr(dx), r.weights ? ptr<float>(dw) : nullptr,
+                           option<fp4_act>(a[3]), rows, cols, ptr(dx), r.weights ? ptr<float>(dw) : nullptr,
                            stream(a[8], dy)));
     return r.weights ? tuple(dx, dw) : wrap(dx);
     END_HANDLE_TH_ERRORS
