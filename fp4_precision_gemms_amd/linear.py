@@ -27,10 +27,14 @@ Captured into a HIP graph, a layer's forward and backward pass go into the same
 capture, after a warm-up on the capturing stream and with no eager graph of its
 parameters alive (torch's gradient accumulation would wait for the stream of
 that one).
+
+The gradients have none of their own: torch refuses a backward pass that reaches a
+layer's gradient (once_differentiable).
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (AXIS_ROWS, FMT_MXFP4, HAD_DET, HAD_NONE, OUT_BF16, RTN, code_shape, fp4_gemm_grouped,
                fp4_gemm_grouped_wgrad, fp4_gemm_mx, fp4_hadamard_quantize, fp4_hadamard_quantize_dual,
@@ -60,6 +64,7 @@ class MXFP4LinearFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         xtq, xts, wtq, wts = ctx.saved_tensors
         had, had_n, sign_seed, grad_rounding, sr_seed = ctx.cfg
@@ -116,6 +121,7 @@ class MXFP4NormLinearFunction(torch.autograd.Function):
         return y, h
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh):
         h, rstd, norm_weight, ntq, nts, wtq, wts = ctx.saved_tensors
         added, had, had_n, sign_seed, grad_rounding, sr_seed = ctx.cfg
@@ -187,6 +193,7 @@ class MXFP4GroupedLinearFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         offsets, xtq, xts, wtq, wts = ctx.saved_tensors
         rows, K, padded, had, had_n, sign_seed, grad_rounding, sr_seed = ctx.cfg

@@ -15,11 +15,12 @@ them, through the few-row products.
 
 Captured into a HIP graph, forward and backward pass go into the same capture,
 after a warm-up on the capturing stream and with no eager graph of its parameters
-alive, as for the layers of linear.py.
+alive, as for the layers of linear.py.  The gradients have none of their own, as there.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (ACT_SILU, HAD_DET, RTN, SCORE_SOFTMAX, fp4_gemm_grouped, fp4_gemm_grouped_wgrad, fp4_glu,
                fp4_glu_backward, fp4_glu_quantize, fp4_moe_combine, fp4_moe_gather, fp4_moe_route,
@@ -42,6 +43,7 @@ class RouteFunction(torch.autograd.Function):
         return ids, weights
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, _, dweights):
         logits, ids = ctx.saved_tensors
         return fp4_moe_route_backward(dweights.float().contiguous(), logits, ids, *ctx.cfg), None, None, None
@@ -71,6 +73,7 @@ class MXFP4MoEFunction(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         (weights, offsets, order, position, xtq, xts, w1tq, w1ts, kept, kept_scales, ytq, yts, w2tq,
          w2ts) = ctx.saved_tensors
