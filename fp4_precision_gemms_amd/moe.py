@@ -98,7 +98,8 @@ class MXFP4MoEFunction(torch.autograd.Function):
 class MXFP4MoE(torch.nn.Module):
     """`experts` experts of a gated activation, k of them a token: forward(x,
     logits) with x [T, in_features] (bf16) and the router's logits [T, experts]
-    (fp32 or bf16)."""
+    (fp32 or bf16).  T is at least 1: a batch without tokens is refused
+    (FP4_ERR_SHAPE), as a size of 0 is by every call."""
 
     def __init__(self, experts: int, k: int, in_features: int, inner: int, act: int = ACT_SILU,
                  score: int = SCORE_SOFTMAX, normalize: bool = True, had: int = HAD_DET, had_n: int = 32,
@@ -125,7 +126,7 @@ def moe_decode(codes: torch.Tensor, scales: torch.Tensor, logits: torch.Tensor, 
     fp4_rmsnorm_quantize writes them) to bf16 [T, C].  w1q, w1s / w2q, w2s: the
     experts' weights [E, 2 I, C] and [E, C, I] as fp4_gemm_grouped takes them (the
     last two of quantize_experts).  The weights go to the second product's rows
-    here, in binary32."""
+    here, in binary32.  At least one token, as for the layer."""
     ids, weights = fp4_moe_route(logits, k, score, normalize)
     offsets, _, position = fp4_moe_sort(ids, w1q.shape[0])
     aq, as_ = fp4_moe_gather(codes, position, scales)
