@@ -330,7 +330,8 @@ __global__ __launch_bounds__(64) void moe_route_back(const float* __restrict__ d
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         v[i] = at[expert_at<LANES, V>(i)];
-        if (dense) v[i] = s[i] * r * (v[i] - inner);
+        // zero for what is no choice, also where a gradient of the weights is no number
+        if (dense) v[i] = s[i] != 0.0f ? s[i] * r * (v[i] - inner) : 0.0f;
     }
     if (V >= 4 && whole) {
 #pragma unroll

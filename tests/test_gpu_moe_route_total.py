@@ -59,3 +59,25 @@ def test_a_token_beside_one_with_infinite_logits(E, k, score, normalize):
         share = 1.0 / (k if normalize else E)            # all logits infinite: equal parts
         assert ((b[1][4] - share).abs() <= 2.0 ** -22 * share).all()
         assert b[1][0].tolist() == [1.0] + [0.0] * (k - 1)
+
+
+@pytest.mark.parametrize("E,k", SIZES)
+def test_masked_logits_get_zero_from_gradients_that_are_no_numbers(E, k):
+    """Zero for every logit that is no choice, as documented, whatever the weights'
+    gradient."""
+    need_gpu()
+    say("route masked", E, k)
+    torch.manual_seed(E + 2)
+    T, inf = 37, float("inf")
+    l = torch.randn(T, E, device="cuda")
+    masked = torch.rand(T, E, device="cuda") < 0.4
+    l = l.masked_fill(masked, -inf).masked_fill(masked & (torch.rand(T, E, device="cuda") < 0.3), float("nan"))
+    for score, normalize in ((F.SCORE_SOFTMAX, False), (F.SCORE_SOFTMAX, True), (F.SCORE_SIGMOID, True), (F.SCORE_SIGMOID, False)):
+        ids, w = F.fp4_moe_route(l, k, score, normalize)
+        g = torch.randn(T, k, device="cuda")
+        g[1::3, 0], g[2::3, 0] = inf, float("nan")
+        d = F.fp4_moe_route_backward(g, l, ids, score, normalize)
+        assert not d[masked].any()                       # a NaN counts as one here
+        live = (ids[:, 0] >= 0)
+        live[0::3] = False
+        assert not torch.isfinite(d[live].gather(1, ids[live][:, :1].long())).any() or score == F.SCORE_SIGMOID
