@@ -27,9 +27,11 @@
 // is one maximum over the lanes (DPP), and the lane that held it moves up its next
 // one.  No ties are left to look for.  (With a wave a token, a ballot for the lane
 // that holds the maximum and its other experts looked through again for each choice,
-// 16384 tokens of 256 experts, 8 choices took 15.0 us, of 64, 6 choices 8.8; now 8.2
-// and 4.7, of which the logits' bytes are 3.4 and 0.8, the launch 2.3 and the rest
-// vector instructions; back 12.6 and 6.5, now 7.6 and 4.0.)
+// 16384 tokens of 256 experts, 8 choices took 15.0 us, of 64, 6 choices 8.8; now 8.6
+// and 4.5 with the logits in a cache, 10.0 and 4.9 without; back 12.6 and 6.5, now 7.8
+// and 3.8, 9.9 and 4.2 without.)  Forward bound by the vector instructions: 1006 a wave
+// of four tokens, whose 4 cycles each are 83 % of the compute units' busy ones (of 1024
+// experts 1316 a wave, also 83 %); backward, 418, by the bytes.
 #include "exp_device.hpp"
 #include "fp4_device.hpp"
 #include "fp4_launch.hpp"
@@ -129,7 +131,7 @@ __device__ __forceinline__ float token_sum(float v) {
     else return row_sum(v);
 }
 
-// Descending, by odd-even merges.
+// Descending, by Batcher's odd-even merges.
 template <int V, typename P>
 __device__ __forceinline__ void sort_lane(P* p) {
 #pragma unroll
@@ -375,6 +377,10 @@ hipError_t launch_v(const float* dweights, const void* logits, int bf16, int64_t
 
 hipError_t launch_any(const float* dweights, const void* logits, int bf16, int64_t tokens, int64_t E, int64_t k,
                       int sigmoid, int normalize, int* ids, float* weights, void* dlogits, hipStream_t st) {
+    // a wave a token takes what 16 lanes cannot, which is slower wherever they can (the
+    // comment at the top); of the 16 that a lane sorts it keeps no more than can be
+    // chosen from it (16384 x 256, 8 choices, softmax over all: 9.8 us with 8 kept,
+    // 12.2 with 16)
     auto* run = E <= 64 ? &launch_v<64, 1, 64> : E <= 128 ? &launch_v<64, 2, 64> : E <= 256 ? &launch_v<64, 4, 64>
                 : E <= 512 ? &launch_v<64, 8, 64> : &launch_v<64, 16, 64>;
     if (k <= 16 && E <= 256)

@@ -1,7 +1,8 @@
 // wave.hpp -- reductions over a 64-lane wave by data-parallel moves (DPP), the
 // result in every lane by way of a scalar register: no LDS traffic and no
 // latency of one (a sum of a wave takes 7 vector instructions; the same by __shfl_xor
-// 6 trips through the LDS pipe).
+// 6 trips through the LDS pipe).  The norm keeps a sum of its own by __shfl_xor, also
+// of binary64 numbers, whose order its results go by.
 #pragma once
 
 #include <hip/hip_runtime.h>
