@@ -211,9 +211,9 @@ __device__ __forceinline__ void load_logits(const void* logits, int64_t t, int E
 
 // The scores of a lane's logits over the largest one, 0 for what is no choice, and
 // their sum over the token's lanes: the forward pass divides by it and the backward
-// pass by the same bits.  The exponential is the corrected one: equal logits err the
-// same way, so that hundreds of them would leave the plain one's error, which grows
-// with the argument, whole in the sum.
+// pass by the same bits.  Equal logits err the same way, so the exponential is one
+// whose error does not grow with its argument: hundreds of them would leave it whole
+// in the sum.
 template <int LANES, int V>
 __device__ __forceinline__ float scores(const float* l, float top, float* s) {
 #pragma unroll

@@ -512,7 +512,6 @@ typedef enum {
  * also where every score of a token is below binary32).  A logit that is
  * -infinity or NaN is no choice; where nothing else is left the id is -1 and the
  * weight 0.  An infinite largest logit counts as the limit: equal logits share.
- * Computed in binary32, an exponential below 2^-126 as 0.
  * Requirements: 1 <= E <= 1024, 1 <= k <= min(E, 64); normalize 0 or 1 (else
  * FP4_ERR_ENUM); pointers aligned to their elements.
  */
@@ -612,10 +611,10 @@ typedef enum {
 /*
  * fp4_glu -- the gated activation between two products: from x bf16 [rows, 2
  * cols], gate and up side by side, y[r, c] = w_r act(x[r, c]) x[r, cols + c],
- * computed in binary32 (exp(-|s|) below 2^-126 as 0) and rounded once, to bf16 [rows,
- * cols] (y_bf16, NULL if not wanted) and / or to an operand of `rows` rows of `cols`
- * elements in `fmt` (codes and scales as fp4_rmsnorm_quantize writes them, both NULL
- * if not wanted).  xq [rows, 2 cols], xs [rows, 2 cols / 32]: the checkpoint for the
+ * computed in binary32 and rounded once, to bf16 [rows, cols] (y_bf16, NULL if not
+ * wanted) and / or to an operand of `rows` rows of `cols` elements in `fmt`
+ * (codes and scales as fp4_rmsnorm_quantize writes them, both NULL if not
+ * wanted).  xq [rows, 2 cols], xs [rows, 2 cols / 32]: the checkpoint for the
  * backward pass, x in MXFP8 (both NULL if not wanted).
  * weights (fp32 [rows], NULL: all 1) and order (int32 [rows], NULL: row r's weight
  * is weights[r]): row r's weight is weights[order[r]], 0 where order[r] is outside

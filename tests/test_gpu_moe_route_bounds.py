@@ -50,8 +50,8 @@ def spread(rel, part, live):
 
 def over_top(l, top):
     """exp(l - top) and the relative error of the kernel's: the difference rounded
-    once (a u in the exponent), the exponential a step (2 u), its correction and the
-    product (2 u), what the correction leaves out (1 u)."""
+    once (a u in the exponent), the exponential a step (2 u), its argument's roundings
+    (3 u)."""
     with np.errstate(all="ignore"):
         a = np.where(l > -np.inf, np.minimum(top - l, 104.0), 104.0)
         return np.where(l > -np.inf, np.exp(-(top - l)), 0.0), (a + 5) * U
