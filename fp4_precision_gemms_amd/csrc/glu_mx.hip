@@ -234,6 +234,9 @@ hipError_t launch_glu_back(const void* dy, const uint8_t* xq, const uint8_t* xs,
     // 321 with 512, 299 with 1024; 96 x 14336 8.2, 6.7 and 6.0; but 16384 x 4096 87, 86
     // and 103); a wave where it is one or two pieces of it, and where 256 threads would
     // idle for the most part, if there are rows enough (12000 x 1408 27.1 and 24.9 us).
+    // A wave and 256 threads for up to 1024 columns: 12000 x 512 13.5 and 17.3 us, 12000 x
+    // 1024 22.8 and 25.0; with fewer rows they are even, or the wave loses: 1999 x 512 4.0
+    // and 4.1, 1999 x 736 5.9 and 5.7, 96 x 512 2.6 and 2.8, 96 x 736 3.4 and 2.8.
     auto* const run = cols >= 8192                                       ? &launch_back<1024>
                       : cols <= 1024 || (cols < 2048 && rows >= 1024) ? &launch_back<64>
                                                                          : &launch_back<256>;

@@ -27,11 +27,11 @@
 // is one maximum over the lanes (DPP), and the lane that held it moves up its next
 // one.  No ties are left to look for.  (With a wave a token, a ballot for the lane
 // that holds the maximum and its other experts looked through again for each choice,
-// 16384 tokens of 256 experts, 8 choices took 15.0 us, of 64, 6 choices 8.8; now 8.6
-// and 4.5 with the logits in a cache, 10.0 and 4.9 without; back 12.6 and 6.5, now 7.8
-// and 3.8, 9.9 and 4.2 without.)  Forward bound by the vector instructions: 1006 a wave
-// of four tokens, whose 4 cycles each are 83 % of the compute units' busy ones (of 1024
-// experts 1316 a wave, also 83 %); backward, 418, by the bytes.
+// 16384 tokens of 256 experts, 8 choices took 15.0 us, of 64, 6 choices 8.8; now 8.4
+// and 4.5 with the logits in a cache, 10.0 and 4.9 without; back 12.6 and 6.5, now 7.6
+// and 3.8, 9.8 and 4.2 without.)  Forward bound by the vector instructions: 1007 a wave
+// of four tokens, whose 4 cycles each are 82 % of the compute units' busy ones (of 1024
+// experts 1317 a wave, 84 %); backward, 419, by the bytes.
 #include "exp_device.hpp"
 #include "fp4_device.hpp"
 #include "fp4_launch.hpp"
@@ -183,7 +183,8 @@ __device__ __forceinline__ int expert_at(int i) {
 }
 
 // The logits of a lane's experts, -infinity past the last one; `whole`: rows of E % 4
-// == 0 elements at aligned addresses, four in one load.
+// == 0 elements at aligned addresses, four in one load (16384 x 256, softmax over all:
+// fp32 10.1 us and 10.5 one by one, bf16 7.3 and 10.6; back 10.7 and 15.4, 8.0 and 12.9).
 template <int LANES, int V, bool BF16>
 __device__ __forceinline__ void load_logits(const void* logits, int64_t t, int E, bool whole, float* l) {
     if (V >= 4 && whole) {

@@ -209,6 +209,8 @@ hipError_t launch_moe_sort(const int* ids, int64_t slots, int64_t experts, int* 
                            int* counts, hipStream_t st) {
     const int64_t n = moe_sort_workgroups(slots);
     if (n == 1) {
+        // as few slots a thread as take them: 96 slots 2.7 us with one and 4.2 with four,
+        // 1800 3.6 with two and 4.6
         auto* const place = slots <= kThreads       ? &launch_place<1, true>
                             : slots <= 2 * kThreads ? &launch_place<2, true>
                                                     : &launch_place<4, true>;
